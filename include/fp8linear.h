@@ -83,7 +83,8 @@ typedef enum {
   FP8_DT_F16 = 1,
   FP8_DT_BF16 = 2,
   FP8_DT_E4M3 = 3,
-  FP8_DT_E5M2 = 4
+  FP8_DT_E5M2 = 4,
+  FP8_DT_I8 = 5 /* 8-bit integers with one scale per row (fp8_i8_* only) */
 } fp8_dtype_t;
 
 /*
@@ -450,6 +451,112 @@ int fp8_gemm(int64_t batch, int64_t M, int64_t N, int64_t K, fp8_operand_t a, in
 int fp8_gemm_fp8out(int64_t M, int64_t N, int64_t K, fp8_operand_t a, fp8_operand_t b,
                     fp8_operand_t bias, int32_t fmt_out, fp8_ring_t* ring_out, uint8_t* c8,
                     float* scale_used, float* amax_out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Linear layers over ragged groups of rows: a mixture's experts.
+ *
+ * The rows of X [T, K] are sorted by expert; offsets is a DEVICE array of
+ * E + 1 int32, and expert e has the rows [offsets[e], offsets[e+1]) (none:
+ * equal offsets).  offsets[0] is 0 or the first row in use, offsets[E] the
+ * end of the last group: rows outside [offsets[0], offsets[E]) belong to no
+ * expert, and the calls neither read them (but see the quantize of rows
+ * before offsets[0] below) nor write the outputs' rows there.  The host
+ * never reads offsets.  They must not decrease and must stay within [0, T];
+ * where they do not, the results of the groups concerned are unspecified
+ * and no memory outside the operands is touched.
+ * Weights are W [E, N, K], one matrix per expert.
+ * Limits: T < 2^31, 1 <= E <= 65535 (FP8_ERR_SHAPE otherwise).
+ * Results do not depend on scheduling: the same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of the workspace that fp8_grouped_linear_bwd needs for db: fp32
+ * column sums of 32-row chunks, N per chunk; at most min(E, T) chunks more
+ * than T / 32.  0 for negative sizes. */
+size_t fp8_grouped_db_workspace_bytes(int64_t T, int32_t E, int64_t N);
+
+/*
+ * Forward: Y[t] = X8[t] W8[e]^T / (sx sw[e]) (+ bias[e]) for the rows t of
+ * expert e, one rounding to bf16.
+ *   x, w     as in fp8_linear_fwd: high precision (quantized here, per tensor,
+ *            with ring_x / ring_w or dynamically; W over all experts) or fp8
+ *            codes of the call's format.  A high-precision x is quantized over
+ *            its rows [0, offsets[E]).
+ *   w_scales number of scales of pre-quantized w: 1, or E (one per expert).
+ *            Ignored for high-precision w.
+ *   bias     bf16 [E, N] or NULL.
+ *   y        bf16 [T, N].
+ *   x8_out, w8_out, s*_used, amax_*  as in fp8_linear_fwd; for pre-quantized w
+ *            sw_used receives its w_scales scales.
+ */
+int fp8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
+                           fp8_operand_t x, fp8_operand_t w, int32_t w_scales, const void* bias,
+                           int32_t fmt, fp8_ring_t* ring_x, fp8_ring_t* ring_w, void* y,
+                           uint8_t* x8_out, uint8_t* w8_out, float* sx_used, float* sw_used,
+                           float* amax_x, float* amax_w, hipStream_t stream);
+
+/*
+ * Backward, from one quantize of G [T, N]:
+ *   dX[t]  = G8[t] W8[e] / (sg sw[e])              bf16 [T, K]
+ *   dW[e]  = sum over e's rows of G8[t]^T X8[t] / (sg sx)   bf16 [E, N, K]
+ *   db[e]  = sum over e's rows of G[t]             bf16 [E, N]
+ * dx, dw and db may each be NULL (not computed; w8 is needed for dx only, x8
+ * for dw only).  An expert without rows gets zeros in dW and db.  db sums G
+ * as given: a high-precision g itself, or dec(g8) / sg.
+ *   g        high precision (quantized here with ring_g, or dynamically, over
+ *            rows [0, offsets[E])) or fp8 codes of fmt_g.
+ *   db_ws    workspace of fp8_grouped_db_workspace_bytes(T, E, N); required
+ *            for db when T > 0.  Its contents need not survive the call.
+ *   w_scales number of scales of w8: 1 or E.
+ */
+int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
+                           fp8_operand_t g, int32_t fmt_g, fp8_ring_t* ring_g, fp8_operand_t x8,
+                           fp8_operand_t w8, int32_t w_scales, void* dx, void* dw, void* db,
+                           float* db_ws, uint8_t* g8_out, float* sg_used, float* amax_g,
+                           hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Linear layers in 8-bit integers with one scale per token and one per
+ * output channel (serving).  Codes are int8, scales are quantization
+ * multipliers (q ~ x s), as everywhere in this library.  The integer sums
+ * are exact: K <= 131071 keeps them inside int32 (FP8_ERR_SHAPE beyond).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * q[r, k] = rint(fl32(x[r, k] s[r])), ties to even, with
+ * s[r] = fl32(127 / max_k |x[r, k]|); x [rows, cols] F32, F16 or BF16.
+ * A row of zeros (or so small that the quotient overflows) gets s = 1 and
+ * zeros; a row holding a NaN or an infinity gets s = NaN and zeros.
+ * Quantizes activations by token and, applied to W [N, K], weights by
+ * output channel.
+ */
+int fp8_i8_quantize_rows(const void* x, int32_t in_dtype, int64_t rows, int64_t cols, int8_t* q,
+                         float* scale, hipStream_t stream);
+
+/*
+ * Y[m, n] = (sum_k xq[m, k] w[n, k]) (1/sx[m]) (1/sw[n]) (+ bias[n]), the sum
+ * in int32, the rest in fp32, one rounding to out_dtype.
+ *   x         F32 / F16 / BF16 [M, K]: quantized by token here, codes to
+ *             x8_out [M, K] and scales to sx_out [M] (both required); or
+ *             FP8_DT_I8 codes with scale [M] (x8_out, sx_out unused).
+ *   w         FP8_DT_I8 codes [N, K] with scale [N].
+ *   bias      [N] of out_dtype, or NULL.
+ *   y         [M, N], out_dtype FP8_DT_BF16 or FP8_DT_F16.
+ * A row of x with s = NaN gives a row of NaN.
+ */
+int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_operand_t w,
+                      const void* bias, int32_t out_dtype, void* y, int8_t* x8_out, float* sx_out,
+                      hipStream_t stream);
+
+/*
+ * The same over ragged groups of rows (offsets, T, E as in
+ * fp8_grouped_linear_fwd): w [E, N, K] with scale [E, N], bias [E, N].  Rows
+ * behind offsets[E] are not quantized and their rows of x8_out, sx_out and y
+ * are left as they were.
+ */
+int fp8_i8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
+                              fp8_operand_t x, fp8_operand_t w, const void* bias,
+                              int32_t out_dtype, void* y, int8_t* x8_out, float* sx_out,
+                              hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,8 @@ Python; without the built library every call raises.
 
 Conventions: fmt / dtype values are the C enums below; pre-quantized
 operands are passed as ``Quantized(codes_uint8, fmt, scale_f32)``; rings are
-``ScaleRing`` objects that own their device buffer and the C struct.
+``ScaleRing`` objects that own their device buffer and the C struct; 8-bit
+integer operands are ``QuantizedRows(codes_int8, scales_f32)``.
 """
 
 from __future__ import annotations
@@ -21,7 +22,7 @@ import torch
 from ._build import LIB_PATH
 
 FP8_E4M3, FP8_E5M2 = 0, 1
-FP8_DT_F32, FP8_DT_F16, FP8_DT_BF16, FP8_DT_E4M3, FP8_DT_E5M2 = 0, 1, 2, 3, 4
+FP8_DT_F32, FP8_DT_F16, FP8_DT_BF16, FP8_DT_E4M3, FP8_DT_E5M2, FP8_DT_I8 = 0, 1, 2, 3, 4, 5
 FP8_OK, FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_DTYPE, FP8_ERR_RING, FP8_ERR_HIP = range(6)
 FP8_K_CONTIG, FP8_K_STRIDED = 0, 1
 FP8_QUANT_ROWS, FP8_QUANT_TRANSPOSED, FP8_QUANT_DUAL = 0, 1, 2
@@ -33,7 +34,9 @@ C_SYMBOLS = (
     "fp8_abi_version", "fp8_source_hash", "fp8_status_str", "fp8_ring_bytes", "fp8_ring_init", "fp8_quantize",
     "fp8_quantize_pair", "fp8_linear_fwd", "fp8_linear_bwd_dx", "fp8_db_workspace_bytes",
     "fp8_linear_bwd_dw", "fp8_gemm", "fp8_quantize_2d", "fp8_gemm_fp8out", "fp8_linear_bwd",
-    "fp8_linear_bwd_dw_noalloc",
+    "fp8_linear_bwd_dw_noalloc", "fp8_grouped_db_workspace_bytes", "fp8_grouped_linear_fwd",
+    "fp8_grouped_linear_bwd", "fp8_i8_quantize_rows", "fp8_i8_linear_fwd",
+    "fp8_i8_grouped_linear_fwd",
 )
 
 
@@ -88,6 +91,19 @@ def lib() -> ctypes.CDLL:
         L.fp8_gemm.argtypes = [i64, i64, i64, i64, op, i32, i64, i64, op, i32, i64, i64, op, vp,
                                i64, i64, vp]
         L.fp8_gemm_fp8out.argtypes = [i64, i64, i64, op, op, op, i32, rp, vp, vp, vp, vp]
+        L.fp8_grouped_db_workspace_bytes.restype = sz
+        L.fp8_grouped_db_workspace_bytes.argtypes = [i64, i32, i64]
+        L.fp8_grouped_linear_fwd.argtypes = [i64, i32, i64, i64, vp, op, op, i32, vp, i32, rp, rp,
+                                             vp, vp, vp, vp, vp, vp, vp, vp]
+        L.fp8_grouped_linear_bwd.argtypes = [i64, i32, i64, i64, vp, op, i32, rp, op, op, i32, vp,
+                                             vp, vp, vp, vp, vp, vp, vp]
+        L.fp8_i8_quantize_rows.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+        L.fp8_i8_linear_fwd.argtypes = [i64, i64, i64, op, op, vp, i32, vp, vp, vp, vp]
+        L.fp8_i8_grouped_linear_fwd.argtypes = [i64, i32, i64, i64, vp, op, op, vp, i32, vp, vp, vp,
+                                                vp]
+        for name in ("fp8_grouped_linear_fwd", "fp8_grouped_linear_bwd", "fp8_i8_quantize_rows",
+                     "fp8_i8_linear_fwd", "fp8_i8_grouped_linear_fwd"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("fp8_ring_init", "fp8_quantize", "fp8_quantize_pair", "fp8_quantize_2d",
                      "fp8_linear_fwd", "fp8_gemm", "fp8_linear_bwd_dx",
                      "fp8_linear_bwd_dw", "fp8_gemm_fp8out", "fp8_linear_bwd",
@@ -115,6 +131,10 @@ def fp8_ring_bytes(hist_len: int) -> int:
 
 def fp8_db_workspace_bytes(M: int, N: int) -> int:
     return lib().fp8_db_workspace_bytes(M, N)
+
+
+def fp8_grouped_db_workspace_bytes(T: int, E: int, N: int) -> int:
+    return lib().fp8_grouped_db_workspace_bytes(T, E, N)
 
 
 # ---------------------------------------------------------------- marshalling
@@ -565,3 +585,276 @@ def bind_fp8_gemm_fp8out(a, b, c8, fmt_out, ring_out, scale_used, amax_out=None,
                          stream=None):
     return _bind("fp8_gemm_fp8out", _gemm_fp8out_args(a, b, c8, fmt_out, ring_out, scale_used,
                                                       amax_out, bias, stream))
+
+
+# ---------------------------------------------------------------- ragged groups, 8-bit integers
+# These calls also serve single tokens, where the call itself is what takes
+# time: their checks take one pass over each tensor, and sizes and pointers
+# go to the C call as they are.  Every tensor must be on one GPU; the call
+# runs with that GPU current, on its current stream unless one is given.
+
+@dataclass
+class QuantizedRows:
+    """8-bit integer operand: int8 codes [.., rows, k] and one device float32
+    scale for each row [.., rows] (a quantization multiplier: q ~ x s)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+
+_F32, _U8, _I8, _I32, _BF16 = ((torch.float32,), (torch.uint8,), (torch.int8,), (torch.int32,),
+                               (torch.bfloat16,))
+
+
+def _gpu_of(t, what):
+    t = t.codes if isinstance(t, (Quantized, QuantizedRows)) else t
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
+    return t.device
+
+
+def _arg(t, what, dtypes, shape, dev, optional=False, numel=None):
+    """Data pointer of a checked tensor argument (None when absent)."""
+    if t is None and optional:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (numel is None or t.numel() >= numel)):
+        _need(t, what, dtypes, shape=shape, numel=numel, optional=False)
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{what}: must be a GPU tensor on {dev} (got {t.device})")
+    return t.data_ptr()
+
+
+def _shape_of(t, dims, what):
+    d = t.codes if isinstance(t, (Quantized, QuantizedRows)) else t
+    if not isinstance(d, torch.Tensor) or d.dim() != dims:
+        raise ValueError(f"{what}: expected a {dims}-D tensor")
+    return d.shape
+
+
+def _arg_operand(t, what, shape, dev, hp_ok=True, scales=(1,)):
+    """Checked operand: a high-precision tensor, or Quantized with one of the
+    given numbers of scales.  Returns (C operand, number of scales)."""
+    if isinstance(t, Quantized):
+        if t.fmt not in _FMT_DT:
+            raise ValueError(f"{what}: unknown fp8 format {t.fmt}")
+        sp = _arg(t.scale, f"{what}.scale", _F32, None, dev)
+        n = t.scale.numel()
+        if n not in scales:
+            raise ValueError(f"{what}.scale: {n} scales, expected {' or '.join(map(str, scales))}")
+        return _Operand(_arg(t.codes, f"{what}.codes", _U8, shape, dev), _FMT_DT[t.fmt], sp), n
+    if not hp_ok:
+        raise TypeError(f"{what}: expected a Quantized operand")
+    return _Operand(_arg(t, what, _HP, shape, dev), _TORCH_DT[t.dtype], None), 1
+
+
+def _arg_stream(stream, dev):
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
+    return stream.cuda_stream
+
+
+def _run(name, args, dev):
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != FP8_OK:
+        raise Fp8Error(st, name)
+
+
+def _bind_run(name, args, dev):
+    return lambda: _run(name, args, dev)
+
+
+_NO_OPERAND = _Operand(None, FP8_DT_BF16, None)
+
+
+def _grouped_fwd_args(x, w, bias, offsets, fmt, y, ring_x, ring_w, x8_out, w8_out, sx_used,
+                      sw_used, amax_x, amax_w, stream):
+    T, K = _shape_of(x, 2, "x")
+    E, N, Kw = _shape_of(w, 3, "w")
+    dev = _gpu_of(x, "x")
+    ox, _ = _arg_operand(x, "x", (T, K), dev)
+    ow, ns = _arg_operand(w, "w", (E, N, K), dev, scales=(1, E))
+    args = (T, E, N, K, _arg(offsets, "offsets", _I32, (E + 1,), dev), ox, ow, ns,
+            _arg(bias, "bias", _BF16, (E, N), dev, True), fmt, _ring(ring_x), _ring(ring_w),
+            _arg(y, "y", _BF16, (T, N), dev), _arg(x8_out, "x8_out", _U8, (T, K), dev, True),
+            _arg(w8_out, "w8_out", _U8, (E, N, K), dev, True),
+            _arg(sx_used, "sx_used", _F32, None, dev, True, numel=1),
+            _arg(sw_used, "sw_used", _F32, None, dev, True, numel=ns),
+            _arg(amax_x, "amax_x", _F32, None, dev, True, numel=1),
+            _arg(amax_w, "amax_w", _F32, None, dev, True, numel=1), _arg_stream(stream, dev))
+    return args, dev
+
+
+def fp8_grouped_linear_fwd(x, w, bias, offsets, fmt, y, ring_x=None, ring_w=None, x8_out=None,
+                           w8_out=None, sx_used=None, sw_used=None, amax_x=None, amax_w=None,
+                           stream=None):
+    """y[t] = x[t] w[e]^T (+ bias[e]) for the rows t of expert e, in FP8.
+    x: [T, K] tensor or Quantized, rows sorted by expert; w: [E, N, K] tensor
+    or Quantized with 1 or E scales; bias: bf16 [E, N] or None; offsets: int32
+    [E + 1] on the GPU, expert e has rows offsets[e] .. offsets[e+1] - 1;
+    y: bf16 [T, N], written in the experts' rows only."""
+    _run("fp8_grouped_linear_fwd", *_grouped_fwd_args(x, w, bias, offsets, fmt, y, ring_x, ring_w,
+                                                      x8_out, w8_out, sx_used, sw_used, amax_x,
+                                                      amax_w, stream))
+
+
+def bind_fp8_grouped_linear_fwd(x, w, bias, offsets, fmt, y, ring_x=None, ring_w=None, x8_out=None,
+                                w8_out=None, sx_used=None, sw_used=None, amax_x=None, amax_w=None,
+                                stream=None):
+    return _bind_run("fp8_grouped_linear_fwd", *_grouped_fwd_args(
+        x, w, bias, offsets, fmt, y, ring_x, ring_w, x8_out, w8_out, sx_used, sw_used, amax_x,
+        amax_w, stream))
+
+
+def _grouped_bwd_args(g, fmt_g, offsets, x8, w8, dx, dw, db, db_ws, ring_g, g8_out, sg_used,
+                      amax_g, stream):
+    T, N = _shape_of(g, 2, "g")
+    dev = _gpu_of(g, "g")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets: expected an int32 tensor of E + 1 elements")
+    E = offsets.shape[0] - 1
+    if dx is not None:
+        K = _shape_of(dx, 2, "dx")[1]
+    elif dw is not None:
+        K = _shape_of(dw, 3, "dw")[2]
+    else:
+        K = 0
+    og, _ = _arg_operand(g, "g", (T, N), dev)
+    ox, ow, ns = _NO_OPERAND, _NO_OPERAND, 1
+    if dw is not None:
+        ox, _ = _arg_operand(x8, "x8", (T, K), dev, hp_ok=False)
+    if dx is not None:
+        ow, ns = _arg_operand(w8, "w8", (E, N, K), dev, hp_ok=False, scales=(1, E))
+    wsp = None
+    if db is not None and db_ws is not None:
+        if not isinstance(db_ws, torch.Tensor) or not db_ws.is_contiguous():
+            raise ValueError("db_ws: expected a contiguous tensor")
+        if db_ws.device != dev:
+            raise ValueError(f"db_ws: must be a GPU tensor on {dev} (got {db_ws.device})")
+        need = fp8_grouped_db_workspace_bytes(T, E, N)
+        if db_ws.numel() * db_ws.element_size() < need:
+            raise ValueError(f"db_ws: {db_ws.numel() * db_ws.element_size()} bytes, "
+                             f"at least {need} needed")
+        wsp = db_ws.data_ptr()
+        if wsp % 4:
+            raise ValueError("db_ws: must be 4-byte aligned")
+    args = (T, E, N, K, _arg(offsets, "offsets", _I32, (E + 1,), dev), og, fmt_g, _ring(ring_g),
+            ox, ow, ns, _arg(dx, "dx", _BF16, (T, K), dev, True),
+            _arg(dw, "dw", _BF16, (E, N, K), dev, True), _arg(db, "db", _BF16, (E, N), dev, True),
+            wsp, _arg(g8_out, "g8_out", _U8, (T, N), dev, True),
+            _arg(sg_used, "sg_used", _F32, None, dev, True, numel=1),
+            _arg(amax_g, "amax_g", _F32, None, dev, True, numel=1), _arg_stream(stream, dev))
+    return args, dev
+
+
+def fp8_grouped_linear_bwd(g, fmt_g, offsets, x8, w8, dx=None, dw=None, db=None, db_ws=None,
+                           ring_g=None, g8_out=None, sg_used=None, amax_g=None, stream=None):
+    """The gradients of fp8_grouped_linear_fwd that are given a buffer: dx bf16
+    [T, K] (experts' rows only), dw bf16 [E, N, K], db bf16 [E, N] (db_ws: any
+    tensor of fp8_grouped_db_workspace_bytes bytes).  g: [T, N] tensor
+    (quantized here) or Quantized; x8, w8: the forward's Quantized operands."""
+    _run("fp8_grouped_linear_bwd", *_grouped_bwd_args(g, fmt_g, offsets, x8, w8, dx, dw, db, db_ws,
+                                                      ring_g, g8_out, sg_used, amax_g, stream))
+
+
+def bind_fp8_grouped_linear_bwd(g, fmt_g, offsets, x8, w8, dx=None, dw=None, db=None, db_ws=None,
+                                ring_g=None, g8_out=None, sg_used=None, amax_g=None, stream=None):
+    return _bind_run("fp8_grouped_linear_bwd", *_grouped_bwd_args(
+        g, fmt_g, offsets, x8, w8, dx, dw, db, db_ws, ring_g, g8_out, sg_used, amax_g, stream))
+
+
+def _i8_quantize_args(x, q, scale, stream):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x: expected a tensor of at least one dimension")
+    dev, cols = x.device, x.shape[-1]
+    lead = x.shape[:-1]
+    rows = 1
+    for d in lead:
+        rows *= d
+    args = (_arg(x, "x", _HP, None, dev), _TORCH_DT[x.dtype], rows, cols,
+            _arg(q, "q", _I8, x.shape, dev), _arg(scale, "scale", _F32, lead, dev),
+            _arg_stream(stream, dev))
+    return args, dev
+
+
+def fp8_i8_quantize_rows(x, q, scale, stream=None):
+    """q = rint(x s) with s = 127 / max |x| of each row: x [.., k], q int8 of
+    x's shape, scale float32 [..]."""
+    _run("fp8_i8_quantize_rows", *_i8_quantize_args(x, q, scale, stream))
+
+
+def bind_fp8_i8_quantize_rows(x, q, scale, stream=None):
+    return _bind_run("fp8_i8_quantize_rows", *_i8_quantize_args(x, q, scale, stream))
+
+
+_OUT16 = (torch.bfloat16, torch.float16)
+
+
+def _i8_rows(t, what, shape, dev):
+    return _Operand(_arg(t.codes, f"{what}.codes", _I8, shape, dev), FP8_DT_I8,
+                    _arg(t.scale, f"{what}.scale", _F32, shape[:-1], dev))
+
+
+def _i8_args(x, w, bias, y, x8_out, sx_out, wshape, bshape, dev):
+    """C arguments shared by the dense and the grouped call: x, w, bias, out
+    dtype, y, x8_out, sx_out."""
+    M, K = _shape_of(x, 2, "x")
+    if not isinstance(w, QuantizedRows):
+        raise TypeError("w: expected a QuantizedRows operand")
+    yp = _arg(y, "y", _OUT16, (M, wshape[-2]), dev)
+    if isinstance(x, QuantizedRows):
+        ox, qp, sp = _i8_rows(x, "x", (M, K), dev), None, None
+    else:
+        ox = _Operand(_arg(x, "x", _HP, (M, K), dev), _TORCH_DT[x.dtype], None)
+        qp = _arg(x8_out, "x8_out", _I8, (M, K), dev)
+        sp = _arg(sx_out, "sx_out", _F32, None, dev, numel=M)
+    return (ox, _i8_rows(w, "w", wshape, dev),
+            _arg(bias, "bias", (y.dtype,), bshape, dev, True), _TORCH_DT[y.dtype], yp, qp, sp)
+
+
+def _i8_linear_args(x, w, bias, y, x8_out, sx_out, stream):
+    M, K = _shape_of(x, 2, "x")
+    N = _shape_of(w, 2, "w")[0]
+    dev = _gpu_of(x, "x")
+    return (M, N, K, *_i8_args(x, w, bias, y, x8_out, sx_out, (N, K), (N,), dev),
+            _arg_stream(stream, dev)), dev
+
+
+def fp8_i8_linear_fwd(x, w, bias, y, x8_out=None, sx_out=None, stream=None):
+    """y = x w^T (+ bias) in 8-bit integers, a scale for each token and output
+    channel.  x: [M, K] tensor (quantized here into x8_out int8 [M, K] and
+    sx_out float32 [M]) or QuantizedRows; w: QuantizedRows [N, K]; y bf16 or
+    fp16 [M, N]; bias of y's dtype [N] or None."""
+    _run("fp8_i8_linear_fwd", *_i8_linear_args(x, w, bias, y, x8_out, sx_out, stream))
+
+
+def bind_fp8_i8_linear_fwd(x, w, bias, y, x8_out=None, sx_out=None, stream=None):
+    return _bind_run("fp8_i8_linear_fwd", *_i8_linear_args(x, w, bias, y, x8_out, sx_out, stream))
+
+
+def _i8_grouped_args(x, w, bias, offsets, y, x8_out, sx_out, stream):
+    T, K = _shape_of(x, 2, "x")
+    E, N, _ = _shape_of(w, 3, "w")
+    dev = _gpu_of(x, "x")
+    return (T, E, N, K, _arg(offsets, "offsets", _I32, (E + 1,), dev),
+            *_i8_args(x, w, bias, y, x8_out, sx_out, (E, N, K), (E, N), dev),
+            _arg_stream(stream, dev)), dev
+
+
+def fp8_i8_grouped_linear_fwd(x, w, bias, offsets, y, x8_out=None, sx_out=None, stream=None):
+    """fp8_i8_linear_fwd over experts: w QuantizedRows [E, N, K] (scales
+    [E, N]), bias [E, N], offsets as in fp8_grouped_linear_fwd.  Rows behind
+    the last expert's are left as they were in y, x8_out and sx_out."""
+    _run("fp8_i8_grouped_linear_fwd", *_i8_grouped_args(x, w, bias, offsets, y, x8_out, sx_out,
+                                                        stream))
+
+
+def bind_fp8_i8_grouped_linear_fwd(x, w, bias, offsets, y, x8_out=None, sx_out=None, stream=None):
+    return _bind_run("fp8_i8_grouped_linear_fwd", *_i8_grouped_args(x, w, bias, offsets, y, x8_out,
+                                                                    sx_out, stream))

@@ -13,14 +13,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libfp8linear.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = [os.path.join(CSRC, "fp8l_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fp8l_api.hip", "fp8l_grouped.hip", "fp8l_i8.hip",
+                                           "fp8l_version.hip")]
+OBJ_DIR = os.path.join(HERE, "_build")  # objects; not tracked
 PROBE_LIB_PATH = os.path.join(HERE, "libfp8probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "fp8l_probe.hip")]
-HEADERS = [os.path.join(CSRC, f) for f in ("fp8l_device.hpp", "fp8l_quantize.hpp", "fp8l_gemm.hpp",
-                                                     "fp8l_gemm3.hpp", "fp8l_gemm4.hpp", "fp8l_gemm5.hpp",
-                                                     "fp8l_gemm_pair.hpp")] + [
-    os.path.join(ROOT, "include", "fp8linear.h")
-]
 
 
 def source_hash() -> str:
@@ -45,38 +42,52 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def build_command(out: str = LIB_PATH, extra: list[str] | None = None,
-                  sources: list[str] | None = None) -> list[str]:
+def _flags(source: str) -> list[str]:
     return [
-        hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",
+        "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
         # packed fp32 VALU forms stay off (see the library's design notes)
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-I", os.path.join(ROOT, "include"),
-        f'-DFP8L_SOURCE_HASH="{source_hash()}"',
-        *(extra or []),
-        *(SOURCES if sources is None else sources), "-o", out,
+        *([f'-DFP8L_SOURCE_HASH="{source_hash()}"'] if "version" in os.path.basename(source) else []),
     ]
 
 
-def build(verbose: bool = False) -> str:
-    """Compile both libraries (always recompiles; the two hipcc runs go in
-    parallel).  Returns the path of libfp8linear.so."""
-    jobs = [(LIB_PATH, build_command(LIB_PATH + ".tmp")),
-            (PROBE_LIB_PATH, build_command(PROBE_LIB_PATH + ".tmp", sources=PROBE_SOURCES))]
-    procs = [(out, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                    text=True)) for out, cmd in jobs]
+def compile_command(source: str, out: str, extra: list[str] | None = None) -> list[str]:
+    return [hipcc(), *_flags(source), *(extra or []), "-c", source, "-o", out]
+
+
+def link_command(objects: list[str], out: str) -> list[str]:
+    return [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objects, "-o", out]
+
+
+def _run_all(jobs: list[tuple[str, list[str]]], verbose: bool) -> None:
+    """Run the commands in parallel; raise with the output of those that failed."""
+    procs = [(name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                     text=True)) for name, cmd in jobs]
     failed = []
-    for out, proc in procs:
+    for name, proc in procs:
         text, _ = proc.communicate()
         msgs = [ln for ln in text.splitlines() if "packed-fp32-ops" not in ln and ln.strip()]
         if proc.returncode != 0:
-            failed.append(f"hipcc failed for {os.path.basename(out)}:\n" + "\n".join(msgs))
+            failed.append(f"hipcc failed for {name}:\n" + "\n".join(msgs))
         elif verbose and msgs:
             print("\n".join(msgs))
     if failed:
         raise RuntimeError("\n".join(failed))
-    for out, _ in jobs:
-        os.replace(out + ".tmp", out)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile both libraries (always recompiles; the translation units are
+    compiled in parallel).  Returns the path of libfp8linear.so."""
+    libs = {LIB_PATH: SOURCES, PROBE_LIB_PATH: PROBE_SOURCES}
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    obj = {src: os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
+           for srcs in libs.values() for src in srcs}
+    _run_all([(os.path.basename(src), compile_command(src, o)) for src, o in obj.items()], verbose)
+    _run_all([(os.path.basename(lib), link_command([obj[s] for s in srcs], lib + ".tmp"))
+              for lib, srcs in libs.items()], verbose)
+    for lib in libs:
+        os.replace(lib + ".tmp", lib)
     return LIB_PATH
 
 

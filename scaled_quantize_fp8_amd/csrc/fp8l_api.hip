@@ -21,104 +21,24 @@
 #include "fp8l_gemm.hpp"
 #include "fp8l_gemm5.hpp"
 #include "fp8l_gemm_pair.hpp"
+#include "fp8l_host.hpp"
 #include "fp8l_quantize.hpp"
 
 namespace fp8l {
-namespace {
 
-// Per-device host caches are atomics: library calls may come from several
-// host threads, and two first calls on one device may both fill an entry
-// (with the same value).
-int cu_count() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-      n = 256;
-    cached[dev].store(n, std::memory_order_relaxed);
+// Ring reset (one block): scale 1, idx 0, hist 0, every counter and max 0.
+__global__ void ring_init_kernel(RingHdr* h, float* hist, int H) {
+  for (int j = threadIdx.x; j < H; j += blockDim.x) hist[j] = 0.0f;
+  uint32_t* w = reinterpret_cast<uint32_t*>(h);
+  for (int j = threadIdx.x; j < (int)(sizeof(RingHdr) / 4); j += blockDim.x) w[j] = 0u;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    h->scale = 1.0f;
+    h->hist_len = (uint32_t)H;
   }
-  return n;
 }
 
-// Raise a kernel's dynamic LDS limit to lds bytes, once per device (the
-// flag is published after the attribute is set, so a thread that sees it
-// launches after the setting).
-void set_lds_limit(const void* kernel, int lds, std::atomic<bool> (&done)[64]) {
-  int dev = 0;
-  const bool known = hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < 64;
-  if (known && done[dev].load(std::memory_order_acquire)) return;
-  (void)hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (known) done[dev].store(true, std::memory_order_release);
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool is_hp(int32_t dt) { return dt == FP8_DT_F32 || dt == FP8_DT_F16 || dt == FP8_DT_BF16; }
-bool is_f8(int32_t dt) { return dt == FP8_DT_E4M3 || dt == FP8_DT_E5M2; }
-bool valid_fmt(int32_t f) { return f == FP8_E4M3 || f == FP8_E5M2; }
-int32_t fmt_dtype(int32_t f) { return f == FP8_E4M3 ? FP8_DT_E4M3 : FP8_DT_E5M2; }
-int dtype_fmt(int32_t dt) { return dt == FP8_DT_E4M3 ? kE4M3 : kE5M2; }
-bool is_fp8_dtype(int32_t dt) { return dt == FP8_DT_E4M3 || dt == FP8_DT_E5M2; }
-
-// a * b fits in int64 (a, b >= 0)
-bool mul_ok(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / 4 / a; }
-
-int check_ring(const fp8_ring_t* r) {
-  if (!r) return FP8_OK;
-  if (!r->dev) return FP8_ERR_NULL;
-  if (r->hist_len < 1 || r->hist_len > FP8_RING_MAX_HIST) return FP8_ERR_RING;
-  if (((uintptr_t)r->dev & 255u) != 0) return FP8_ERR_RING;
-  return FP8_OK;
-}
-
-// a scale output must not be the ring's own scale slot
-int check_alias(const fp8_ring_t* r, const float* scale_out) {
-  if (r && scale_out && (const void*)scale_out >= r->dev &&
-      (const char*)scale_out < (const char*)r->dev + sizeof(RingHdr))
-    return FP8_ERR_RING;
-  return FP8_OK;
-}
-
-// True while the stream is being captured into a graph.  A query that fails
-// counts as not capturing (a launch on such a stream fails on its own).
-bool capturing(hipStream_t st) {
-  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  return hipStreamIsCapturing(st, &cs) == hipSuccess && cs == hipStreamCaptureStatusActive;
-}
-
-// A ring's first use seeds it with an extra amax pass, decided on the host
-// from ring->seeded.  Captured into a graph, that pass and the seeding
-// conversion would run again on every replay (dynamic scaling, while the
-// host flag says seeded), so an unseeded ring is refused under capture.
-int check_seed_capture(const fp8_ring_t* r, hipStream_t st) {
-  return (r && !r->seeded && capturing(st)) ? FP8_ERR_RING : FP8_OK;
-}
-
-// Checks for one quantize (shared by the four entry points).
-int check_quant(const void* x, int32_t in_dtype, int64_t n, int32_t fmt, const uint8_t* q,
-                const fp8_ring_t* ring, const float* scale_used, const float* amax_out,
-                hipStream_t stream) {
-  if (n < 0) return FP8_ERR_SHAPE;
-  if (!is_hp(in_dtype) || !valid_fmt(fmt)) return FP8_ERR_DTYPE;
-  if (n > 0 && (!x || !q)) return FP8_ERR_NULL;
-  if (!scale_used) return FP8_ERR_NULL;
-  if (!ring && !amax_out) return FP8_ERR_NULL;
-  int st = check_ring(ring);
-  if (st) return st;
-  if ((st = check_alias(ring, scale_used))) return st;
-  return check_seed_capture(ring, stream);
-}
-
-// 2-D shape of a quantize: the column-sum variant (ws != null) or the
-// transposed/dual variant (tkernel: q and/or qt).
-struct ColsumSpec {
-  int64_t rows, cols;
-  float* ws;
-  uint8_t* qt = nullptr;
-  bool tkernel = false;
-};
+__global__ void zero_u32_kernel(uint32_t* p) { *p = 0u; }
 
 int64_t flat_blocks(int64_t n, int64_t cap) {
   int64_t blocks = (n + kBlockChunk - 1) / kBlockChunk;
@@ -144,10 +64,43 @@ void launch_convert(const QArgs& a, const ColsumSpec* cs, hipStream_t st) {
   }
 }
 
+// The amax passes: max |x| into the header of a ring that the converting
+// launch will seed, or (dynamic scaling) into amax_out.
+template <int IN>
+void launch_amax_ring(const void* x, int64_t n, RingHdr* h, const RowLimit& limit, hipStream_t st) {
+  const int64_t blocks = flat_blocks(n, (int64_t)cu_count() * 8);
+  hipLaunchKernelGGL((amax_ring_kernel<IN>), dim3((unsigned)blocks), dim3(kQThreads), 0, st, x, n,
+                     (int)aligned16(x), h, limit);
+}
+
+template <int IN>
+void launch_amax_dyn(const void* x, int64_t n, float* amax_out, const RowLimit& limit,
+                     hipStream_t st) {
+  hipLaunchKernelGGL(zero_u32_kernel, dim3(1), dim3(1), 0, st, reinterpret_cast<uint32_t*>(amax_out));
+  const int64_t blocks = flat_blocks(n, (int64_t)cu_count());
+  hipLaunchKernelGGL((amax_dyn_kernel<IN>), dim3((unsigned)blocks), dim3(kQThreads), 0, st, x, n,
+                     (int)aligned16(x), reinterpret_cast<uint32_t*>(amax_out), limit);
+}
+
+void enqueue_amax(const void* x, int32_t dt, int64_t n, const fp8_ring_t* ring, float* amax_out,
+                  const RowLimit& limit, hipStream_t st) {
+  RingHdr* h = ring ? reinterpret_cast<RingHdr*>(ring->dev) : nullptr;
+  auto run = [&](auto in) {
+    constexpr int IN = decltype(in)::value;
+    if (h) launch_amax_ring<IN>(x, n, h, limit, st);
+    else launch_amax_dyn<IN>(x, n, amax_out, limit, st);
+  };
+  if (dt == FP8_DT_F32) run(std::integral_constant<int, kInF32>{});
+  else if (dt == FP8_DT_F16) run(std::integral_constant<int, kInF16>{});
+  else run(std::integral_constant<int, kInBF16>{});
+}
+
 template <int IN, int FMT>
 void enqueue_quant_t(const void* x, int64_t n, uint8_t* q, fp8_ring_t* ring, float* scale_used,
-                     float* amax_out, const ColsumSpec* cs, hipStream_t st, bool defer) {
+                     float* amax_out, const ColsumSpec* cs, hipStream_t st, bool defer,
+                     const RowLimit& limit) {
   QArgs a = {};
+  a.limit = limit;
   a.x = x;
   a.q = q;
   a.n = n;
@@ -162,7 +115,6 @@ void enqueue_quant_t(const void* x, int64_t n, uint8_t* q, fp8_ring_t* ring, flo
     a.qt = cs->qt;
     a.qt_vec = cs->qt && aligned16(cs->qt) && cs->rows % 16 == 0;
   }
-  const int vec_x = aligned16(x);
   if (ring) {
     a.ring = reinterpret_cast<RingHdr*>(ring->dev);
     a.hist = reinterpret_cast<float*>(reinterpret_cast<char*>(ring->dev) + sizeof(RingHdr));
@@ -174,17 +126,12 @@ void enqueue_quant_t(const void* x, int64_t n, uint8_t* q, fp8_ring_t* ring, flo
     } else {
       // first use: the amax pass leaves max |x| in the ring header, the
       // converting launch seeds the scale from it, converts and folds.
-      const int64_t blocks = flat_blocks(n, (int64_t)cu_count() * 8);
-      hipLaunchKernelGGL((amax_ring_kernel<IN>), dim3((unsigned)blocks), dim3(kQThreads), 0, st, x,
-                         n, vec_x, a.ring);
+      launch_amax_ring<IN>(x, n, a.ring, limit, st);
       launch_convert<IN, FMT, kScaleSeed>(a, cs, st);
       ring->seeded = 1;
     }
   } else {
-    hipLaunchKernelGGL(zero_u32_kernel, dim3(1), dim3(1), 0, st, reinterpret_cast<uint32_t*>(amax_out));
-    const int64_t blocks = flat_blocks(n, (int64_t)cu_count());
-    hipLaunchKernelGGL((amax_dyn_kernel<IN>), dim3((unsigned)blocks), dim3(kQThreads), 0, st, x, n,
-                       vec_x, reinterpret_cast<uint32_t*>(amax_out));
+    launch_amax_dyn<IN>(x, n, amax_out, limit, st);
     launch_convert<IN, FMT, kScaleDyn>(a, cs, st);
   }
 }
@@ -236,27 +183,11 @@ void enqueue_quant2_in(int32_t fmt, const void* x0, int64_t n0, uint8_t* q0, fp8
 template <int IN>
 void enqueue_quant_in(const void* x, int64_t n, int32_t fmt, uint8_t* q, fp8_ring_t* ring,
                       float* scale_used, float* amax_out, const ColsumSpec* cs, hipStream_t st,
-                      bool defer) {
+                      bool defer, const RowLimit& limit) {
   if (fmt == FP8_E4M3)
-    enqueue_quant_t<IN, kE4M3>(x, n, q, ring, scale_used, amax_out, cs, st, defer);
+    enqueue_quant_t<IN, kE4M3>(x, n, q, ring, scale_used, amax_out, cs, st, defer, limit);
   else
-    enqueue_quant_t<IN, kE5M2>(x, n, q, ring, scale_used, amax_out, cs, st, defer);
-}
-
-// A quantize through this ring may leave its fold to the GEMM that consumes
-// the codes: the ring is seeded (one converting launch, no seeding pass) and
-// its window fits the one wave that folds it.
-bool can_defer(const fp8_ring_t* r) { return r && r->seeded && r->hist_len <= 64; }
-
-// The fold the consuming GEMM does for a deferred quantize through r.
-RingFold fold_of(const fp8_ring_t* r, int32_t fmt, float* amax_out) {
-  RingFold f = {};
-  f.ring = reinterpret_cast<RingHdr*>(r->dev);
-  f.hist = reinterpret_cast<float*>(reinterpret_cast<char*>(r->dev) + sizeof(RingHdr));
-  f.hist_len = r->hist_len;
-  f.fmt_max = fmt == FP8_E4M3 ? FmtTraits<kE4M3>::kMax : FmtTraits<kE5M2>::kMax;
-  f.amax_out = amax_out;
-  return f;
+    enqueue_quant_t<IN, kE5M2>(x, n, q, ring, scale_used, amax_out, cs, st, defer, limit);
 }
 
 // The fold of a ring whose groups a deferring launch filled, as a launch of
@@ -269,23 +200,26 @@ __global__ __launch_bounds__(64) void ring_fold2_kernel(RingFold f0, RingFold f1
   ring_fold_wave(f1);
 }
 
+void enqueue_fold(const RingFold& f, hipStream_t st) {
+  hipLaunchKernelGGL(ring_fold_kernel, dim3(1), dim3(64), 0, st, f);
+}
+
 // One quantize.  may_defer: the caller launches a GEMM on the codes next,
 // on the same stream, which folds the ring when this returns true.
 bool enqueue_quant(const void* x, int32_t in_dtype, int64_t n, int32_t fmt, uint8_t* q,
                    fp8_ring_t* ring, float* scale_used, float* amax_out, const ColsumSpec* cs,
-                   hipStream_t st, bool may_defer = false) {
+                   hipStream_t st, bool may_defer, const RowLimit& limit) {
   const bool defer = may_defer && can_defer(ring);
   // no consuming GEMM to hand the fold to: a one-wave launch folds it
   const bool fold_after = !may_defer && can_defer(ring);
   const bool groups_only = defer || fold_after;
   if (in_dtype == FP8_DT_F32)
-    enqueue_quant_in<kInF32>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only);
+    enqueue_quant_in<kInF32>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only, limit);
   else if (in_dtype == FP8_DT_F16)
-    enqueue_quant_in<kInF16>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only);
+    enqueue_quant_in<kInF16>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only, limit);
   else
-    enqueue_quant_in<kInBF16>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only);
-  if (fold_after)
-    hipLaunchKernelGGL(ring_fold_kernel, dim3(1), dim3(64), 0, st, fold_of(ring, fmt, amax_out));
+    enqueue_quant_in<kInBF16>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only, limit);
+  if (fold_after) enqueue_fold(fold_of(ring, fmt, amax_out), st);
   return defer;
 }
 
@@ -347,7 +281,6 @@ void launch_gemm3_t(GemmArgs& g, hipStream_t st) {
                      lds, st, g);
 }
 
-enum { kTileAuto = 0, kTile256x256, kTile256x128, kTile128x128, kTileV1, kTile256x256w8, kTile128x128w8 };
 
 // FP8L_TILE forces a tile configuration (for sweeps and tests): 256x256,
 // 256x128, 128x128 or v1 (the general register-staged kernel).  Read at
@@ -566,9 +499,7 @@ void finish_gemm_args(GemmArgs& g) {
   g.c_vec = ((uintptr_t)g.c & 7u) == 0 && g.ldc % 4 == 0 && g.bsc % 4 == 0;
 }
 
-int hip_status() { return hipGetLastError() == hipSuccess ? FP8_OK : FP8_ERR_HIP; }
 
-}  // namespace
 
 // Library-owned device memory of fp8_linear_bwd_dw_noalloc: the db column
 // partials, FP8_NOALLOC_WS_MAX bytes, one copy per GPU for the life of the
@@ -600,13 +531,6 @@ float* scratch_dev() {
 using namespace fp8l;
 
 extern "C" {
-
-int fp8_abi_version(void) { return FP8_ABI_VERSION; }
-
-#ifndef FP8L_SOURCE_HASH
-#define FP8L_SOURCE_HASH "unknown"
-#endif
-const char* fp8_source_hash(void) { return FP8L_SOURCE_HASH; }
 
 const char* fp8_status_str(int status) {
   switch (status) {

@@ -19,7 +19,9 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 #define FP8L_DEV __device__ __forceinline__
 
-enum { kE4M3 = 0, kE5M2 = 1 };
+// kI8: 8-bit integer codes (the row-scaled linear layers); the GEMM kernels
+// take it in the place of a format for both operands.
+enum { kE4M3 = 0, kE5M2 = 1, kI8 = 2 };
 enum { kInF32 = 0, kInF16 = 1, kInBF16 = 2 };
 
 // Largest finite magnitude of each OCP format [OCP]: E4M3 S.1111.110 = 448,

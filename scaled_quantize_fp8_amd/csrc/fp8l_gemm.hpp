@@ -105,6 +105,9 @@ struct GemmArgs {
   // blk0 + b, and blk0 is a multiple of 8, so b and the launch block sit on
   // the same XCD (workgroups are dealt round-robin over the 8 XCDs).
   int32_t blk0, nblk;
+  // 8-bit integer operands (kI8): scale_a holds one scale per row of C and
+  // scale_b one per column, C and the bias are fp16 when out_f16, else bf16
+  int32_t out_f16;
 };
 
 // This block's index within its problem, and the problem's block count (x).
@@ -304,27 +307,48 @@ FP8L_DEV void tile_coords(int pid, int tiles_m, int tiles_n, int& tm, int& tn) {
   tn = in_group / gm;
 }
 
+// One output value of the 8-bit integer GEMMs from its integer sum (the
+// accumulator's bits): one rounding to fp32, one product with the combined
+// scale, the bias in the same fma, one rounding to the output type.
+FP8L_DEV float i8_value(float acc_bits, float scale, float bias) {
+  return __builtin_fmaf((float)__float_as_int(acc_bits), scale, bias);
+}
+FP8L_DEV uint32_t f32_to_f16(float f) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
+}
+FP8L_DEV float f16_to_f32(uint32_t h) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+
+// One 16x16 tile step over 128 bytes of K: one FP8 MFMA, or two 8-bit
+// integer ones of 64 (each takes half of every lane's 32 bytes; which K
+// positions meet in which half is the same for both operands, and integer
+// sums do not depend on the order).
+template <int FA, int FB>
+FP8L_DEV v4f mma_16x16(v8i b, v8i a, v4f c) {
+  if constexpr (FA == kI8) {
+    typedef int v4i_t __attribute__((ext_vector_type(4)));
+    v4i_t s = __builtin_bit_cast(v4i_t, c);
+    s = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_shufflevector(b, b, 0, 1, 2, 3),
+                                              __builtin_shufflevector(a, a, 0, 1, 2, 3), s, 0, 0, 0);
+    s = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_shufflevector(b, b, 4, 5, 6, 7),
+                                              __builtin_shufflevector(a, a, 4, 5, 6, 7), s, 0, 0, 0);
+    return __builtin_bit_cast(v4f, s);
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, 0, 0, 0);
+  }
+}
+
+// Tile (tm, tn) of the problem g by one block; smem: kGemmLds bytes.
+constexpr int kGemmLds = 4 * kTileBytes;
 template <int LA, int LB, int FA, int FB>
-__global__ __launch_bounds__(kGThreads, 2) void gemm_kernel(GemmArgs g) {
-  batch_slice(g);
-  ring_folds(g);
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2][2][kTileBytes];
+FP8L_DEV void gemm_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem_) {
+  uint8_t(*smem)[2][kTileBytes] = reinterpret_cast<uint8_t(*)[2][kTileBytes]>(smem_);
   const int tid = threadIdx.x;
   const int wave = tid >> 6;
   const int lane = tid & 63;
-  int tm, tn;
-  tile_coords(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
   const int64_t i0 = (int64_t)tm * kBM;
   const int64_t j0 = (int64_t)tn * kBN;
-
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
-    if (g.aux_scale_dst0) *g.aux_scale_dst0 = *g.aux_scale_src0;
-    if (g.aux_amax_dst0) *g.aux_amax_dst0 = 0.0f;
-    if (g.aux_scale_dst1) *g.aux_scale_dst1 = *g.aux_scale_src1;
-    if (g.aux_amax_dst1) *g.aux_amax_dst1 = 0.0f;
-  }
-
-  if (g.db) db_finalize<kGThreads>(g);
 
   const int wm = wave >> 1, wn = wave & 1;
   v4f acc[4][4];
@@ -359,8 +383,7 @@ __global__ __launch_bounds__(kGThreads, 2) void gemm_kernel(GemmArgs g) {
     for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int b = 0; b < 4; ++b)
-        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[b], fa[a], acc[a][b], FB, FA,
-                                                                      0, 0, 0, 0);
+        acc[a][b] = mma_16x16<FA, FB>(fb[b], fa[a], acc[a][b]);
     if (more) {
       store_tile<LA>(smem[cur ^ 1][0], ra);
       store_tile<LB>(smem[cur ^ 1][1], rb);
@@ -369,9 +392,11 @@ __global__ __launch_bounds__(kGThreads, 2) void gemm_kernel(GemmArgs g) {
   }
 
   // epilogue: lane holds C[i0 + wm*64 + 16a + (lane&15)][j0 + wn*64 + 16b + 4*(lane>>4) + t]
-  const float dq = (1.0f / *g.scale_a) * (1.0f / *g.scale_b);
-  const float inv_bs =
-      (g.bias_kind == kBiasE4M3 || g.bias_kind == kBiasE5M2) ? 1.0f / *g.bias_scale : 1.0f;
+  float dq = 1.0f, inv_bs = 1.0f;
+  if constexpr (FA != kI8) {
+    dq = (1.0f / *g.scale_a) * (1.0f / *g.scale_b);
+    if (g.bias_kind == kBiasE4M3 || g.bias_kind == kBiasE5M2) inv_bs = 1.0f / *g.bias_scale;
+  }
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const int64_t j = j0 + wn * 64 + 16 * b + 4 * (lane >> 4);
@@ -379,15 +404,35 @@ __global__ __launch_bounds__(kGThreads, 2) void gemm_kernel(GemmArgs g) {
     if (g.bias_kind != kBiasNone) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        if (j + t < g.Nc) bias[t] = bias_at(g, j + t, inv_bs);
+        if (j + t < g.Nc) {
+          if (FA == kI8 && g.out_f16)
+            bias[t] = f16_to_f32(reinterpret_cast<const uint16_t*>(g.bias)[j + t]);
+          else
+            bias[t] = bias_at(g, j + t, inv_bs);
+        }
+    }
+    float isb[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if constexpr (FA == kI8) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (j + t < g.Nc) isb[t] = 1.0f / g.scale_b[j + t];
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int64_t i = i0 + wm * 64 + 16 * a + (lane & 15);
       if (i >= g.Mc) continue;
       uint32_t h[4];
+      if constexpr (FA == kI8) {
+        const float isa = 1.0f / g.scale_a[i];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) h[t] = f32_to_bf16(__builtin_fmaf(acc[a][b][t], dq, bias[t]));
+        for (int t = 0; t < 4; ++t) {
+          const float v = i8_value(acc[a][b][t], isa * isb[t], bias[t]);
+          h[t] = g.out_f16 ? f32_to_f16(v) : f32_to_bf16(v);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) h[t] = f32_to_bf16(__builtin_fmaf(acc[a][b][t], dq, bias[t]));
+      }
       uint16_t* dst = g.c + i * g.ldc + j;
       if (g.c_vec && j + 4 <= g.Nc) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
@@ -398,6 +443,25 @@ __global__ __launch_bounds__(kGThreads, 2) void gemm_kernel(GemmArgs g) {
       }
     }
   }
+}
+
+template <int LA, int LB, int FA, int FB>
+__global__ __launch_bounds__(kGThreads, 2) void gemm_kernel(GemmArgs g) {
+  batch_slice(g);
+  ring_folds(g);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kGemmLds];
+  int tm, tn;
+  tile_coords(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    if (g.aux_scale_dst0) *g.aux_scale_dst0 = *g.aux_scale_src0;
+    if (g.aux_amax_dst0) *g.aux_amax_dst0 = 0.0f;
+    if (g.aux_scale_dst1) *g.aux_scale_dst1 = *g.aux_scale_src1;
+    if (g.aux_amax_dst1) *g.aux_amax_dst1 = 0.0f;
+  }
+
+  if (g.db) db_finalize<kGThreads>(g);
+  gemm_tile<LA, LB, FA, FB>(g, tm, tn, smem);
 }
 
 }  // namespace fp8l

@@ -152,21 +152,59 @@ struct MfmaSlot {
 #define FP8L_CO3 FP8L_CO2, FP8L_CO(2)
 #define FP8L_CO4 FP8L_CO3, FP8L_CO(3)
 #define FP8L_CI(i) [b##i] "v"(*m[i].b), [x##i] "v"(*m[i].x)
+#define FP8L_FMT [fb] "n"(FB), [fa] "n"(FA)
 #define FP8L_CI1 FP8L_CI(0)
 #define FP8L_CI2 FP8L_CI1, FP8L_CI(1)
 #define FP8L_CI3 FP8L_CI2, FP8L_CI(2)
 #define FP8L_CI4 FP8L_CI3, FP8L_CI(3)
-#define FP8L_FMT [fb] "n"(FB), [fa] "n"(FA)
+#define FP8L_FI1 FP8L_CI1, FP8L_FMT
+#define FP8L_FI2 FP8L_CI2, FP8L_FMT
+#define FP8L_FI3 FP8L_CI3, FP8L_FMT
+#define FP8L_FI4 FP8L_CI4, FP8L_FMT
+
+// 8-bit integer operands: a lane's 32 bytes of a 64-byte K step feed two
+// v_mfma_i32_32x32x32_i8, its low and its high 16 bytes (K positions
+// {0..15, 32..47} and {16..31, 48..63} of the step, alike in both operands;
+// integer sums do not depend on the order).  The accumulators hold int32
+// bits.  A chain of two on one accumulator needs no wait states.
+#define FP8L_ML(i) "v_mfma_i32_32x32x32_i8 %[c" #i "], %[b" #i "], %[x" #i "], %[c" #i "]\n\t"
+#define FP8L_MH(i) "v_mfma_i32_32x32x32_i8 %[c" #i "], %[d" #i "], %[y" #i "], %[c" #i "]\n\t"
+#define FP8L_MI1 FP8L_ML(0) FP8L_MH(0)
+#define FP8L_MI2 FP8L_ML(0) FP8L_ML(1) FP8L_MH(0) FP8L_MH(1)
+#define FP8L_MI3 FP8L_ML(0) FP8L_ML(1) FP8L_ML(2) FP8L_MH(0) FP8L_MH(1) FP8L_MH(2)
+#define FP8L_MI4 FP8L_MI2 FP8L_ML(2) FP8L_ML(3) FP8L_MH(2) FP8L_MH(3)
+#define FP8L_II(i)                                                          \
+  [b##i] "v"(lo4(*m[i].b)), [d##i] "v"(hi4(*m[i].b)), [x##i] "v"(lo4(*m[i].x)), \
+      [y##i] "v"(hi4(*m[i].x))
+#define FP8L_II1 FP8L_II(0)
+#define FP8L_II2 FP8L_II1, FP8L_II(1)
+#define FP8L_II3 FP8L_II2, FP8L_II(2)
+#define FP8L_II4 FP8L_II3, FP8L_II(3)
+FP8L_DEV v4i lo4(v8i v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3); }
+FP8L_DEV v4i hi4(v8i v) { return __builtin_shufflevector(v, v, 4, 5, 6, 7); }
+
+// Expands S(M, I, n) for the block's MFMA count NM (1..4) and element kind:
+// MF / FI are the FP8 instruction and its inputs, MI / II the integer ones.
+#define FP8L_BY_COUNT(S)                           \
+  do {                                             \
+    if constexpr (FA == kI8) {                     \
+      if constexpr (NM == 1) S(MI, II, 1);         \
+      else if constexpr (NM == 2) S(MI, II, 2);    \
+      else if constexpr (NM == 3) S(MI, II, 3);    \
+      else S(MI, II, 4);                           \
+    } else {                                       \
+      if constexpr (NM == 1) S(MF, FI, 1);         \
+      else if constexpr (NM == 2) S(MF, FI, 2);    \
+      else if constexpr (NM == 3) S(MF, FI, 3);    \
+      else S(MF, FI, 4);                           \
+    }                                              \
+  } while (0)
 
 template <int FA, int FB, int NM>
 FP8L_DEV void mfma_only(const MfmaSlot (&m)[4]) {
   // s_nop 1: operands may have just been written by VALU
-#define FP8L_ONLY(n) \
-  asm volatile("s_nop 1\n\t" FP8L_MF##n "" : FP8L_CO##n : FP8L_CI##n, FP8L_FMT)
-  if constexpr (NM == 1) FP8L_ONLY(1);
-  else if constexpr (NM == 2) FP8L_ONLY(2);
-  else if constexpr (NM == 3) FP8L_ONLY(3);
-  else FP8L_ONLY(4);
+#define FP8L_ONLY(M, I, n) asm volatile("s_nop 1\n\t" FP8L_##M##n "" : FP8L_CO##n : FP8L_##I##n)
+  FP8L_BY_COUNT(FP8L_ONLY);
 #undef FP8L_ONLY
 }
 
@@ -272,6 +310,69 @@ struct BiasStage {
     return fp8_to_f32_rt(sb[jl], g.bias_kind == kBiasE4M3 ? kE4M3 : kE5M2) * inv_bs;
   }
 };
+
+// Scales of the 8-bit integer GEMMs: one per row of C (scale_a) and one per
+// column (scale_b), BM + BN floats staged in LDS behind the bias by DMA
+// loads of 64 floats each, issued ahead of the operand stages like the bias
+// (rows and columns past the edge read zeros and are never stored).  Four
+// bytes per lane: a group's first row, and so its scales, start at any
+// multiple of 4 bytes.
+template <int BM, int BN, int NW>
+struct RowColScales {
+  static constexpr int kBytes = 4 * (BM + BN);
+  FP8L_DEV static void load(const GemmArgs& g, int64_t i0, int64_t j0, uint8_t* s, int wave) {
+    const int lane = threadIdx.x & 63;
+    const int rows = (int)(g.Mc - i0 < BM ? g.Mc - i0 : BM);
+    const int cols = (int)(g.Nc - j0 < BN ? g.Nc - j0 : BN);
+    for (int c = wave; c < (BM + BN) / 64; c += NW) {
+      const bool row = c < BM / 64;
+      const int first = 64 * (row ? c : c - BM / 64);
+      const __amdgpu_buffer_rsrc_t rs =
+          make_rsrc(row ? g.scale_a + i0 : g.scale_b + j0, (uint32_t)(4 * (row ? rows : cols)));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(s + 256 * c), 4, 4u * (first + lane), 0, 0, 0);
+    }
+  }
+  FP8L_DEV static float row(const uint8_t* s, int il) {
+    return reinterpret_cast<const float*>(s)[il];
+  }
+  FP8L_DEV static float col(const uint8_t* s, int jl) {
+    return reinterpret_cast<const float*>(s)[BM + jl];
+  }
+};
+
+// Four outputs of the 8-bit integer GEMMs (acc: the int32 sums' bits, isa
+// and isc: 1/scale of the row and of each column), packed to bf16 or fp16.
+FP8L_DEV uint2 i8_pack4(const float acc[4], float isa, const float isc[4], const float bias[4],
+                        int f16) {
+  float v[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) v[t] = i8_value(acc[t], isa * isc[t], bias[t]);
+  if (f16)
+    return make_uint2(f32_to_f16(v[0]) | (f32_to_f16(v[1]) << 16),
+                      f32_to_f16(v[2]) | (f32_to_f16(v[3]) << 16));
+  return make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+}
+
+// Column factors and bias of four consecutive block columns.
+template <int BM, int BN, int NW>
+FP8L_DEV void i8_cols(const GemmArgs& g, const uint8_t* sbias, const uint8_t* sscale, int64_t j0,
+                      int jl, float isc[4], float bias[4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    isc[t] = 1.0f / RowColScales<BM, BN, NW>::col(sscale, jl + t);
+    bias[t] = 0.0f;
+    if (g.bias_kind != kBiasNone) {
+      // the bias has the output's type
+      uint32_t h = 0;
+      if (BiasStage<BN>::staged(g))
+        h = reinterpret_cast<const uint16_t*>(sbias)[jl + t];
+      else if (j0 + jl + t < g.Nc)
+        h = reinterpret_cast<const uint16_t*>(g.bias)[j0 + jl + t];
+      bias[t] = g.out_f16 ? f16_to_f32(h) : bf16_to_f32(h);
+    }
+  }
+}
 
 // One operand of the pipelined kernel.  R: tile extent along C; NW: waves.
 template <int L, int R, int NW>
@@ -445,15 +546,12 @@ struct Op3 {
 template <int FA, int FB, int NM, int OFF>
 FP8L_DEV void kc1o(uint32_t a0, uint32_t a1, v8i& n0, const MfmaSlot (&m)[4]) {
   v4i r0, r1;
-#define FP8L_KC1O(n)                                                                      \
-  asm volatile(FP8L_RKC(r0, a0, o0) FP8L_RKC(r1, a1, o0) FP8L_MF##n "s_waitcnt lgkmcnt(0)" \
+#define FP8L_KC1O(M, I, n)                                                                      \
+  asm volatile(FP8L_RKC(r0, a0, o0) FP8L_RKC(r1, a1, o0) FP8L_##M##n "s_waitcnt lgkmcnt(0)" \
                : [r0] "=&v"(r0), [r1] "=&v"(r1), FP8L_CO##n                                \
-               : [a0] "v"(a0), [a1] "v"(a1), [o0] "n"(OFF), FP8L_CI##n, FP8L_FMT           \
+               : [a0] "v"(a0), [a1] "v"(a1), [o0] "n"(OFF), FP8L_##I##n           \
                : "memory")
-  if constexpr (NM == 1) FP8L_KC1O(1);
-  else if constexpr (NM == 2) FP8L_KC1O(2);
-  else if constexpr (NM == 3) FP8L_KC1O(3);
-  else FP8L_KC1O(4);
+  FP8L_BY_COUNT(FP8L_KC1O);
 #undef FP8L_KC1O
   n0 = v8i{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 }
@@ -462,17 +560,13 @@ FP8L_DEV void kc1o(uint32_t a0, uint32_t a1, v8i& n0, const MfmaSlot (&m)[4]) {
 template <int FA, int FB, int NM, int D1 = 2048, int O0 = 0>
 FP8L_DEV void kc2o(uint32_t a0, uint32_t a1, v8i& n0, v8i& n1, const MfmaSlot (&m)[4]) {
   v4i r0, r1, r2, r3;
-#define FP8L_KC2O(n)                                                                           \
+#define FP8L_KC2O(M, I, n)                                                                       \
   asm volatile(FP8L_RKC(r0, a0, o0) FP8L_RKC(r1, a1, o0) FP8L_RKC(r2, a0, o1)                  \
-                   FP8L_RKC(r3, a1, o1) FP8L_MF##n "s_waitcnt lgkmcnt(0)"                      \
+                   FP8L_RKC(r3, a1, o1) FP8L_##M##n "s_waitcnt lgkmcnt(0)"                      \
                : [r0] "=&v"(r0), [r1] "=&v"(r1), [r2] "=&v"(r2), [r3] "=&v"(r3), FP8L_CO##n     \
-               : [a0] "v"(a0), [a1] "v"(a1), [o0] "n"(O0), [o1] "n"(O0 + D1), FP8L_CI##n,    \
-                 FP8L_FMT                                                                      \
+               : [a0] "v"(a0), [a1] "v"(a1), [o0] "n"(O0), [o1] "n"(O0 + D1), FP8L_##I##n        \
                : "memory")
-  if constexpr (NM == 1) FP8L_KC2O(1);
-  else if constexpr (NM == 2) FP8L_KC2O(2);
-  else if constexpr (NM == 3) FP8L_KC2O(3);
-  else FP8L_KC2O(4);
+  FP8L_BY_COUNT(FP8L_KC2O);
 #undef FP8L_KC2O
   n0 = v8i{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
   n1 = v8i{r2.x, r2.y, r2.z, r2.w, r3.x, r3.y, r3.z, r3.w};
@@ -482,17 +576,14 @@ FP8L_DEV void kc2o(uint32_t a0, uint32_t a1, v8i& n0, v8i& n1, const MfmaSlot (&
 template <int FA, int FB, int NM, int DT>
 FP8L_DEV void x1o(uint32_t b, v8i& n0, const MfmaSlot (&m)[4]) {
   v2i r0, r1, r2, r3;
-#define FP8L_X1O(n)                                                                            \
+#define FP8L_X1O(M, I, n)                                                                        \
   asm volatile(FP8L_RX(r0, p0, o0) FP8L_RX(r1, p0, o1) FP8L_RX(r2, p0, o2) FP8L_RX(r3, p0, o3) \
-                   FP8L_MF##n "s_waitcnt lgkmcnt(0)"                                           \
+                   FP8L_##M##n "s_waitcnt lgkmcnt(0)"                                           \
                : [r0] "=&v"(r0), [r1] "=&v"(r1), [r2] "=&v"(r2), [r3] "=&v"(r3), FP8L_CO##n     \
                : [p0] "v"(b), [o0] "n"(0), [o1] "n"(DT), [o2] "n"(2 * DT), [o3] "n"(3 * DT),     \
-                 FP8L_CI##n, FP8L_FMT                                                          \
+                 FP8L_##I##n                                                          \
                : "memory")
-  if constexpr (NM == 1) FP8L_X1O(1);
-  else if constexpr (NM == 2) FP8L_X1O(2);
-  else if constexpr (NM == 3) FP8L_X1O(3);
-  else FP8L_X1O(4);
+  FP8L_BY_COUNT(FP8L_X1O);
 #undef FP8L_X1O
   n0 = v8i{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
 }
@@ -501,19 +592,16 @@ FP8L_DEV void x1o(uint32_t b, v8i& n0, const MfmaSlot (&m)[4]) {
 template <int FA, int FB, int NM, int DT>
 FP8L_DEV void x2o(uint32_t b0, uint32_t b1, v8i& n0, v8i& n1, const MfmaSlot (&m)[4]) {
   v2i r0, r1, r2, r3, r4, r5, r6, r7;
-#define FP8L_X2O(n)                                                                             \
+#define FP8L_X2O(M, I, n)                                                                        \
   asm volatile(FP8L_RX(r0, p0, o0) FP8L_RX(r1, p0, o1) FP8L_RX(r2, p0, o2) FP8L_RX(r3, p0, o3)  \
                    FP8L_RX(r4, p1, o0) FP8L_RX(r5, p1, o1) FP8L_RX(r6, p1, o2)                  \
-                       FP8L_RX(r7, p1, o3) FP8L_MF##n "s_waitcnt lgkmcnt(0)"                    \
+                       FP8L_RX(r7, p1, o3) FP8L_##M##n "s_waitcnt lgkmcnt(0)"                    \
                : [r0] "=&v"(r0), [r1] "=&v"(r1), [r2] "=&v"(r2), [r3] "=&v"(r3), [r4] "=&v"(r4), \
                  [r5] "=&v"(r5), [r6] "=&v"(r6), [r7] "=&v"(r7), FP8L_CO##n                     \
                : [p0] "v"(b0), [p1] "v"(b1), [o0] "n"(0), [o1] "n"(DT), [o2] "n"(2 * DT),        \
-                 [o3] "n"(3 * DT), FP8L_CI##n, FP8L_FMT                                         \
+                 [o3] "n"(3 * DT), FP8L_##I##n                                         \
                : "memory")
-  if constexpr (NM == 1) FP8L_X2O(1);
-  else if constexpr (NM == 2) FP8L_X2O(2);
-  else if constexpr (NM == 3) FP8L_X2O(3);
-  else FP8L_X2O(4);
+  FP8L_BY_COUNT(FP8L_X2O);
 #undef FP8L_X2O
   n0 = v8i{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
   n1 = v8i{r4.x, r4.y, r5.x, r5.y, r6.x, r6.y, r7.x, r7.y};
@@ -550,9 +638,10 @@ constexpr int gemm3_bias_off() {
                                                          : BM * (BN * 2 + 16);
 }
 
-template <int BM, int BN, int WGM, int WGN>
+template <int BM, int BN, int WGM, int WGN, bool I8 = false>
 constexpr int gemm3_lds_bytes() {
-  return gemm3_bias_off<BM, BN>() + BiasStage<BN>::kBytes;
+  return gemm3_bias_off<BM, BN>() + BiasStage<BN>::kBytes +
+         (I8 ? RowColScales<BM, BN, WGM * WGN>::kBytes : 0);
 }
 
 // Epilogue of gemm3_kernel: bf16 output, or the FP8-output GEMM's passes
@@ -662,12 +751,12 @@ FP8L_DEV void fp8_out_epilogue(const GemmArgs& g, const v16f (&acc)[FM][FN], flo
   }
 }
 
+// Tile (tm, tn) of the problem g by one block, on the dynamic LDS at smem3.
 template <int BM, int BN, int WGM, int WGN, int LA, int LB, int FA, int FB, int EPI = kEpiBF16,
           int OF = kE4M3>
-__global__ __launch_bounds__(64 * WGM * WGN, (BM * BN <= 128 * 128) ? 2 : 1)
-void gemm3_kernel(GemmArgs g) {
-  batch_slice(g);
+FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
   constexpr int NW = WGM * WGN;
+  constexpr bool I8 = FA == kI8;
   using OA = Op3<LA, BM, NW>;
   using OB = Op3<LB, BN, NW>;
   constexpr int WTM = BM / WGM, WTN = BN / WGN;  // wave tile
@@ -675,11 +764,8 @@ void gemm3_kernel(GemmArgs g) {
   static_assert(FM % 2 == 0 && FN % 2 == 0, "fragments are read in pairs");
   constexpr int kStep = OA::kBytes + OB::kBytes;  // LDS bytes per K step
   constexpr int kDma = OA::kPerWave + OB::kPerWave;  // DMA instructions per wave per step
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem3[];
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  int tm, tn;
-  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
   const int64_t i0 = (int64_t)tm * BM, j0 = (int64_t)tn * BN;
   uint8_t* const sbias = smem3 + gemm3_bias_off<BM, BN>();  // BiasStage area
 
@@ -708,7 +794,9 @@ void gemm3_kernel(GemmArgs g) {
 
   // prologue: DMA steps 0..3, then step 0's fragments
   BiasStage<BN>::load(g, j0, sbias, wv);  // ahead of the stages (see BiasStage)
-  const EpiScales es = load_scales(g);
+  uint8_t* const sscale = sbias + BiasStage<BN>::kBytes;  // RowColScales area (I8)
+  if constexpr (I8) RowColScales<BM, BN, NW>::load(g, i0, j0, sscale, wv);
+  const EpiScales es = I8 ? EpiScales{1.0f, 1.0f, 1.0f} : load_scales(g);
   const float s_out = out_scale<EPI, OF>(g);
   for (int s = 0; s < kStages3 && s < nk; ++s) {
     oa.issue(ra, step_buf(s), s);
@@ -863,6 +951,7 @@ void gemm3_kernel(GemmArgs g) {
   constexpr int RS = BN * 2 + 16;  // LDS bytes per staged row
   mfma_drain();                    // accumulators are read by VALU below
   side_work<64 * WGM * WGN>(g);    // after the drain: it may reuse fragment registers
+  if (nk == 0) wait_vm<0>();       // no step's wait covered the bias and scales
   barrier_only();                  // every wave is done reading operand tiles
   const float dq = es.dq(), inv_bs = es.inv_bs();
   if constexpr (EPI != kEpiBF16) {
@@ -875,8 +964,10 @@ void gemm3_kernel(GemmArgs g) {
 #pragma unroll
     for (int grp = 0; grp < 4; ++grp) {
       const int jl = wn * WTN + 32 * b + 8 * grp + 4 * (lane >> 5);
-      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (g.bias_kind != kBiasNone) {
+      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, isc[4];
+      if constexpr (I8) {
+        i8_cols<BM, BN, NW>(g, sbias, sscale, j0, jl, isc, bias);
+      } else if (g.bias_kind != kBiasNone) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           bias[t] = BiasStage<BN>::get(g, sbias, j0, jl + t, inv_bs);
@@ -885,6 +976,13 @@ void gemm3_kernel(GemmArgs g) {
       for (int a = 0; a < FM; ++a) {
         const int il = wm * WTM + 32 * a + (lane & 31);
         float v[4];
+        if constexpr (I8) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = acc[a][b][4 * grp + t];
+          *reinterpret_cast<uint2*>(smem3 + il * RS + jl * 2) =
+              i8_pack4(v, 1.0f / RowColScales<BM, BN, NW>::row(sscale, il), isc, bias, g.out_f16);
+          continue;
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) v[t] = __builtin_fmaf(acc[a][b][4 * grp + t], dq, bias[t]);
         *reinterpret_cast<uint2*>(smem3 + il * RS + jl * 2) =
@@ -902,6 +1000,17 @@ void gemm3_kernel(GemmArgs g) {
       __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(smem3 + r * RS + ch * 16),
                                   reinterpret_cast<v4u*>(g.c + (i0 + r) * g.ldc + j0 + 8 * ch));
   }
+}
+
+template <int BM, int BN, int WGM, int WGN, int LA, int LB, int FA, int FB, int EPI = kEpiBF16,
+          int OF = kE4M3>
+__global__ __launch_bounds__(64 * WGM * WGN, (BM * BN <= 128 * 128) ? 2 : 1)
+void gemm3_kernel(GemmArgs g) {
+  batch_slice(g);
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem3[];
+  int tm, tn;
+  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
+  gemm3_tile<BM, BN, WGM, WGN, LA, LB, FA, FB, EPI, OF>(g, tm, tn, smem3);
 }
 
 }  // namespace fp8l

@@ -28,11 +28,10 @@ namespace fp8l {
 constexpr int kGemm4BiasOff =
     kStages3 * 512 * kBK3 > 256 * (256 * 2 + 16) ? kStages3 * 512 * kBK3 : 256 * (256 * 2 + 16);
 
-// The kernel's work for one block, on the dynamic LDS at smem4 (also run by
-// the grouped launch of fp8l_gemm_pair.hpp).
+// Tile (tm, tn) of the problem g by one block, on the dynamic LDS at smem4.
 template <int LA, int LB, int FA, int FB, int EPI = kEpiBF16, int OF = kE4M3>
-FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
-  batch_slice(g);
+FP8L_DEV void gemm4_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem4) {
+  constexpr bool I8 = FA == kI8;
   constexpr int BM = 256, BN = 256, WGM = 2, WGN = 4, NW = WGM * WGN;
   using OA = Op3<LA, BM, NW>;
   using OB = Op3<LB, BN, NW>;
@@ -44,8 +43,6 @@ FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
   static_assert(kDma == 4, "one DMA load after each of the four read groups");
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  int tm, tn;
-  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
   const int64_t i0 = (int64_t)tm * BM, j0 = (int64_t)tn * BN;
   uint8_t* const sbias = smem4 + kGemm4BiasOff;  // BiasStage area
 
@@ -93,7 +90,9 @@ FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
 
   // prologue: DMA steps 0..3, read step 0, issue its first two MFMAs
   BiasStage<BN>::load(g, j0, sbias, wv);  // ahead of the stages (see BiasStage)
-  const EpiScales es = load_scales(g);
+  uint8_t* const sscale = sbias + BiasStage<BN>::kBytes;  // RowColScales area (I8)
+  if constexpr (I8) RowColScales<BM, BN, NW>::load(g, i0, j0, sscale, wv);
+  const EpiScales es = I8 ? EpiScales{1.0f, 1.0f, 1.0f} : load_scales(g);
   const float s_out = out_scale<EPI, OF>(g);
   for (int s = 0; s < kStages3 && s <= nk; ++s) issue_step(s);
   if (nk > 0) {
@@ -226,8 +225,10 @@ FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
 #pragma unroll
     for (int grp = 0; grp < 4; ++grp) {
       const int jl = rb0 + 32 * b + 8 * grp + 4 * (lane >> 5);
-      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (g.bias_kind != kBiasNone) {
+      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, isc[4];
+      if constexpr (I8) {
+        i8_cols<BM, BN, NW>(g, sbias, sscale, j0, jl, isc, bias);
+      } else if (g.bias_kind != kBiasNone) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           bias[t] = BiasStage<BN>::get(g, sbias, j0, jl + t, inv_bs);
@@ -236,6 +237,13 @@ FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
       for (int a = 0; a < FM; ++a) {
         const int il = ra0 + 32 * a + (lane & 31);
         float v[4];
+        if constexpr (I8) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = acc[a][b][4 * grp + t];
+          *reinterpret_cast<uint2*>(smem4 + il * RS + jl * 2) =
+              i8_pack4(v, 1.0f / RowColScales<BM, BN, NW>::row(sscale, il), isc, bias, g.out_f16);
+          continue;
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) v[t] = __builtin_fmaf(acc[a][b][4 * grp + t], dq, bias[t]);
         *reinterpret_cast<uint2*>(smem4 + il * RS + jl * 2) =
@@ -255,12 +263,25 @@ FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
   }
 }
 
+// The kernel's work for one block (also run by the grouped launch of
+// fp8l_gemm_pair.hpp): its tile in XCD-major order.
+template <int LA, int LB, int FA, int FB, int EPI = kEpiBF16, int OF = kE4M3>
+FP8L_DEV void gemm4_body(GemmArgs& g, uint8_t* smem4) {
+  batch_slice(g);
+  int tm, tn;
+  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
+  gemm4_tile<LA, LB, FA, FB, EPI, OF>(g, tm, tn, smem4);
+}
+
 template <int LA, int LB, int FA, int FB, int EPI = kEpiBF16, int OF = kE4M3>
 __global__ __launch_bounds__(512, 1) void gemm4_kernel(GemmArgs g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem4[];
   gemm4_body<LA, LB, FA, FB, EPI, OF>(g, smem4);
 }
 
-constexpr int gemm4_lds_bytes() { return kGemm4BiasOff + BiasStage<256>::kBytes; }
+template <bool I8 = false>
+constexpr int gemm4_lds_bytes() {
+  return kGemm4BiasOff + BiasStage<256>::kBytes + (I8 ? RowColScales<256, 256, 8>::kBytes : 0);
+}
 
 }  // namespace fp8l

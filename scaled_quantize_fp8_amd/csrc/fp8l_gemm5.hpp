@@ -172,17 +172,25 @@ struct Stage128<kCross, R, NW> : Op3<kCross, R, NW> {
   }
 };
 
+// Sum of two partial sums: fp32, or int32 bits.
+template <bool I8>
+FP8L_DEV float add_sums(float a, float b) {
+  if constexpr (I8)
+    return __int_as_float(__float_as_int(a) + __float_as_int(b));
+  else
+    return a + b;
+}
+
 // LDS: the operand ring (the output staging and the K-half exchange reuse
 // it), then the bias of the block's 128 columns (BiasStage).
 constexpr int kGemm5BiasOff = kStages3 * 2 * 256 * kBK3 > 128 * (128 * 2 + 16)
                                   ? kStages3 * 2 * 256 * kBK3
                                   : 128 * (128 * 2 + 16);
 
-// The kernel's work for one block, on the dynamic LDS at smem5 (also run by
-// the grouped launch of fp8l_gemm_pair.hpp).
+// Tile (tm, tn) of the problem g by one block, on the dynamic LDS at smem5.
 template <int LA, int LB, int FA, int FB>
-FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
-  batch_slice(g);
+FP8L_DEV void gemm5_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem5) {
+  constexpr bool I8 = FA == kI8;
   constexpr int BM = 128, BN = 128, NW = 8;
   using OA = Stage128<LA, BM, NW>;  // 16 KB per stage, two DMA loads per wave
   using OB = Stage128<LB, BN, NW>;
@@ -191,8 +199,6 @@ FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
   constexpr int kDma = 4;                          // loads per wave per stage
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  int tm, tn;
-  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
   const int64_t i0 = (int64_t)tm * BM, j0 = (int64_t)tn * BN;
   uint8_t* const sbias = smem5 + kGemm5BiasOff;  // BiasStage area
 
@@ -250,7 +256,9 @@ FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
   auto slot = [&](int a, int b, int par) { return MfmaSlot{&acc[a][b], &fb[par][b], &fa[par][a]}; };
 
   BiasStage<BN>::load(g, j0, sbias, wv);  // ahead of the stages (see BiasStage)
-  const EpiScales es = load_scales(g);
+  uint8_t* const sscale = sbias + BiasStage<BN>::kBytes;  // RowColScales area (I8)
+  if constexpr (I8) RowColScales<BM, BN, NW>::load(g, i0, j0, sscale, wv);
+  const EpiScales es = I8 ? EpiScales{1.0f, 1.0f, 1.0f} : load_scales(g);
   for (int s = 0; s < kStages3 && s < ns; ++s) {
     load(s, J0{});
     load(s, J1{});
@@ -342,6 +350,7 @@ FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
   mfma_drain();
   side_work<64 * NW>(g);  // after the drain: its VALU work may reuse fragment registers
   const float dq = es.dq(), inv_bs = es.inv_bs();
+  if (ns == 0) wait_vm<0>();  // no stage's wait covered the bias and scales
   barrier_only();  // every wave's last stage reads are done
   auto xslot = [&](int a, int b, int g4) {
     return smem5 + kXchg + ((quad * 2 + a) * 2 + b) * 4096 + g4 * 1024 + lane * 16;
@@ -365,7 +374,8 @@ FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
       const v4f p = *reinterpret_cast<const v4f*>(xslot(kq, b, g4));
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        own[b][4 * g4 + t] = (kq == 0 ? acc[0][b][4 * g4 + t] : acc[1][b][4 * g4 + t]) + p[t];
+        own[b][4 * g4 + t] =
+            add_sums<I8>(kq == 0 ? acc[0][b][4 * g4 + t] : acc[1][b][4 * g4 + t], p[t]);
     }
 
   // Epilogue as in gemm3_kernel, for fragment row kq of the quadrant.
@@ -375,13 +385,21 @@ FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
 #pragma unroll
     for (int grp = 0; grp < 4; ++grp) {
       const int jl = rb0 + 32 * b + 8 * grp + 4 * (lane >> 5);
-      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, isc[4];
+      float v[4];
+      if constexpr (I8) {
+        i8_cols<BM, BN, NW>(g, sbias, sscale, j0, jl, isc, bias);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] = own[b][4 * grp + t];
+        *reinterpret_cast<uint2*>(smem5 + il * RS + jl * 2) =
+            i8_pack4(v, 1.0f / RowColScales<BM, BN, NW>::row(sscale, il), isc, bias, g.out_f16);
+        continue;
+      }
       if (g.bias_kind != kBiasNone) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           bias[t] = BiasStage<BN>::get(g, sbias, j0, jl + t, inv_bs);
       }
-      float v[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) v[t] = __builtin_fmaf(own[b][4 * grp + t], dq, bias[t]);
       *reinterpret_cast<uint2*>(smem5 + il * RS + jl * 2) =
@@ -400,12 +418,25 @@ FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
   }
 }
 
+// The kernel's work for one block (also run by the grouped launch of
+// fp8l_gemm_pair.hpp): its tile in XCD-major order.
+template <int LA, int LB, int FA, int FB>
+FP8L_DEV void gemm5_body(GemmArgs& g, uint8_t* smem5) {
+  batch_slice(g);
+  int tm, tn;
+  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
+  gemm5_tile<LA, LB, FA, FB>(g, tm, tn, smem5);
+}
+
 template <int LA, int LB, int FA, int FB>
 __global__ __launch_bounds__(512, 1) void gemm5_kernel(GemmArgs g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem5[];
   gemm5_body<LA, LB, FA, FB>(g, smem5);
 }
 
-constexpr int gemm5_lds_bytes() { return kGemm5BiasOff + BiasStage<128>::kBytes; }
+template <bool I8 = false>
+constexpr int gemm5_lds_bytes() {
+  return kGemm5BiasOff + BiasStage<128>::kBytes + (I8 ? RowColScales<128, 128, 8>::kBytes : 0);
+}
 
 }  // namespace fp8l

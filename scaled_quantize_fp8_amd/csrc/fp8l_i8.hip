@@ -1,0 +1,162 @@
+// C entry points of the linear layers in 8-bit integers with one scale per
+// token and one per output channel, dense and over ragged groups of rows.
+// Checks run before the first launch; nothing is allocated.
+#include "fp8l_grouped_host.hpp"
+#include "fp8l_i8.hpp"
+
+namespace fp8l {
+namespace {
+
+// One tile per block in XCD-major order.
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void i8_gemm_kernel(GemmArgs g) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_i8[];
+  int tm, tn;
+  tile_coords_xcd(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  Tile::run(g, tm, tn, smem_i8);
+}
+
+template <class Tile>
+void launch_i8_t(GemmArgs& g, hipStream_t st) {
+  static std::atomic<bool> lds_set[64];
+  set_lds_limit((const void*)i8_gemm_kernel<Tile>, Tile::kLds, lds_set);
+  g.tiles_m = (int32_t)((g.Mc + Tile::kBM - 1) / Tile::kBM);
+  g.tiles_n = (int32_t)((g.Nc + Tile::kBN - 1) / Tile::kBN);
+  hipLaunchKernelGGL((i8_gemm_kernel<Tile>), dim3((unsigned)g.tiles_m * (unsigned)g.tiles_n),
+                     dim3(Tile::kThreads), Tile::kLds, st, g);
+}
+
+bool i8_fast_ok(const GemmArgs& g) {
+  GroupStrides s = {};
+  return rows_fast_ok<kKContig>(g, s) && (g.Mc + 256) * g.lda < (1LL << 31);
+}
+
+int i8_tile(const GemmArgs& g) {
+  if (!i8_fast_ok(g)) return kTileV1;
+  const int f = forced_tile();
+  if (f == kTileV1 || f == kTile128x128w8 || f == kTile256x256w8) return f;
+  return kTileV1;
+}
+
+void enqueue_rows(const void* x, int32_t dt, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                  const int32_t* valid, hipStream_t st) {
+  if (rows == 0) return;
+  RowsArgs a = {x, q, scale, rows, cols, 0, valid};
+  a.vec_ok = aligned16(x) && ((uintptr_t)q & 7u) == 0 && cols % 8 == 0;
+  const int64_t cap = (int64_t)cu_count() * 8;
+  const dim3 grid((unsigned)(rows < cap ? rows : cap));
+  if (dt == FP8_DT_F32)
+    hipLaunchKernelGGL(quantize_rows_kernel<kInF32>, grid, dim3(kQThreads), 0, st, a);
+  else if (dt == FP8_DT_F16)
+    hipLaunchKernelGGL(quantize_rows_kernel<kInF16>, grid, dim3(kQThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL(quantize_rows_kernel<kInBF16>, grid, dim3(kQThreads), 0, st, a);
+}
+
+// 128 * 128 * K stays below 2^31: the int32 sums cannot overflow, whatever
+// the codes.
+constexpr int64_t kI8MaxK = 131071;
+
+int check_i8(int64_t M, int64_t N, int64_t K, const fp8_operand_t& x, const fp8_operand_t& w,
+             int32_t out_dtype, const void* y, const int8_t* x8_out, const float* sx_out) {
+  if (K > kI8MaxK) return FP8_ERR_SHAPE;
+  if (out_dtype != FP8_DT_BF16 && out_dtype != FP8_DT_F16) return FP8_ERR_DTYPE;
+  if (w.dtype != FP8_DT_I8) return FP8_ERR_DTYPE;
+  if (is_hp(x.dtype)) {
+    if (M * K > 0 && (!x.data || !x8_out)) return FP8_ERR_NULL;
+    if (M > 0 && !sx_out) return FP8_ERR_NULL;
+  } else if (x.dtype == FP8_DT_I8) {
+    if ((M * K > 0 && !x.data) || (M > 0 && !x.scale)) return FP8_ERR_NULL;
+  } else {
+    return FP8_ERR_DTYPE;
+  }
+  if ((N * K > 0 && !w.data) || (N > 0 && !w.scale)) return FP8_ERR_NULL;
+  if (M * N > 0 && !y) return FP8_ERR_NULL;
+  return FP8_OK;
+}
+
+// The GEMM's arguments; a high-precision x is quantized first.
+GemmArgs i8_args(int64_t M, int64_t N, int64_t K, const fp8_operand_t& x, const fp8_operand_t& w,
+                 const void* bias, int32_t out_dtype, void* y, int8_t* x8_out, float* sx_out,
+                 const int32_t* valid, hipStream_t st) {
+  GemmArgs g = {};
+  if (is_hp(x.dtype)) {
+    enqueue_rows(x.data, x.dtype, M, K, x8_out, sx_out, valid, st);
+    g.a = reinterpret_cast<const uint8_t*>(x8_out);
+    g.scale_a = sx_out;
+  } else {
+    g.a = reinterpret_cast<const uint8_t*>(x.data);
+    g.scale_a = x.scale;
+  }
+  g.lda = K;
+  g.b = reinterpret_cast<const uint8_t*>(w.data);
+  g.ldb = K;
+  g.scale_b = w.scale;
+  g.Mc = M;
+  g.Nc = N;
+  g.Kc = K;
+  g.c = reinterpret_cast<uint16_t*>(y);
+  g.ldc = N;
+  g.bias = bias;
+  g.bias_kind = bias ? kBiasBF16 : kBiasNone;  // two bytes each, in y's type
+  g.out_f16 = out_dtype == FP8_DT_F16;
+  return g;
+}
+
+}  // namespace
+}  // namespace fp8l
+
+using namespace fp8l;
+
+extern "C" {
+
+int fp8_i8_quantize_rows(const void* x, int32_t in_dtype, int64_t rows, int64_t cols, int8_t* q,
+                         float* scale, hipStream_t stream) {
+  if (rows < 0 || cols < 0 || !mul_ok(rows, cols)) return FP8_ERR_SHAPE;
+  if (!is_hp(in_dtype)) return FP8_ERR_DTYPE;
+  if (rows * cols > 0 && (!x || !q)) return FP8_ERR_NULL;
+  if (rows > 0 && !scale) return FP8_ERR_NULL;
+  enqueue_rows(x, in_dtype, rows, cols, q, scale, nullptr, stream);
+  return hip_status();
+}
+
+int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_operand_t w,
+                      const void* bias, int32_t out_dtype, void* y, int8_t* x8_out, float* sx_out,
+                      hipStream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return FP8_ERR_SHAPE;
+  if (!mul_ok(M, K) || !mul_ok(N, K) || !mul_ok(M, N)) return FP8_ERR_SHAPE;
+  if (((M + 127) / 128) > INT32_MAX / ((N + 127) / 128 + 1)) return FP8_ERR_SHAPE;
+  const int st = check_i8(M, N, K, x, w, out_dtype, y, x8_out, sx_out);
+  if (st) return st;
+  GemmArgs g = i8_args(M, N, K, x, w, bias, out_dtype, y, x8_out, sx_out, nullptr, stream);
+  finish_grouped_args(g, GroupStrides{});
+  if (M > 0 && N > 0) {
+    const int tile = i8_tile(g);
+    if (tile == kTile256x256w8) launch_i8_t<Tile256<kKContig, kKContig, kI8, kI8>>(g, stream);
+    else if (tile == kTile128x128w8) launch_i8_t<Tile128<kKContig, kKContig, kI8, kI8>>(g, stream);
+    else launch_i8_t<TileAny<kKContig, kKContig, kI8, kI8>>(g, stream);
+  }
+  return hip_status();
+}
+
+int fp8_i8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
+                              fp8_operand_t x, fp8_operand_t w, const void* bias,
+                              int32_t out_dtype, void* y, int8_t* x8_out, float* sx_out,
+                              hipStream_t stream) {
+  int st = check_grouped(T, E, N, K);
+  if (st) return st;
+  if (!offsets) return FP8_ERR_NULL;
+  if ((st = check_i8(T, N, K, x, w, out_dtype, y, x8_out, sx_out))) return st;
+  GemmArgs g = i8_args(T, N, K, x, w, bias, out_dtype, y, x8_out, sx_out, offsets + E, stream);
+  GroupStrides s = {};
+  s.b = N * K;
+  s.sb = (int32_t)N;
+  s.bias = (int32_t)N;
+  finish_grouped_args(g, s);
+  const Groups gr = {offsets, E, (int32_t)T};
+  if (T > 0 && N > 0)
+    launch_rows<kKContig, kI8, kI8>(g, gr, s, GroupedSide{}, rows_tile<kKContig>(g, gr, s), stream);
+  return hip_status();
+}
+
+}  // extern "C"

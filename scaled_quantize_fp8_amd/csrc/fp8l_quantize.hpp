@@ -47,6 +47,18 @@ constexpr int kBlockChunk = 4 * kWaveChunk;
 constexpr int kColStrip = 256;              // columns per block (column-sum kernel)
 constexpr int kColRowsPerChunk = 32;        // rows per block = one workspace row
 
+// Rows in use, known on the device only: of a [max_rows, cols] tensor the
+// first *rows are quantized and the rest neither read nor written (the rows
+// behind the last group of a ragged batch).  rows null: no limit.
+struct RowLimit {
+  const int32_t* rows;
+  int64_t max_rows, cols;
+};
+FP8L_DEV int64_t limited(int64_t n, const RowLimit& l) {
+  if (!l.rows) return n;
+  return min<int64_t>(max(*l.rows, 0), l.max_rows) * l.cols;
+}
+
 struct QArgs {
   const void* x;
   uint8_t* q;
@@ -61,6 +73,7 @@ struct QArgs {
   int32_t vec_ok;     // x, q 16-byte aligned (and cols % 8 == 0 for the column variant)
   uint8_t* qt;        // transposed variant: [cols, rows] codes or null (q may be null)
   int32_t qt_vec;     // qt 16-byte aligned and rows % 16 == 0
+  RowLimit limit;     // flat variant
 };
 
 template <int IN>
@@ -327,12 +340,13 @@ FP8L_DEV void finish_launch(const QArgs& a, uint32_t mx, float s, uint32_t bid, 
 template <int IN, int FMT, int SMODE>
 FP8L_DEV void quantize_flat_body(const QArgs& a, uint32_t bid, uint32_t nblk) {
   const float s = launch_scale<FMT, SMODE>(a);
+  const int64_t n = limited(a.n, a.limit);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t mx = 0;
-  for (int64_t base = (int64_t)bid * kBlockChunk + wave * kWaveChunk; base < a.n;
+  for (int64_t base = (int64_t)bid * kBlockChunk + wave * kWaveChunk; base < n;
        base += (int64_t)nblk * kBlockChunk) {
     const int64_t e0 = base + 8 * lane, e1 = base + 512 + 8 * lane;
-    if (a.vec_ok && base + kWaveChunk <= a.n) {
+    if (a.vec_ok && base + kWaveChunk <= n) {
       float v0[8], v1[8];
       load8<IN>(a.x, e0, v0);
       load8<IN>(a.x, e1, v1);
@@ -347,10 +361,10 @@ FP8L_DEV void quantize_flat_body(const QArgs& a, uint32_t bid, uint32_t nblk) {
       mx = max(mx, max(m0, m1));
     } else {
       float v[8];
-      if (e0 < a.n)
-        mx = max(mx, quant_scalar8<IN, FMT>(a.x, a.q, e0, (int)min<int64_t>(8, a.n - e0), s, v));
-      if (e1 < a.n)
-        mx = max(mx, quant_scalar8<IN, FMT>(a.x, a.q, e1, (int)min<int64_t>(8, a.n - e1), s, v));
+      if (e0 < n)
+        mx = max(mx, quant_scalar8<IN, FMT>(a.x, a.q, e0, (int)min<int64_t>(8, n - e0), s, v));
+      if (e1 < n)
+        mx = max(mx, quant_scalar8<IN, FMT>(a.x, a.q, e1, (int)min<int64_t>(8, n - e1), s, v));
     }
   }
   finish_launch<FMT, SMODE>(a, mx, s, bid, nblk);
@@ -530,8 +544,8 @@ FP8L_DEV uint32_t flat_absmax(const void* x, int64_t n, int vec_ok) {
 // top_amax (counters back at zero) for the converting launch that follows.
 template <int IN>
 __global__ __launch_bounds__(kQThreads) void amax_ring_kernel(const void* x, int64_t n, int vec_ok,
-                                                             RingHdr* h) {
-  amax_pass_finish(h, flat_absmax<IN>(x, n, vec_ok), blockIdx.x, gridDim.x);
+                                                             RingHdr* h, RowLimit lim) {
+  amax_pass_finish(h, flat_absmax<IN>(x, limited(n, lim), vec_ok), blockIdx.x, gridDim.x);
 }
 
 // amax pass of a dynamic quantize: one device atomic max per block into
@@ -539,9 +553,9 @@ __global__ __launch_bounds__(kQThreads) void amax_ring_kernel(const void* x, int
 // one block per CU, so the atomics stay few.
 template <int IN>
 __global__ __launch_bounds__(kQThreads) void amax_dyn_kernel(const void* x, int64_t n, int vec_ok,
-                                                            uint32_t* target) {
+                                                            uint32_t* target, RowLimit lim) {
   __shared__ uint32_t sh4[4];
-  const uint32_t bm = block_max_u32(flat_absmax<IN>(x, n, vec_ok), sh4);
+  const uint32_t bm = block_max_u32(flat_absmax<IN>(x, limited(n, lim), vec_ok), sh4);
   if (threadIdx.x == 0 && bm != 0) atom_max(target, bm);
 }
 
@@ -578,19 +592,5 @@ __global__ __launch_bounds__(kQThreads) void colsum_fp8_kernel(const uint8_t* g8
   for (int y = 0; y < 8; ++y) t += shsum[y][col];
   if (gc < cols) colsum[(int64_t)blockIdx.y * cols + gc] = t;
 }
-
-// Ring reset (one block): scale 1, idx 0, hist 0, every counter and max 0.
-__global__ void ring_init_kernel(RingHdr* h, float* hist, int H) {
-  for (int j = threadIdx.x; j < H; j += blockDim.x) hist[j] = 0.0f;
-  uint32_t* w = reinterpret_cast<uint32_t*>(h);
-  for (int j = threadIdx.x; j < (int)(sizeof(RingHdr) / 4); j += blockDim.x) w[j] = 0u;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    h->scale = 1.0f;
-    h->hist_len = (uint32_t)H;
-  }
-}
-
-__global__ void zero_u32_kernel(uint32_t* p) { *p = 0u; }
 
 }  // namespace fp8l
