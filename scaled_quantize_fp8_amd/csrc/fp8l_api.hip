@@ -294,6 +294,11 @@ int forced_tile() {
   if (!strcmp(e, "v1")) return kTileV1;
   if (!strcmp(e, "256x256w8")) return kTile256x256w8;
   if (!strcmp(e, "128x128w8")) return kTile128x128w8;
+  if (!strcmp(e, "128x256")) return kTile128x256;    // this and the rest:
+  if (!strcmp(e, "skinny16")) return kTileSkinny16;  // grouped and integer layers only
+  if (!strcmp(e, "skinny32")) return kTileSkinny32;
+  if (!strcmp(e, "skinny48")) return kTileSkinny48;
+  if (!strcmp(e, "skinny64")) return kTileSkinny64;
   return kTileAuto;
 }
 

@@ -638,10 +638,9 @@ constexpr int gemm3_bias_off() {
                                                          : BM * (BN * 2 + 16);
 }
 
-template <int BM, int BN, int WGM, int WGN, bool I8 = false>
+template <int BM, int BN, int WGM, int WGN>
 constexpr int gemm3_lds_bytes() {
-  return gemm3_bias_off<BM, BN>() + BiasStage<BN>::kBytes +
-         (I8 ? RowColScales<BM, BN, WGM * WGN>::kBytes : 0);
+  return gemm3_bias_off<BM, BN>() + BiasStage<BN>::kBytes;
 }
 
 // Epilogue of gemm3_kernel: bf16 output, or the FP8-output GEMM's passes
@@ -751,12 +750,12 @@ FP8L_DEV void fp8_out_epilogue(const GemmArgs& g, const v16f (&acc)[FM][FN], flo
   }
 }
 
-// Tile (tm, tn) of the problem g by one block, on the dynamic LDS at smem3.
 template <int BM, int BN, int WGM, int WGN, int LA, int LB, int FA, int FB, int EPI = kEpiBF16,
           int OF = kE4M3>
-FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
+__global__ __launch_bounds__(64 * WGM * WGN, (BM * BN <= 128 * 128) ? 2 : 1)
+void gemm3_kernel(GemmArgs g) {
+  batch_slice(g);
   constexpr int NW = WGM * WGN;
-  constexpr bool I8 = FA == kI8;
   using OA = Op3<LA, BM, NW>;
   using OB = Op3<LB, BN, NW>;
   constexpr int WTM = BM / WGM, WTN = BN / WGN;  // wave tile
@@ -764,8 +763,11 @@ FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
   static_assert(FM % 2 == 0 && FN % 2 == 0, "fragments are read in pairs");
   constexpr int kStep = OA::kBytes + OB::kBytes;  // LDS bytes per K step
   constexpr int kDma = OA::kPerWave + OB::kPerWave;  // DMA instructions per wave per step
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem3[];
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  int tm, tn;
+  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
   const int64_t i0 = (int64_t)tm * BM, j0 = (int64_t)tn * BN;
   uint8_t* const sbias = smem3 + gemm3_bias_off<BM, BN>();  // BiasStage area
 
@@ -794,9 +796,7 @@ FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
 
   // prologue: DMA steps 0..3, then step 0's fragments
   BiasStage<BN>::load(g, j0, sbias, wv);  // ahead of the stages (see BiasStage)
-  uint8_t* const sscale = sbias + BiasStage<BN>::kBytes;  // RowColScales area (I8)
-  if constexpr (I8) RowColScales<BM, BN, NW>::load(g, i0, j0, sscale, wv);
-  const EpiScales es = I8 ? EpiScales{1.0f, 1.0f, 1.0f} : load_scales(g);
+  const EpiScales es = load_scales(g);
   const float s_out = out_scale<EPI, OF>(g);
   for (int s = 0; s < kStages3 && s < nk; ++s) {
     oa.issue(ra, step_buf(s), s);
@@ -951,7 +951,7 @@ FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
   constexpr int RS = BN * 2 + 16;  // LDS bytes per staged row
   mfma_drain();                    // accumulators are read by VALU below
   side_work<64 * WGM * WGN>(g);    // after the drain: it may reuse fragment registers
-  if (nk == 0) wait_vm<0>();       // no step's wait covered the bias and scales
+  if (nk == 0) wait_vm<0>();       // no step's wait covered the bias
   barrier_only();                  // every wave is done reading operand tiles
   const float dq = es.dq(), inv_bs = es.inv_bs();
   if constexpr (EPI != kEpiBF16) {
@@ -964,10 +964,8 @@ FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
 #pragma unroll
     for (int grp = 0; grp < 4; ++grp) {
       const int jl = wn * WTN + 32 * b + 8 * grp + 4 * (lane >> 5);
-      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, isc[4];
-      if constexpr (I8) {
-        i8_cols<BM, BN, NW>(g, sbias, sscale, j0, jl, isc, bias);
-      } else if (g.bias_kind != kBiasNone) {
+      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (g.bias_kind != kBiasNone) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           bias[t] = BiasStage<BN>::get(g, sbias, j0, jl + t, inv_bs);
@@ -976,13 +974,6 @@ FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
       for (int a = 0; a < FM; ++a) {
         const int il = wm * WTM + 32 * a + (lane & 31);
         float v[4];
-        if constexpr (I8) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) v[t] = acc[a][b][4 * grp + t];
-          *reinterpret_cast<uint2*>(smem3 + il * RS + jl * 2) =
-              i8_pack4(v, 1.0f / RowColScales<BM, BN, NW>::row(sscale, il), isc, bias, g.out_f16);
-          continue;
-        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) v[t] = __builtin_fmaf(acc[a][b][4 * grp + t], dq, bias[t]);
         *reinterpret_cast<uint2*>(smem3 + il * RS + jl * 2) =
@@ -1000,17 +991,6 @@ FP8L_DEV void gemm3_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem3) {
       __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(smem3 + r * RS + ch * 16),
                                   reinterpret_cast<v4u*>(g.c + (i0 + r) * g.ldc + j0 + 8 * ch));
   }
-}
-
-template <int BM, int BN, int WGM, int WGN, int LA, int LB, int FA, int FB, int EPI = kEpiBF16,
-          int OF = kE4M3>
-__global__ __launch_bounds__(64 * WGM * WGN, (BM * BN <= 128 * 128) ? 2 : 1)
-void gemm3_kernel(GemmArgs g) {
-  batch_slice(g);
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem3[];
-  int tm, tn;
-  tile_coords_xcd(prob_block(g), g.tiles_m, g.tiles_n, tm, tn);
-  gemm3_tile<BM, BN, WGM, WGN, LA, LB, FA, FB, EPI, OF>(g, tm, tn, smem3);
 }
 
 }  // namespace fp8l

@@ -15,6 +15,7 @@
 #pragma once
 
 #include "fp8l_device.hpp"
+#include "fp8l_gemm.hpp"
 
 namespace fp8l {
 
@@ -33,14 +34,15 @@ struct GroupSpan {
 
 FP8L_DEV int group_edge(const Groups& g, int i) { return min(max(g.off[i], 0), g.T); }
 
-// Inclusive prefix sum over the 64 lanes.
+// Inclusive prefix sum over the 64 lanes: shifts inside the rows of 16 lanes
+// (a lane without a source adds 0), then each row's total to the later rows.
 FP8L_DEV int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15, rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31, rows 2 and 3
   return v;
 }
 
@@ -91,6 +93,44 @@ FP8L_DEV GroupSpan find_group(const Groups& g, int per, int u) {
     carry = __builtin_amdgcn_readlane(incl, 63);
   }
   return GroupSpan{-1, 0, 0, 0, carry};
+}
+
+// This block's tile of a launch over all groups' units times tiles_n tile
+// columns (e = -1: none): tiles numbered group by group, XCD x (blocks
+// x mod 8) taking the x-th eighth; tm within the group.  With at most 64
+// groups one pass over the offsets does it.
+FP8L_DEV GroupSpan rows_work(const Groups& g, int per, int tiles_n, int& tm, int& tn) {
+  const int lane = threadIdx.x & 63;
+  const int x = blockIdx.x % 8, k = blockIdx.x / 8;
+  int s = 0, t = 0, n = 0, incl = 0, total;
+  if (g.E <= 64) {
+    if (lane < g.E) {
+      s = group_edge(g, lane);
+      t = max(group_edge(g, lane + 1), s);
+      n = units_of(t - s, per);
+    }
+    incl = wave_scan(n);
+    total = __builtin_amdgcn_readlane(incl, 63);
+  } else {
+    total = group_units(g, per);
+  }
+  const int nb = total * tiles_n, q = nb / 8, r = nb % 8;
+  if (k >= q + (x < r ? 1 : 0)) return GroupSpan{-1, 0, 0, 0, 0};
+  const int pid = x * q + min(x, r) + k;
+  const int u = pid / tiles_n;
+  GroupSpan sp;
+  if (g.E <= 64) {
+    const int l = __builtin_ctzll(__ballot(incl > u));
+    sp.e = l;
+    sp.start = __builtin_amdgcn_readlane(s, l);
+    sp.end = __builtin_amdgcn_readlane(t, l);
+    sp.before = __builtin_amdgcn_readlane(incl - n, l);
+    sp.unit = u - sp.before;
+  } else {
+    sp = find_group(g, per, u);
+  }
+  tile_coords(pid - sp.before * tiles_n, units_of(sp.end - sp.start, per), tiles_n, tm, tn);
+  return sp;
 }
 
 // Rows and units of group e itself, and the units before it.

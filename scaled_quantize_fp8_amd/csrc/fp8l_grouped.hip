@@ -74,6 +74,8 @@ void launch_dw(GemmArgs& g, int fa, int fb, const Groups& gr, const GroupStrides
     constexpr int FA = decltype(a)::value, FB = decltype(b)::value;
     if (tile == kTile256x256w8)
       launch_contract<Tile256<kCross, kCross, FA, FB>>(g, gr, s, st);
+    else if (tile == kTile128x256)
+      launch_contract<Tile128x256<kCross, kCross, FA, FB>>(g, gr, s, st);
     else if (tile == kTile128x128w8)
       launch_contract<Tile128<kCross, kCross, FA, FB>>(g, gr, s, st);
     else

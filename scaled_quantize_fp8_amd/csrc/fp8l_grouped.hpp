@@ -28,6 +28,7 @@
 #pragma once
 
 #include "fp8l_gemm5.hpp"
+#include "fp8l_gemm6.hpp"
 #include "fp8l_group.hpp"
 
 namespace fp8l {
@@ -81,6 +82,14 @@ struct Tile256 {
   }
 };
 template <int LA, int LB, int FA, int FB>
+struct Tile128x256 {
+  static constexpr int kBM = 128, kBN = 256, kThreads = 256, kBlocks = 2;
+  static constexpr int kLds = gemm6_lds_bytes<FA == kI8>();
+  FP8L_DEV static void run(const GemmArgs& g, int tm, int tn, uint8_t* s) {
+    gemm6_tile<LA, LB, FA, FB>(g, tm, tn, s);
+  }
+};
+template <int LA, int LB, int FA, int FB>
 struct Tile128 {
   static constexpr int kBM = 128, kBN = 128, kThreads = 512, kBlocks = 1;
   static constexpr int kLds = gemm5_lds_bytes<FA == kI8>();
@@ -89,28 +98,29 @@ struct Tile128 {
   }
 };
 
-// I8: scale_a holds one scale per row, scale_b one per column of each group.
+// Move a problem's operands to tile row tm (of bm rows) of a group; A ends
+// with the group.  I8: scale_a holds one scale per row.
+template <bool I8>
+FP8L_DEV void move_to_rows(GemmArgs& g, const GroupStrides& st, const GroupSpan& sp, int tm,
+                           int bm) {
+  const int64_t row = sp.start + (int64_t)tm * bm;
+  g.a += row * g.lda;
+  g.c += row * g.ldc;
+  g.Mc = min<int64_t>(sp.end - row, bm);
+  g.b += sp.e * st.b;
+  g.scale_b += (int64_t)sp.e * st.sb;
+  if (I8) g.scale_a += row;
+  if (g.bias) g.bias = reinterpret_cast<const uint16_t*>(g.bias) + (int64_t)sp.e * st.bias;
+}
+
 template <class Tile, bool I8>
 __global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void grouped_rows_kernel(
     GemmArgs g, Groups gr, GroupStrides st, GroupedSide side) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem_rows[];
-  const int nb = group_units(gr, Tile::kBM) * g.tiles_n;
-  const int x = blockIdx.x % 8, k = blockIdx.x / 8;
-  const int q = nb / 8, r = nb % 8;
-  if (k < q + (x < r ? 1 : 0)) {
-    const int pid = x * q + min(x, r) + k;
-    const GroupSpan sp = find_group(gr, Tile::kBM, pid / g.tiles_n);
-    int tm, tn;
-    tile_coords(pid - sp.before * g.tiles_n, units_of(sp.end - sp.start, Tile::kBM), g.tiles_n, tm,
-                tn);
-    const int64_t row = sp.start + (int64_t)tm * Tile::kBM;
-    g.a += row * g.lda;
-    g.c += row * g.ldc;
-    g.Mc = min<int64_t>(sp.end - row, Tile::kBM);  // A ends with the group
-    g.b += sp.e * st.b;
-    g.scale_b += (int64_t)sp.e * st.sb;
-    if (I8) g.scale_a += row;
-    if (g.bias) g.bias = reinterpret_cast<const uint16_t*>(g.bias) + (int64_t)sp.e * st.bias;
+  int tm, tn;
+  const GroupSpan sp = rows_work(gr, Tile::kBM, g.tiles_n, tm, tn);
+  if (sp.e >= 0) {
+    move_to_rows<I8>(g, st, sp, tm, Tile::kBM);
     Tile::run(g, 0, tn, smem_rows);
   }
   grouped_side(side);

@@ -2,8 +2,11 @@
 // and the 8-bit integer entry points.
 #pragma once
 
+#include <math.h>
+
 #include "fp8l_grouped.hpp"
 #include "fp8l_host.hpp"
+#include "fp8l_skinny.hpp"
 
 namespace fp8l {
 
@@ -47,19 +50,101 @@ bool rows_fast_ok(const GemmArgs& g, const GroupStrides& s) {
          512 * g.lda < (1LL << 31) && (b_rows + 256) * g.ldb < (1LL << 31);
 }
 
-// Tile of a rows launch, by the mean group (the host knows no other):
-// 256x256 from 96 rows on (8190 rows in 64 groups, 1536 -> 6912: 228 us
-// against 303 on 128x128), else 128x128.
+// Waves that split K in a skinny launch of `waves` tile columns, doubled
+// while a wave has over 24 pieces of K (16 experts of 4096 -> 11008, one row
+// each: 130 us at 32 pieces per wave, 105 at 16), or the chip has room for
+// more waves and pieces to give them (one row, 4096 -> 11008: 12.6 us at 8
+// waves against 13.6 at 2 and 21.7 at 1; 1536 -> 6912: 5.4 at 4, 6.7 at 8 with
+// one or two pieces each), or there are so few waves that any split helps
+// (512 -> 512: 3.4 us at 8 waves, 4.5 at 1).
+inline int skinny_kw(int64_t waves, int64_t K) {
+  const int64_t pieces = (K + 127) / 128;
+  int kw = 1;
+  while (kw < 8 && (pieces > 24 * kw || (waves * kw < 8192 && pieces >= 4 * kw) ||
+                    (waves * kw < 1024 && 2 * pieces > kw)))
+    kw *= 2;
+  return kw;
+}
+
+// Microseconds of a launch of `tiles` tiles with contraction K, from fits to
+// a sweep of the integer GEMM over 64 .. 4096 rows of six layer shapes
+// (within about 15%): a fixed part per launch and per round of tiles on the
+// CUs (first stages, epilogue), and a part per unit of K.  One round at
+// K = 1536 / 4096 / 11008:
+//   128x128, one block per CU:    13 / 25 /  55 us
+//   128x256, one block per CU:    20 / 40 / 100, two: 37 / 88 / 223
+//   256x256:                      29 / 58 / 135
+inline double tile_us(int tile, double tiles, double K) {
+  const double cus = cu_count();
+  switch (tile) {
+    case kTile128x128w8: return 3 + ceil(tiles / cus) * (4 + K * 0.0044);
+    case kTile256x256w8: return 3 + ceil(tiles / cus) * (8 + K * 0.0125);
+    default: {  // kTile128x256
+      if (tiles <= cus) return 8 + K * 0.0080;
+      const double rounds = tiles / (2 * cus) + 0.25;
+      return 3 + (rounds < 1 ? 1 : rounds) * (5 + K * 0.0195);
+    }
+  }
+}
+
+// The fastest of the three for launches of t128 tiles of 128x128, t12 of
+// 128x256, t256 of 256x256.
+inline int pick_of(double t128, double t12, double t256, double K, double* us) {
+  const double a = tile_us(kTile128x128w8, t128, K), b = tile_us(kTile128x256, t12, K),
+               c = tile_us(kTile256x256w8, t256, K);
+  *us = a < b ? (a < c ? a : c) : (b < c ? b : c);
+  return *us == a ? kTile128x128w8 : (*us == b ? kTile128x256 : kTile256x256w8);
+}
+
+// The same for the skinny kernel: a piece of 128 bytes of K for 16 columns
+// takes 0.13 us of a CU with up to 16 rows (HBM bound), 0.19 with 32, 0.25
+// with 48, 0.32 with 64 (A comes from L2 for every 16 columns); of blocks
+// beyond one per CU about a third overlaps.
+inline double skinny_us(int mt, double units, int64_t N, int64_t K) {
+  const int64_t cols = (N + 15) / 16;
+  const int kw = skinny_kw((int64_t)(units * cols), K), jw = 8 / kw;
+  const double blocks = units * (double)((cols + jw - 1) / jw);
+  const double load = blocks / cu_count();
+  const double per_piece[4] = {0.13, 0.19, 0.25, 0.32};
+  return 3.5 + (load < 1 ? 1 : 0.3 + 0.7 * load) * (double)((K + 127) / 128) * jw * per_piece[mt - 1];
+}
+
+// Units of `per` rows to expect of T rows in E groups of unknown sizes: rows
+// thrown at the groups at random hit E (1 - exp(-T / E)) of them, and each of
+// those loses half a unit.
+inline double expected_units(int64_t T, int64_t E, int64_t per) {
+  const double most = (double)most_units(T, E, per);
+  if (E == 1) return most;
+  const double live = E * (1.0 - exp(-(double)T / E));
+  const double u = (double)T / per + 0.5 * live;
+  return u < live ? live : (u < most ? u : most);
+}
+
+// The fastest tile for T rows in E groups, N columns, contraction K.
+inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
+  const double u128 = expected_units(T, E, 128), u256 = expected_units(T, E, 256);
+  const double n128 = (double)((N + 127) / 128), n256 = (double)((N + 255) / 256);
+  double us = 0;
+  int best = pick_of(u128 * n128, u128 * n256, u256 * n256, (double)K, &us);
+  for (int mt = 1; skinny && mt <= 4; ++mt) {
+    const double t = skinny_us(mt, expected_units(T, E, 16 * mt), N, K);
+    if (t < us) us = t, best = kTileSkinny16 + mt - 1;
+  }
+  return best;
+}
+
+// Tile of a rows launch.
 template <int LB>
 int rows_tile(const GemmArgs& g, const Groups& gr, const GroupStrides& s) {
   if (!rows_fast_ok<LB>(g, s)) return kTileV1;
   const int f = forced_tile();
-  if (f == kTileV1 || f == kTile128x128w8 || f == kTile256x256w8) return f;
-  return gr.T / gr.E >= 96 ? kTile256x256w8 : kTile128x128w8;
+  if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8) return f;
+  if (LB == kKContig && f >= kTileSkinny16) return f;
+  return pick_tile(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
 }
 
-// Tile of a contract launch: 256x256 unless dW is small (4096 x 1024 in 32
-// groups with the dX of 4093 rows: 171 us against 263 on 128x128).
+// Tile of a contract launch, by the mean group (4093 rows in 32 groups, dW of
+// 4096 x 1024: 82 us on 128x256, 88 on 256x256, 116 on 128x128).
 inline int contract_tile(const GemmArgs& g, const Groups& gr) {
   // one resource covers a group's rows of both operands: at most all T rows
   const bool ok = aligned16(g.a) && aligned16(g.b) && aligned16(g.c) && g.lda % 16 == 0 &&
@@ -67,9 +152,11 @@ inline int contract_tile(const GemmArgs& g, const Groups& gr) {
                   (g.Kc + 256) * g.ldb < (1LL << 31);
   if (!ok) return kTileV1;
   const int f = forced_tile();
-  if (f == kTileV1 || f == kTile128x128w8 || f == kTile256x256w8) return f;
-  const int64_t tiles = ((g.Mc + 255) / 256) * ((g.Nc + 255) / 256) * gr.E;
-  return 2 * tiles >= cu_count() ? kTile256x256w8 : kTile128x128w8;
+  if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8) return f;
+  const double m128 = (double)((g.Mc + 127) / 128) * gr.E, m256 = (double)((g.Mc + 255) / 256) * gr.E;
+  const double n128 = (double)((g.Nc + 127) / 128), n256 = (double)((g.Nc + 255) / 256);
+  double us = 0;
+  return pick_of(m128 * n128, m128 * n256, m256 * n256, (double)gr.T / gr.E, &us);
 }
 
 template <class Tile, bool I8>
@@ -83,11 +170,41 @@ void launch_rows_t(GemmArgs& g, const Groups& gr, const GroupStrides& s, const G
                      Tile::kLds, st, g, gr, s, side);
 }
 
+template <class S>
+void launch_skinny_groups(GemmArgs& g, const Groups& gr, const GroupStrides& s,
+                          const GroupedSide& side, hipStream_t st) {
+  const int64_t units = most_units(gr.T, gr.E, S::kBM);
+  const int64_t cols = (g.Nc + S::kWaveN - 1) / S::kWaveN;
+  const int kw = skinny_kw(units * cols, g.Kc), jw = 8 / kw;
+  g.tiles_n = (int32_t)((cols + jw - 1) / jw);
+  const int64_t most = (units * g.tiles_n + 7) & ~7LL;
+  hipLaunchKernelGGL((skinny_groups_kernel<S>), dim3((unsigned)most), dim3(S::kThreads),
+                     kw > 1 ? S::kLds : 0, st, g, gr, s, side, kw);
+}
+
+template <class S>
+void launch_skinny(GemmArgs& g, hipStream_t st) {
+  g.tiles_m = (int32_t)((g.Mc + S::kBM - 1) / S::kBM);
+  const int64_t cols = (g.Nc + S::kWaveN - 1) / S::kWaveN;
+  const int kw = skinny_kw(g.tiles_m * cols, g.Kc), jw = 8 / kw;
+  g.tiles_n = (int32_t)((cols + jw - 1) / jw);
+  hipLaunchKernelGGL((skinny_kernel<S>), dim3((unsigned)g.tiles_m * (unsigned)g.tiles_n),
+                     dim3(S::kThreads), kw > 1 ? S::kLds : 0, st, g, kw);
+}
+
 template <int LB, int FA, int FB>
 void launch_rows(GemmArgs& g, const Groups& gr, const GroupStrides& s, const GroupedSide& side,
                  int tile, hipStream_t st) {
+  if constexpr (LB == kKContig) {
+    if (tile == kTileSkinny16) return launch_skinny_groups<Skinny<FA, FB, 1, 1>>(g, gr, s, side, st);
+    if (tile == kTileSkinny32) return launch_skinny_groups<Skinny<FA, FB, 2, 1>>(g, gr, s, side, st);
+    if (tile == kTileSkinny48) return launch_skinny_groups<Skinny<FA, FB, 3, 1>>(g, gr, s, side, st);
+    if (tile == kTileSkinny64) return launch_skinny_groups<Skinny<FA, FB, 4, 1>>(g, gr, s, side, st);
+  }
   if (tile == kTile256x256w8)
     launch_rows_t<Tile256<kKContig, LB, FA, FB>, FA == kI8>(g, gr, s, side, st);
+  else if (tile == kTile128x256)
+    launch_rows_t<Tile128x256<kKContig, LB, FA, FB>, FA == kI8>(g, gr, s, side, st);
   else if (tile == kTile128x128w8)
     launch_rows_t<Tile128<kKContig, LB, FA, FB>, FA == kI8>(g, gr, s, side, st);
   else

@@ -31,15 +31,11 @@ bool i8_fast_ok(const GemmArgs& g) {
   return rows_fast_ok<kKContig>(g, s) && (g.Mc + 256) * g.lda < (1LL << 31);
 }
 
-// 256x256 when its tiles fill at least half the CUs, else 128x128 (4096
-// tokens, 4096 -> 11008: 196 us against 265; 33 tokens, 11008 -> 4096: 103
-// against 40).
 int i8_tile(const GemmArgs& g) {
   if (!i8_fast_ok(g)) return kTileV1;
   const int f = forced_tile();
-  if (f == kTileV1 || f == kTile128x128w8 || f == kTile256x256w8) return f;
-  const int64_t tiles256 = ((g.Mc + 255) / 256) * ((g.Nc + 255) / 256);
-  return 2 * tiles256 >= cu_count() ? kTile256x256w8 : kTile128x128w8;
+  if (f == kTileV1 || f >= kTile256x256w8) return f;
+  return pick_tile(g.Mc, 1, g.Nc, g.Kc, true);
 }
 
 void enqueue_rows(const void* x, int32_t dt, int64_t rows, int64_t cols, int8_t* q, float* scale,
@@ -136,7 +132,12 @@ int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_oper
   finish_grouped_args(g, GroupStrides{});
   if (M > 0 && N > 0) {
     const int tile = i8_tile(g);
-    if (tile == kTile256x256w8) launch_i8_t<Tile256<kKContig, kKContig, kI8, kI8>>(g, stream);
+    if (tile == kTileSkinny16) launch_skinny<Skinny<kI8, kI8, 1, 1>>(g, stream);
+    else if (tile == kTileSkinny32) launch_skinny<Skinny<kI8, kI8, 2, 1>>(g, stream);
+    else if (tile == kTileSkinny48) launch_skinny<Skinny<kI8, kI8, 3, 1>>(g, stream);
+    else if (tile == kTileSkinny64) launch_skinny<Skinny<kI8, kI8, 4, 1>>(g, stream);
+    else if (tile == kTile128x256) launch_i8_t<Tile128x256<kKContig, kKContig, kI8, kI8>>(g, stream);
+    else if (tile == kTile256x256w8) launch_i8_t<Tile256<kKContig, kKContig, kI8, kI8>>(g, stream);
     else if (tile == kTile128x128w8) launch_i8_t<Tile128<kKContig, kKContig, kI8, kI8>>(g, stream);
     else launch_i8_t<TileAny<kKContig, kKContig, kI8, kI8>>(g, stream);
   }

@@ -1,0 +1,187 @@
+// GEMM for few rows (decoding): C[i, j] = sum_k A(i, k) B(j, k), at most
+// 16 MT rows of A per tile, FP8 or 8-bit integers, both operands
+// k-contiguous; scales, bias and rounding as in the other GEMM kernels.
+//
+// With a handful of rows the matrix pipes idle and the time is that of
+// reading B once from HBM.  So there is no LDS staging and no barrier in the
+// K loop: every wave reads its own 16 NT rows of B straight into MFMA
+// operand registers, many 16-byte loads in flight, and A (small, in L2) the
+// same way.  The MFMA does not care which K position sits in which lane as
+// long as A and B agree, so a lane takes bytes [16 q, 16 q + 16) and
+// [64 + 16 q, 64 + 16 q + 16) of a 128-byte piece of K (q = lane / 16): each
+// load instruction covers 64 contiguous bytes of 16 rows and two of them
+// whole 128-byte lines.
+//
+// A block has 8 waves.  KW of them share a tile column and split K (pieces
+// of 128 bytes dealt round-robin, so that together they read whole rows),
+// 8 / KW tile columns stand beside each other.  KW is chosen so that the
+// waves fill the chip: 1 when there are columns enough, up to 8 for a narrow
+// B.  The KW partial sums meet in LDS and are added in wave order (int32:
+// exactly), so results do not depend on timing.
+#pragma once
+
+#include "fp8l_gemm3.hpp"
+#include "fp8l_grouped.hpp"
+
+namespace fp8l {
+
+// K pieces of 128 bytes loaded at once.
+template <int MT>
+constexpr int skinny_unroll() { return MT == 1 ? 4 : 2; }
+
+template <int FA, int FB, int MT, int NT>
+struct Skinny {
+  static constexpr int kBM = 16 * MT, kWaveN = 16 * NT, kThreads = 512, kU = skinny_unroll<MT>();
+  static constexpr int kLds = 8 * MT * NT * 1024;
+  static constexpr bool I8 = FA == kI8;
+
+  // Scales and bias of this lane's four outputs of a 16x16 fragment (row
+  // `row`, columns j .. j + 3) as loaded: nothing is computed from them
+  // before the store, so nothing waits for them while the operands load.
+  struct Epi {
+    float sa, sb[4];
+    uint16_t b[4];
+  };
+  FP8L_DEV static Epi epi(const GemmArgs& g, int row, int64_t j) {
+    Epi e;
+    e.sa = g.scale_a[I8 && row < g.Mc ? row : 0];
+    const int64_t j0 = j < g.Nc ? j : 0;  // Nc is a multiple of 8: all four columns or none
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      e.sb[t] = g.scale_b[I8 ? j0 + t : 0];
+      e.b[t] = g.bias_kind != kBiasNone ? reinterpret_cast<const uint16_t*>(g.bias)[j0 + t] : 0;
+    }
+    return e;
+  }
+  FP8L_DEV static void store(const GemmArgs& g, int row, int64_t j, v4f acc, const Epi& e) {
+    if (row >= g.Mc || j >= g.Nc) return;
+    const float isa = 1.0f / e.sa;
+    float v[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float c = isa * (1.0f / e.sb[t]);
+      const float b = I8 && g.out_f16 ? f16_to_f32(e.b[t]) : bf16_to_f32(e.b[t]);
+      v[t] = I8 ? i8_value(acc[t], c, b) : __builtin_fmaf(acc[t], c, b);
+    }
+    uint2 w;
+    if (I8 && g.out_f16)
+      w = make_uint2(f32_to_f16(v[0]) | (f32_to_f16(v[1]) << 16),
+                     f32_to_f16(v[2]) | (f32_to_f16(v[3]) << 16));
+    else
+      w = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+    *reinterpret_cast<uint2*>(g.c + row * g.ldc + j) = w;
+  }
+
+  FP8L_DEV static v8i load2(__amdgpu_buffer_rsrc_t rs, uint32_t lo, uint32_t hi) {
+    const v4i a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, lo, 0, 0));
+    const v4i b = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, hi, 0, 0));
+    return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+
+  // Tile column tn (of 16 NT 8 / KW columns) of the rows g.a .. (g.Mc of them).
+  FP8L_DEV static void run(const GemmArgs& g, int tn, int KW, uint8_t* smem) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
+    const int64_t jb = (int64_t)tn * JW * kWaveN;  // the block's first column
+    const int64_t j0 = jb + jw * kWaveN;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.Mc * g.lda));
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b, (uint32_t)(g.Nc * g.ldb));
+    // row offsets; rows past the end lie past the buffer and read as zeros
+    uint32_t oa[MT], ob[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) oa[m] = (uint32_t)((16 * m + r) * g.lda);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ob[n] = (uint32_t)((j0 + 16 * n + r) * g.ldb);
+    v4f acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    // the epilogue's operands, in flight with the first pieces (with KW > 1
+    // another wave may finish the fragment; it then finds them in cache)
+    Epi e0 = epi(g, r, j0 + 4 * q);
+    const uint32_t K = (uint32_t)g.Kc;
+    const uint32_t pieces = (K + 127) / 128;
+    for (uint32_t p = kw; p < pieces; p += KW * kU) {
+      v8i fa[kU][MT], fb[kU][NT];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t k0 = (p + u * KW) * 128 + 16 * q, k1 = k0 + 64;
+        // bytes past K (the next row's) and pieces past the last: zeros
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          fb[u][n] = load2(rb, k0 < K ? ob[n] + k0 : 0x80000000u, k1 < K ? ob[n] + k1 : 0x80000000u);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          fa[u][m] = load2(ra, k0 < K ? oa[m] + k0 : 0x80000000u, k1 < K ? oa[m] + k1 : 0x80000000u);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[m][n] = mma_16x16<FA, FB>(fb[u][n], fa[u][m], acc[m][n]);
+    }
+    if (KW == 1) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m + n > 0) e0 = epi(g, 16 * m + r, j0 + 16 * n + 4 * q);
+          store(g, 16 * m + r, j0 + 16 * n + 4 * q, acc[m][n], e0);
+        }
+      return;
+    }
+    // partial sums: [wave][fragment][lane] x 16 bytes
+    v4f* const part = reinterpret_cast<v4f*>(smem);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) part[(wave * MT * NT + n * MT + m) * 64 + lane] = acc[m][n];
+    __syncthreads();
+    for (int f = wave; f < JW * MT * NT; f += 8) {
+      const int fj = f / (MT * NT), fn = f % (MT * NT) / MT, fm = f % MT;
+      const v4f* src = part + (fj * KW * MT * NT + f % (MT * NT)) * 64 + lane;
+      v4f s = src[0];
+      for (int w = 1; w < KW; ++w) {
+        const v4f o = src[w * MT * NT * 64];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[t] = add_sums<I8>(s[t], o[t]);
+      }
+      const int row = 16 * fm + r;
+      const int64_t j = jb + fj * kWaveN + 16 * fn + 4 * q;
+      store(g, row, j, s, epi(g, row, j));
+    }
+  }
+};
+
+// Dense: block = (tile column, tile row); consecutive blocks take the tile
+// rows of one column first, so a B with several tile rows is reread from L2.
+template <class S>
+__global__ __launch_bounds__(512, 4) void skinny_kernel(GemmArgs g, int KW) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_skinny[];
+  const int tm = blockIdx.x % g.tiles_m, tn = blockIdx.x / g.tiles_m;
+  const int64_t row = (int64_t)tm * S::kBM;
+  g.a += row * g.lda;
+  g.c += row * g.ldc;
+  g.Mc = min<int64_t>(g.Mc - row, S::kBM);
+  if (S::I8) g.scale_a += row;
+  S::run(g, tn, KW, smem_skinny);
+}
+
+// Groups: as grouped_rows_kernel, in units of 16 MT rows.
+template <class S>
+__global__ __launch_bounds__(512, 4) void skinny_groups_kernel(GemmArgs g, Groups gr, GroupStrides st,
+                                                            GroupedSide side, int KW) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_skinny[];
+  int tm, tn;
+  const GroupSpan sp = rows_work(gr, S::kBM, g.tiles_n, tm, tn);
+  if (sp.e >= 0) {
+    move_to_rows<S::I8>(g, st, sp, tm, S::kBM);
+    S::run(g, tn, KW, smem_skinny);
+  }
+  grouped_side(side);
+}
+
+}  // namespace fp8l

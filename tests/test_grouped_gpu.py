@@ -17,7 +17,8 @@ from tests.rows_util import (GROUPS, bf16, check_groups, offsets_dev, offsets_of
 
 pytestmark = pytest.mark.gpu
 
-TILES = ["v1", "128x128w8", "256x256w8", None]
+TILES = ["v1", "128x128w8", "256x256w8", "128x256", "skinny16", "skinny32",
+         "skinny48", "skinny64", None]
 SENTINEL = 7.0
 
 

@@ -13,7 +13,8 @@ from tests.rows_util import GROUPS, bf16, check_i8, offsets_dev, offsets_of, out
 
 pytestmark = pytest.mark.gpu
 
-TILES = ["v1", "128x128w8", "256x256w8", None]
+TILES = ["v1", "128x128w8", "256x256w8", "128x256", "skinny16", "skinny32",
+         "skinny48", "skinny64", None]
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 
 
