@@ -163,6 +163,47 @@ FP8L_DEV int swz_k(int r) { return (r ^ (r >> 3)) & 7; }
 // consecutive k rows of one chunk, and groups 0/1 sit 32 rows apart.
 FP8L_DEV int swz_x(int kk) { return ((kk >> 1) & 3) | (((kk >> 5) & 1) << 2); }
 
+// 16 bytes at any address: the aligned words that hold them, shifted
+// together, bytes from n (0..16) on zero.
+FP8L_DEV uint4 join16(uint4 f, uint32_t e, const uint8_t* p, int n) {
+  const uint32_t a = (uint32_t)(uintptr_t)p & 3u;
+  const uint32_t w[5] = {f.x, f.y, f.z, f.w, e};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int left = min(max(n - 4 * i, 0), 4);
+    const uint32_t keep = left == 4 ? ~0u : (1u << (8 * left)) - 1u;
+    o[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], a) & keep;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The five words from p's aligned word on, without a branch, so that many
+// such loads are in flight at once.  Only where any_window holds.
+struct __attribute__((aligned(4))) Words4 { uint32_t v[4]; };
+FP8L_DEV void load_words(const uint8_t* p, uint4& f, uint32_t& e) {
+  const uint8_t* q = p - ((uint32_t)(uintptr_t)p & 3u);
+  const Words4 w = *reinterpret_cast<const Words4*>(q);
+  f = make_uint4(w.v[0], w.v[1], w.v[2], w.v[3]);
+  e = *reinterpret_cast<const uint32_t*>(q + 16);
+}
+// Those 20 bytes lie inside the words of an operand that ends at end.
+FP8L_DEV bool any_window(const uint8_t* p, const uint8_t* end) {
+  return (((uintptr_t)p & ~(uintptr_t)3) + 20) <= (((uintptr_t)end + 3) & ~(uintptr_t)3);
+}
+
+// The same 16 bytes near the operand's end: every word read holds at least
+// one valid byte (n >= 1).
+FP8L_DEV uint4 load16_any(const uint8_t* p, int n) {
+  const uint32_t a = (uint32_t)(uintptr_t)p & 3u;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p - a);
+  const int last = ((int)a + n - 1) >> 2;
+  uint32_t w[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = q[min(i, last)];
+  return join16(make_uint4(w[0], w[1], w[2], w[3]), w[4], p, n);
+}
+
 // One 16-byte chunk of an operand tile: outer index o (tile row), inner
 // byte offset in (16 bytes).  Out-of-range bytes read as zero.
 FP8L_DEV uint4 load_chunk(const uint8_t* p, int64_t ld, int64_t o, int64_t olim, int64_t in,
@@ -171,42 +212,90 @@ FP8L_DEV uint4 load_chunk(const uint8_t* p, int64_t ld, int64_t o, int64_t olim,
   if (o >= olim || in >= inlim) return r;
   const uint8_t* q = p + o * ld + in;
   if (vec && in + 16 <= inlim) return *reinterpret_cast<const uint4*>(q);
-  uint32_t w[4] = {0, 0, 0, 0};
-  for (int j = 0; j < 16; ++j)
-    if (in + j < inlim) w[j >> 2] |= (uint32_t)q[j] << (8 * (j & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return load16_any(q, (int)min<int64_t>(16, inlim - in));
 }
 
-// Load this thread's 4 chunks of an operand tile (128 tile rows x 128
-// bytes).  Thread t owns chunk t&7 of tile rows (t>>3) + 32*i.
+// This thread's 4 chunks of an operand tile (128 tile rows x 128 bytes).
+// Thread t owns chunk t&7 of tile rows (t>>3) + 32*i.
 // k-contiguous: tile row = C index (rbase + r), bytes = k0 + 16c.
 // crosswise:    tile row = k0 + r,            bytes = rbase + 16c.
+// load() issues the loads, store() puts the chunks into LDS; between the two
+// an unaligned operand is held as its raw words, so that its loads are in
+// flight together and nothing waits for them before the MFMAs in between.
 template <int L>
-FP8L_DEV void load_tile(const uint8_t* p, int64_t ld, int64_t rbase, int64_t rlim, int64_t k0,
-                        int64_t klim, int vec, uint4 v[4]) {
-  const int t = threadIdx.x;
-  const int c = t & 7;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 3) + 32 * i;
-    if constexpr (L == kKContig)
-      v[i] = load_chunk(p, ld, rbase + r, rlim, k0 + 16 * c, klim, vec);
-    else
-      v[i] = load_chunk(p, ld, k0 + r, klim, rbase + 16 * c, rlim, vec);
-  }
-}
+struct TileChunks {
+  uint4 v[4];
+  uint32_t e[4];
+  bool raw;
 
-template <int L>
-FP8L_DEV void store_tile(uint8_t* s, const uint4 v[4]) {
-  const int t = threadIdx.x;
-  const int c = t & 7;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 3) + 32 * i;
-    const int pc = (L == kKContig) ? (c ^ swz_k(r)) : (c ^ swz_x(r));
-    *reinterpret_cast<uint4*>(s + r * 128 + pc * 16) = v[i];
+  // chunk i's outer index and inner offset
+  FP8L_DEV static void place(int i, int64_t rbase, int64_t k0, int64_t& o, int64_t& in) {
+    const int t = threadIdx.x, c = t & 7, r = (t >> 3) + 32 * i;
+    o = (L == kKContig) ? rbase + r : k0 + r;
+    in = (L == kKContig) ? k0 + 16 * c : rbase + 16 * c;
   }
-}
+  // its first byte and how many are valid (none: the operand's first byte)
+  FP8L_DEV static const uint8_t* where(const uint8_t* p, int64_t ld, int64_t o, int64_t olim,
+                                       int64_t in, int64_t inlim, int& n) {
+    const bool ok = o < olim && in < inlim;
+    n = ok ? (int)min<int64_t>(16, inlim - in) : 0;
+    return ok ? p + o * ld + in : p;
+  }
+
+  FP8L_DEV void load(const uint8_t* p, int64_t ld, int64_t rbase, int64_t rlim, int64_t k0,
+                     int64_t klim, int vec) {
+    const int64_t olim = (L == kKContig) ? rlim : klim, inlim = (L == kKContig) ? klim : rlim;
+    raw = false;
+    if (!vec) {
+      const uint8_t* const end = p + (olim - 1) * ld + inlim;
+      bool ok = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int64_t o, in;
+        int n;
+        place(i, rbase, k0, o, in);
+        ok = ok && any_window(where(p, ld, o, olim, in, inlim, n), end);
+      }
+      raw = __all(ok);
+    }
+    if (raw) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int64_t o, in;
+        int n;
+        place(i, rbase, k0, o, in);
+        load_words(where(p, ld, o, olim, in, inlim, n), v[i], e[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int64_t o, in;
+        place(i, rbase, k0, o, in);
+        v[i] = load_chunk(p, ld, o, olim, in, inlim, vec);
+      }
+    }
+  }
+
+  // the arguments of the load() before it
+  FP8L_DEV void store(uint8_t* s, const uint8_t* p, int64_t ld, int64_t rbase, int64_t rlim,
+                      int64_t k0, int64_t klim) {
+    const int t = threadIdx.x, c = t & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (t >> 3) + 32 * i;
+      if (raw) {
+        int64_t o, in;
+        int n;
+        place(i, rbase, k0, o, in);
+        const uint8_t* const a = where(p, ld, o, (L == kKContig) ? rlim : klim, in,
+                                       (L == kKContig) ? klim : rlim, n);
+        v[i] = join16(v[i], e[i], a, n);
+      }
+      const int pc = (L == kKContig) ? (c ^ swz_k(r)) : (c ^ swz_x(r));
+      *reinterpret_cast<uint4*>(s + r * 128 + pc * 16) = v[i];
+    }
+  }
+};
 
 // MFMA input fragment (16 tile-indices x 128 k) for lane l: index f0 + (l&15),
 // k = 32*(l>>4) + byte.
@@ -358,21 +447,22 @@ FP8L_DEV void gemm_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem_) {
     for (int b = 0; b < 4; ++b) acc[a][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   const int nk = (int)((g.Kc + kBK - 1) / kBK);
-  uint4 ra[4], rb[4];
+  TileChunks<LA> ra;
+  TileChunks<LB> rb;
   if (nk > 0) {
-    load_tile<LA>(g.a, g.lda, i0, g.Mc, 0, g.Kc, g.a_vec, ra);
-    load_tile<LB>(g.b, g.ldb, j0, g.Nc, 0, g.Kc, g.b_vec, rb);
-    store_tile<LA>(smem[0][0], ra);
-    store_tile<LB>(smem[0][1], rb);
+    ra.load(g.a, g.lda, i0, g.Mc, 0, g.Kc, g.a_vec);
+    rb.load(g.b, g.ldb, j0, g.Nc, 0, g.Kc, g.b_vec);
+    ra.store(smem[0][0], g.a, g.lda, i0, g.Mc, 0, g.Kc);
+    rb.store(smem[0][1], g.b, g.ldb, j0, g.Nc, 0, g.Kc);
   }
   __syncthreads();
   for (int kt = 0; kt < nk; ++kt) {
     const int cur = kt & 1;
     const bool more = kt + 1 < nk;
+    const int64_t k1 = (int64_t)(kt + 1) * kBK;
     if (more) {
-      const int64_t k1 = (int64_t)(kt + 1) * kBK;
-      load_tile<LA>(g.a, g.lda, i0, g.Mc, k1, g.Kc, g.a_vec, ra);
-      load_tile<LB>(g.b, g.ldb, j0, g.Nc, k1, g.Kc, g.b_vec, rb);
+      ra.load(g.a, g.lda, i0, g.Mc, k1, g.Kc, g.a_vec);
+      rb.load(g.b, g.ldb, j0, g.Nc, k1, g.Kc, g.b_vec);
     }
     v8i fa[4], fb[4];
 #pragma unroll
@@ -385,8 +475,8 @@ FP8L_DEV void gemm_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem_) {
       for (int b = 0; b < 4; ++b)
         acc[a][b] = mma_16x16<FA, FB>(fb[b], fa[a], acc[a][b]);
     if (more) {
-      store_tile<LA>(smem[cur ^ 1][0], ra);
-      store_tile<LB>(smem[cur ^ 1][1], rb);
+      ra.store(smem[cur ^ 1][0], g.a, g.lda, i0, g.Mc, k1, g.Kc);
+      rb.store(smem[cur ^ 1][1], g.b, g.ldb, j0, g.Nc, k1, g.Kc);
     }
     __syncthreads();
   }

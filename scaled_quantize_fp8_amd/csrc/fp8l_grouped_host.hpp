@@ -73,12 +73,12 @@ inline int skinny_kw(int64_t waves, int64_t K) {
 // K = 1536 / 4096 / 11008:
 //   128x128, one block per CU:    13 / 25 /  55 us
 //   128x256, one block per CU:    20 / 40 / 100, two: 37 / 88 / 223
-//   256x256:                      29 / 58 / 135
+//   256x256:                      32 / 64 / 150
 inline double tile_us(int tile, double tiles, double K) {
   const double cus = cu_count();
   switch (tile) {
     case kTile128x128w8: return 3 + ceil(tiles / cus) * (4 + K * 0.0044);
-    case kTile256x256w8: return 3 + ceil(tiles / cus) * (8 + K * 0.0125);
+    case kTile256x256w8: return 3 + ceil(tiles / cus) * (10 + K * 0.0125);
     default: {  // kTile128x256
       if (tiles <= cus) return 8 + K * 0.0080;
       const double rounds = tiles / (2 * cus) + 0.25;
@@ -133,11 +133,29 @@ inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   return best;
 }
 
+// The same where the pipelined tiles cannot run (odd sizes, unaligned
+// pointers): the general tile (two blocks per CU; 1.5 us per 128 of K alone,
+// 2.7 for two), or the skinny kernel's form for any alignment, whose pieces
+// take about half as long again.
+inline int pick_any(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
+  const double cus = cu_count(), steps = (double)((K + 127) / 128);
+  const double tiles = expected_units(T, E, 128) * (double)((N + 127) / 128);
+  double us = 5 + (tiles <= cus ? 1.5 : 2.7 * (tiles / (2 * cus) + 0.5)) * steps;
+  int best = kTileV1;
+  const int mts[3] = {1, 2, 4}, ids[3] = {kTileSkinny16Any, kTileSkinny32Any, kTileSkinny64Any};
+  for (int i = 0; skinny && i < 3; ++i) {
+    const double t = 1.5 * skinny_us(mts[i], expected_units(T, E, 16 * mts[i]), N, K);
+    if (t < us) us = t, best = ids[i];
+  }
+  return best;
+}
+
 // Tile of a rows launch.
 template <int LB>
 int rows_tile(const GemmArgs& g, const Groups& gr, const GroupStrides& s) {
-  if (!rows_fast_ok<LB>(g, s)) return kTileV1;
   const int f = forced_tile();
+  if (!rows_fast_ok<LB>(g, s))
+    return f == kTileV1 ? f : pick_any(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
   if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8) return f;
   if (LB == kKContig && f >= kTileSkinny16) return f;
   return pick_tile(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
@@ -196,6 +214,12 @@ template <int LB, int FA, int FB>
 void launch_rows(GemmArgs& g, const Groups& gr, const GroupStrides& s, const GroupedSide& side,
                  int tile, hipStream_t st) {
   if constexpr (LB == kKContig) {
+    if (tile == kTileSkinny16Any)
+      return launch_skinny_groups<Skinny<FA, FB, 1, 1, true>>(g, gr, s, side, st);
+    if (tile == kTileSkinny32Any)
+      return launch_skinny_groups<Skinny<FA, FB, 2, 1, true>>(g, gr, s, side, st);
+    if (tile == kTileSkinny64Any)
+      return launch_skinny_groups<Skinny<FA, FB, 4, 1, true>>(g, gr, s, side, st);
     if (tile == kTileSkinny16) return launch_skinny_groups<Skinny<FA, FB, 1, 1>>(g, gr, s, side, st);
     if (tile == kTileSkinny32) return launch_skinny_groups<Skinny<FA, FB, 2, 1>>(g, gr, s, side, st);
     if (tile == kTileSkinny48) return launch_skinny_groups<Skinny<FA, FB, 3, 1>>(g, gr, s, side, st);

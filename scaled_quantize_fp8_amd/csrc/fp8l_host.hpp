@@ -131,7 +131,8 @@ inline int hip_status() { return hipGetLastError() == hipSuccess ? FP8_OK : FP8_
 
 enum { kTileAuto = 0, kTile256x256, kTile256x128, kTile128x128, kTileV1, kTile256x256w8, kTile128x128w8,
        kTile128x256,
-       kTileSkinny16, kTileSkinny32, kTileSkinny48, kTileSkinny64 };
+       kTileSkinny16, kTileSkinny32, kTileSkinny48, kTileSkinny64,
+       kTileSkinny16Any, kTileSkinny32Any, kTileSkinny64Any };
 int forced_tile();
 
 // Defined in fp8l_api.hip.

@@ -32,8 +32,8 @@ bool i8_fast_ok(const GemmArgs& g) {
 }
 
 int i8_tile(const GemmArgs& g) {
-  if (!i8_fast_ok(g)) return kTileV1;
   const int f = forced_tile();
+  if (!i8_fast_ok(g)) return f == kTileV1 ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
   if (f == kTileV1 || f >= kTile256x256w8) return f;
   return pick_tile(g.Mc, 1, g.Nc, g.Kc, true);
 }
@@ -132,7 +132,10 @@ int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_oper
   finish_grouped_args(g, GroupStrides{});
   if (M > 0 && N > 0) {
     const int tile = i8_tile(g);
-    if (tile == kTileSkinny16) launch_skinny<Skinny<kI8, kI8, 1, 1>>(g, stream);
+    if (tile == kTileSkinny16Any) launch_skinny<Skinny<kI8, kI8, 1, 1, true>>(g, stream);
+    else if (tile == kTileSkinny32Any) launch_skinny<Skinny<kI8, kI8, 2, 1, true>>(g, stream);
+    else if (tile == kTileSkinny64Any) launch_skinny<Skinny<kI8, kI8, 4, 1, true>>(g, stream);
+    else if (tile == kTileSkinny16) launch_skinny<Skinny<kI8, kI8, 1, 1>>(g, stream);
     else if (tile == kTileSkinny32) launch_skinny<Skinny<kI8, kI8, 2, 1>>(g, stream);
     else if (tile == kTileSkinny48) launch_skinny<Skinny<kI8, kI8, 3, 1>>(g, stream);
     else if (tile == kTileSkinny64) launch_skinny<Skinny<kI8, kI8, 4, 1>>(g, stream);

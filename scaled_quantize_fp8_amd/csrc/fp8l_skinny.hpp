@@ -26,14 +26,15 @@
 namespace fp8l {
 
 // K pieces of 128 bytes loaded at once.
-template <int MT>
-constexpr int skinny_unroll() { return MT == 1 ? 4 : 2; }
+template <int MT, bool I8, bool ANY>
+constexpr int skinny_unroll() { return MT == 1 ? 4 : ((MT == 4 || ANY) && (I8 || (ANY && MT == 4)) ? 1 : 2); }
 
-template <int FA, int FB, int MT, int NT>
+// ANY: rows of any alignment and sizes of any kind, through load16_any.
+template <int FA, int FB, int MT, int NT, bool ANY = false>
 struct Skinny {
-  static constexpr int kBM = 16 * MT, kWaveN = 16 * NT, kThreads = 512, kU = skinny_unroll<MT>();
-  static constexpr int kLds = 8 * MT * NT * 1024;
+  static constexpr int kBM = 16 * MT, kWaveN = 16 * NT, kThreads = 512, kLds = 8 * MT * NT * 1024;
   static constexpr bool I8 = FA == kI8;
+  static constexpr int kU = skinny_unroll<MT, I8, ANY>();
 
   // Scales and bias of this lane's four outputs of a 16x16 fragment (row
   // `row`, columns j .. j + 3) as loaded: nothing is computed from them
@@ -45,11 +46,12 @@ struct Skinny {
   FP8L_DEV static Epi epi(const GemmArgs& g, int row, int64_t j) {
     Epi e;
     e.sa = g.scale_a[I8 && row < g.Mc ? row : 0];
-    const int64_t j0 = j < g.Nc ? j : 0;  // Nc is a multiple of 8: all four columns or none
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      e.sb[t] = g.scale_b[I8 ? j0 + t : 0];
-      e.b[t] = g.bias_kind != kBiasNone ? reinterpret_cast<const uint16_t*>(g.bias)[j0 + t] : 0;
+      // Nc a multiple of 8: all four columns or none
+      const int64_t jt = j + (ANY ? t : 0) < g.Nc ? j + t : t * !ANY;
+      e.sb[t] = g.scale_b[I8 ? jt : 0];
+      e.b[t] = g.bias_kind != kBiasNone ? reinterpret_cast<const uint16_t*>(g.bias)[jt] : 0;
     }
     return e;
   }
@@ -69,7 +71,69 @@ struct Skinny {
                      f32_to_f16(v[2]) | (f32_to_f16(v[3]) << 16));
     else
       w = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
-    *reinterpret_cast<uint2*>(g.c + row * g.ldc + j) = w;
+    uint16_t* const dst = g.c + row * g.ldc + j;
+    if (!ANY || (g.c_vec && j + 4 <= g.Nc)) {  // Nc a multiple of 8: all four columns or none
+      *reinterpret_cast<uint2*>(dst) = w;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (j + t < g.Nc) dst[t] = (uint16_t)((t < 2 ? w.x : w.y) >> (16 * (t & 1)));
+    }
+  }
+
+  // ANY: bytes [k, k + 16) of row i of p, zeros past K and the rows: the
+  // first byte (the operand's where none is valid) and their number.
+  FP8L_DEV static const uint8_t* where(const uint8_t* p, int64_t ld, int64_t i, int64_t rows,
+                                       int64_t k, int64_t K, int& n) {
+    const bool ok = i < rows && k < K;
+    n = ok ? (int)min<int64_t>(16, K - k) : 0;
+    return ok ? p + i * ld + k : p;
+  }
+  // One operand's F fragments of the pieces at k[0 .. 2 kU): all loads in
+  // flight together, unless some lane's words reach past the operand's end.
+  template <int F>
+  FP8L_DEV static void load_any(const uint8_t* p, int64_t ld, int64_t i0, int64_t rows, int64_t K,
+                                const int64_t (&k)[2 * kU], v8i (&out)[kU][F]) {
+    const uint8_t* const end = p + (rows - 1) * ld + K;
+    bool ok = true;
+    int n;
+#pragma unroll
+    for (int h = 0; h < 2 * kU; ++h)
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        ok = ok && any_window(where(p, ld, i0 + 16 * f, rows, k[h], K, n), end);
+    uint4 v[2 * kU][F];
+    if (__all(ok)) {
+      uint32_t e[2 * kU][F];
+#pragma unroll
+      for (int h = 0; h < 2 * kU; ++h)
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          load_words(where(p, ld, i0 + 16 * f, rows, k[h], K, n), v[h][f], e[h][f]);
+#pragma unroll
+      for (int h = 0; h < 2 * kU; ++h)
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const uint8_t* const a = where(p, ld, i0 + 16 * f, rows, k[h], K, n);
+          v[h][f] = join16(v[h][f], e[h][f], a, n);
+        }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2 * kU; ++h)
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const uint8_t* const a = where(p, ld, i0 + 16 * f, rows, k[h], K, n);
+          v[h][f] = n ? load16_any(a, n) : make_uint4(0, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const uint4 a = v[2 * u][f], b = v[2 * u + 1][f];
+        out[u][f] = v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w,
+                        (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+      }
   }
 
   FP8L_DEV static v8i load2(__amdgpu_buffer_rsrc_t rs, uint32_t lo, uint32_t hi) {
@@ -105,16 +169,27 @@ struct Skinny {
     const uint32_t pieces = (K + 127) / 128;
     for (uint32_t p = kw; p < pieces; p += KW * kU) {
       v8i fa[kU][MT], fb[kU][NT];
+      if constexpr (ANY) {
+        int64_t k[2 * kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const uint32_t k0 = (p + u * KW) * 128 + 16 * q, k1 = k0 + 64;
-        // bytes past K (the next row's) and pieces past the last: zeros
+        for (int u = 0; u < kU; ++u) {
+          k[2 * u] = (int64_t)(p + u * KW) * 128 + 16 * q;
+          k[2 * u + 1] = k[2 * u] + 64;
+        }
+        load_any<NT>(g.b, g.ldb, j0 + r, g.Nc, g.Kc, k, fb);
+        load_any<MT>(g.a, g.lda, r, g.Mc, g.Kc, k, fa);
+      } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          fb[u][n] = load2(rb, k0 < K ? ob[n] + k0 : 0x80000000u, k1 < K ? ob[n] + k1 : 0x80000000u);
+        for (int u = 0; u < kU; ++u) {
+          const uint32_t k0 = (p + u * KW) * 128 + 16 * q, k1 = k0 + 64;
+          // bytes past K (the next row's) and pieces past the last: zeros
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          fa[u][m] = load2(ra, k0 < K ? oa[m] + k0 : 0x80000000u, k1 < K ? oa[m] + k1 : 0x80000000u);
+          for (int n = 0; n < NT; ++n)
+            fb[u][n] = load2(rb, k0 < K ? ob[n] + k0 : 0x80000000u, k1 < K ? ob[n] + k1 : 0x80000000u);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            fa[u][m] = load2(ra, k0 < K ? oa[m] + k0 : 0x80000000u, k1 < K ? oa[m] + k1 : 0x80000000u);
+        }
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u)
