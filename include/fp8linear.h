@@ -505,7 +505,8 @@ int fp8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
  *   g        high precision (quantized here with ring_g, or dynamically, over
  *            rows [0, offsets[E])) or fp8 codes of fmt_g.
  *   db_ws    workspace of fp8_grouped_db_workspace_bytes(T, E, N); required
- *            for db when T > 0.  Its contents need not survive the call.
+ *            for db of a high-precision g when T > 0 (its sums are taken in
+ *            the quantize's pass).  Its contents need not survive the call.
  *   w_scales number of scales of w8: 1 or E.
  */
 int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,

@@ -10,28 +10,14 @@
 namespace fp8l {
 namespace {
 
-// db[e][n] = bf16(mult * sum over e's chunks of ws[chunk][n]), one block per
-// group and 64 columns: wave w adds chunks w, w + 4, .., then the four sums
-// meet in wave order.  A group without rows gets 0.  most: chunks in ws (what
-// offsets that break the contract count beyond it is not read).
-__global__ __launch_bounds__(256) void grouped_db_kernel(const float* ws, int most, Groups gr,
-                                                         int64_t N, const float* scale,
-                                                         uint16_t* db) {
-  __shared__ float sh[4][64];
-  const GroupSpan sp = group_span(gr, kColRowsPerChunk, blockIdx.y);
-  const int chunks = min(units_of(sp.end - sp.start, kColRowsPerChunk), most - sp.before);
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (n < N)
-    for (int c = w; c < chunks; c += 4) s += ws[(int64_t)(sp.before + c) * N + n];
-  sh[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && n < N) {
-    float t = sh[0][lane] + sh[1][lane] + sh[2][lane] + sh[3][lane];
-    if (scale) t *= 1.0f / *scale;
-    db[(int64_t)blockIdx.y * N + n] = (uint16_t)f32_to_bf16(t);
-  }
+__global__ __launch_bounds__(256) void grouped_db_kernel(DbArgs a, Groups gr) {
+  __shared__ float sh[kDbLds / 4];
+  db_block(a, gr, blockIdx.x, sh);
+}
+
+int db_blocks(const DbArgs& a, const Groups& gr) {
+  const int width = a.ws ? 64 : 256;
+  return a.db ? (int)((a.N + width - 1) / width) * gr.E : 0;
 }
 
 template <class Tile>
@@ -106,7 +92,9 @@ bool enqueue_groupsum(const fp8_operand_t& x, int64_t T, int64_t N, int32_t fmt,
     a.hist = reinterpret_cast<float*>(reinterpret_cast<char*>(ring->dev) + sizeof(RingHdr));
     a.hist_len = ring->hist_len;
   }
-  if (!ring || !ring->seeded) enqueue_amax(x.data, x.dtype, n, ring, amax_out, limit, st);
+  a.limit = limit;
+  const bool local = !ring && n <= kLocalMost;
+  if (!local && (!ring || !ring->seeded)) enqueue_amax(x.data, x.dtype, n, ring, amax_out, limit, st);
   const int strips = (int)((N + kColStrip - 1) / kColStrip);
   const dim3 grid((unsigned)(most_units(T, gr.E, kColRowsPerChunk) * strips));
   auto run = [&](auto in, auto f, auto mode) {
@@ -115,7 +103,8 @@ bool enqueue_groupsum(const fp8_operand_t& x, int64_t T, int64_t N, int32_t fmt,
                        grid, dim3(kQThreads), 0, st, a, gr, strips);
   };
   auto by_mode = [&](auto in, auto f) {
-    if (!ring) run(in, f, std::integral_constant<int, kScaleDyn>{});
+    if (local) run(in, f, std::integral_constant<int, kScaleLocal>{});
+    else if (!ring) run(in, f, std::integral_constant<int, kScaleDyn>{});
     else if (!ring->seeded) run(in, f, std::integral_constant<int, kScaleSeed>{});
     else if (defer) run(in, f, std::integral_constant<int, kScaleDefer>{});
     else run(in, f, std::integral_constant<int, kScaleRing>{});
@@ -131,17 +120,46 @@ bool enqueue_groupsum(const fp8_operand_t& x, int64_t T, int64_t N, int32_t fmt,
   return defer;
 }
 
-void enqueue_groupsum_fp8(const uint8_t* g8, int64_t T, int64_t N, int32_t fmt, float* ws,
-                          const Groups& gr, hipStream_t st) {
-  const int strips = (int)((N + kColStrip - 1) / kColStrip);
-  const dim3 grid((unsigned)(most_units(T, gr.E, kColRowsPerChunk) * strips));
-  const int vec = ((uintptr_t)g8 & 7u) == 0 && N % 8 == 0;
-  if (fmt == FP8_E4M3)
-    hipLaunchKernelGGL(groupsum_fp8_kernel<kE4M3>, grid, dim3(kQThreads), 0, st, g8, N, gr, strips,
-                       vec, ws);
-  else
-    hipLaunchKernelGGL(groupsum_fp8_kernel<kE5M2>, grid, dim3(kQThreads), 0, st, g8, N, gr, strips,
-                       vec, ws);
+// dX, dW and db in one launch with one tile shape, where both GEMMs can take
+// a pipelined tile; false: the caller launches them one by one.
+template <class TX, class TW>
+void launch_bwd_t(GemmArgs& gx, GemmArgs& gw, const Groups& gr, const GroupStrides& sx,
+                  const GroupStrides& sw, const GroupedSide& side, const DbArgs& db,
+                  hipStream_t st) {
+  static std::atomic<bool> lds_set[64];
+  set_lds_limit((const void*)grouped_bwd_kernel<TX, TW>, TX::kLds, lds_set);
+  gx.tiles_n = (int32_t)((gx.Nc + TX::kBN - 1) / TX::kBN);
+  gw.tiles_m = (int32_t)((gw.Mc + TW::kBM - 1) / TW::kBM);
+  gw.tiles_n = (int32_t)((gw.Nc + TW::kBN - 1) / TW::kBN);
+  const int64_t nx = (most_units(gr.T, gr.E, TX::kBM) * gx.tiles_n + 7) & ~7LL;
+  const int64_t pad = (gw.tiles_m * gw.tiles_n + 7) & ~7;
+  const int64_t nw = pad * gr.E;
+  hipLaunchKernelGGL((grouped_bwd_kernel<TX, TW>), dim3((unsigned)(nx + nw + db_blocks(db, gr))),
+                     dim3(TX::kThreads), TX::kLds, st, gx, gw, gr, sx, sw, side, (int)nx, (int)nw,
+                     (int)pad, db);
+}
+
+bool launch_bwd(GemmArgs& gx, GemmArgs& gw, int fg, int fw, const Groups& gr,
+                const GroupStrides& sx, const GroupStrides& sw, const GroupedSide& side,
+                const DbArgs& db, hipStream_t st) {
+  if (!rows_fast_ok<kCross>(gx, sx) || !contract_fast_ok(gw)) return false;
+  int tile = forced_tile();
+  if (tile == kTileV1) return false;
+  if (tile != kTile128x128w8 && tile != kTile128x256 && tile != kTile256x256w8)
+    tile = pick_bwd(gx, gw, gr);
+  by_formats(fg, fw, [&](auto a, auto b) {
+    constexpr int FG = decltype(a)::value, FW = decltype(b)::value;
+    if (tile == kTile128x128w8)
+      launch_bwd_t<Tile128<kKContig, kCross, FG, FW>, Tile128<kCross, kCross, FG, FW>>(
+          gx, gw, gr, sx, sw, side, db, st);
+    else if (tile == kTile128x256)
+      launch_bwd_t<Tile128x256<kKContig, kCross, FG, FW>, Tile128x256<kCross, kCross, FG, FW>>(
+          gx, gw, gr, sx, sw, side, db, st);
+    else
+      launch_bwd_t<Tile256<kKContig, kCross, FG, FW>, Tile256<kCross, kCross, FG, FW>>(
+          gx, gw, gr, sx, sw, side, db, st);
+  });
+  return true;
 }
 
 }  // namespace
@@ -270,7 +288,7 @@ int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
     if (!is_f8(x8.dtype)) return FP8_ERR_DTYPE;
     if ((T * K > 0 && !x8.data) || !x8.scale) return FP8_ERR_NULL;
   }
-  const bool sums = db && T > 0 && N > 0;
+  const bool sums = hp && db && T > 0 && N > 0;
   if (sums && !db_ws) return FP8_ERR_NULL;
   if (sums && !fp8_grouped_db_workspace_bytes(T, E, N)) return FP8_ERR_SHAPE;
 
@@ -278,19 +296,27 @@ int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
   const uint8_t* g8;
   const float* sg;
   GroupedSide side = {};
-  const bool have_dx = dx && T * K > 0;
-  bool fold = false;
+  const bool have_dx = dx && T * K > 0, have_dw = dw && N * K > 0;
+  DbArgs da = {};
+  if (db && N > 0) {
+    da.db = reinterpret_cast<uint16_t*>(db);
+    da.N = N;
+  }
   if (hp) {
     const RowLimit limit = {offsets + E, T, N};
-    if (sums)
+    bool fold = false;
+    if (sums) {
       fold = enqueue_groupsum(g, T, N, fmt_g, g8_out, ring_g, sg_used, amax_g, db_ws, gr, limit,
                               stream);
-    else
+    } else {
       fold = enqueue_quant(g.data, g.dtype, T * N, fmt_g, g8_out, ring_g, sg_used, amax_g, nullptr,
                            stream, have_dx, limit);
+    }
     if (fold) side.fold[0] = fold_of(ring_g, fmt_g, amax_g);
     g8 = g8_out;
     sg = sg_used;
+    da.ws = db_ws;
+    da.most = (int32_t)most_units(T, E, kColRowsPerChunk);
   } else {
     g8 = reinterpret_cast<const uint8_t*>(g.data);
     sg = g.scale;
@@ -298,52 +324,49 @@ int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
     side.scale_dst[0] = sg_used;
     side.amax_dst[0] = amax_g;
     side.n[0] = 1;
-    if (sums) enqueue_groupsum_fp8(g8, T, N, fmt_g, db_ws, gr, stream);
+    da.g8 = g8;
+    da.g8_e5m2 = fmt_g == FP8_E5M2;
+    da.vec = aligned16(g8) && N % 16 == 0;
+    da.scale = sg;
   }
-  if (have_dx) {
-    GemmArgs a = {};
-    GroupStrides s = {};
-    a.a = g8;
-    a.lda = N;
-    a.b = reinterpret_cast<const uint8_t*>(w8.data);
-    a.ldb = K;
-    a.Mc = T;
-    a.Nc = K;
-    a.Kc = N;
-    a.c = reinterpret_cast<uint16_t*>(dx);
-    a.ldc = K;
-    a.scale_a = sg;
-    a.scale_b = w8.scale;
-    s.b = N * K;
-    s.sb = w_scales == E && E > 1 ? 1 : 0;
-    finish_grouped_args(a, s);
-    launch_dx(a, fmt_g, dtype_fmt(w8.dtype), gr, s, side, stream);
-  } else {
-    launch_side(side, stream);
-  }
-  if (dw && N * K > 0) {
-    GemmArgs a = {};
-    GroupStrides s = {};
-    a.a = g8;
-    a.lda = N;
-    a.b = reinterpret_cast<const uint8_t*>(x8.data);
-    a.ldb = K;
-    a.Mc = N;
-    a.Nc = K;
-    a.Kc = T;
-    a.c = reinterpret_cast<uint16_t*>(dw);
-    a.ldc = K;
-    a.scale_a = sg;
-    a.scale_b = x8.scale;
-    s.c = N * K;
-    finish_grouped_args(a, s);
-    launch_dw(a, fmt_g, dtype_fmt(x8.dtype), gr, s, stream);
-  }
-  if (db && N > 0)
-    hipLaunchKernelGGL(grouped_db_kernel, dim3((unsigned)((N + 63) / 64), (unsigned)E), dim3(256), 0,
-                       stream, db_ws, (int)most_units(T, E, kColRowsPerChunk), gr, N,
-                       hp ? nullptr : sg,
-                       reinterpret_cast<uint16_t*>(db));
+  GemmArgs gx = {}, gw = {};
+  GroupStrides sx = {}, sw = {};
+  gx.a = g8;
+  gx.lda = N;
+  gx.b = reinterpret_cast<const uint8_t*>(w8.data);
+  gx.ldb = K;
+  gx.Mc = T;
+  gx.Nc = K;
+  gx.Kc = N;
+  gx.c = reinterpret_cast<uint16_t*>(dx);
+  gx.ldc = K;
+  gx.scale_a = sg;
+  gx.scale_b = w8.scale;
+  sx.b = N * K;
+  sx.sb = w_scales == E && E > 1 ? 1 : 0;
+  finish_grouped_args(gx, sx);
+  gw.a = g8;
+  gw.lda = N;
+  gw.b = reinterpret_cast<const uint8_t*>(x8.data);
+  gw.ldb = K;
+  gw.Mc = N;
+  gw.Nc = K;
+  gw.Kc = T;
+  gw.c = reinterpret_cast<uint16_t*>(dw);
+  gw.ldc = K;
+  gw.scale_a = sg;
+  gw.scale_b = x8.scale;
+  sw.c = N * K;
+  finish_grouped_args(gw, sw);
+  if (have_dx && have_dw && w8.dtype == x8.dtype &&
+      launch_bwd(gx, gw, fmt_g, dtype_fmt(w8.dtype), gr, sx, sw, side, da, stream))
+    return hip_status();
+  if (have_dx) launch_dx(gx, fmt_g, dtype_fmt(w8.dtype), gr, sx, side, stream);
+  else launch_side(side, stream);
+  if (have_dw) launch_dw(gw, fmt_g, dtype_fmt(x8.dtype), gr, sw, stream);
+  if (da.db)
+    hipLaunchKernelGGL(grouped_db_kernel, dim3((unsigned)db_blocks(da, gr)), dim3(256), 0, stream,
+                       da, gr);
   return hip_status();
 }
 

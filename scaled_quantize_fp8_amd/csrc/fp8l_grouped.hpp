@@ -126,12 +126,12 @@ __global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void grouped_rows_ke
   grouped_side(side);
 }
 
-// pad: blocks per group, the group's tiles rounded up to a multiple of 8.
+// Tile of block b of a contract problem; pad: blocks per group, the group's
+// tiles rounded up to a multiple of 8.
 template <class Tile>
-__global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void grouped_contract_kernel(
-    GemmArgs g, Groups gr, GroupStrides st, int pad) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem_contract[];
-  const int e = blockIdx.x / pad, l = blockIdx.x % pad;
+FP8L_DEV void contract_block(GemmArgs& g, const Groups& gr, const GroupStrides& st, int pad, int b,
+                             uint8_t* smem) {
+  const int e = b / pad, l = b % pad;
   if (l >= g.tiles_m * g.tiles_n) return;
   int tm, tn;
   tile_coords_xcd(l, g.tiles_m, g.tiles_n, tm, tn);
@@ -142,7 +142,14 @@ __global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void grouped_contrac
   t.b += (int64_t)start * g.ldb;
   t.Kc = end - start;
   t.c += e * st.c;
-  Tile::run(t, tm, tn, smem_contract);
+  Tile::run(t, tm, tn, smem);
+}
+
+template <class Tile>
+__global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void grouped_contract_kernel(
+    GemmArgs g, Groups gr, GroupStrides st, int pad) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_contract[];
+  contract_block<Tile>(g, gr, st, pad, blockIdx.x, smem_contract);
 }
 
 // ---------------------------------------------------------------- db
@@ -168,13 +175,47 @@ FP8L_DEV void chunk_sum_store(const float cs[8], float* ws, int64_t chunk, int64
   if (gc < cols) ws[chunk * cols + gc] = t;
 }
 
+// Scale mode of a small dynamic quantize: every block takes the amax of the
+// whole tensor itself (it is in L2 after the first), which saves the two
+// launches of an amax pass (130 x 256 in four groups, whole backward: 33 us
+// against 23).
+constexpr int kScaleLocal = 4;
+constexpr int64_t kLocalMost = 65536;  // elements
+
+template <int IN>
+FP8L_DEV uint32_t block_absmax(const QArgs& a, uint32_t* sh) {
+  const int64_t n = limited(a.n, a.limit);
+  uint32_t mx = 0;
+  const int64_t nv = a.vec_ok ? n / 8 : 0;
+  for (int64_t c = threadIdx.x; c < nv; c += kQThreads) {
+    float v[8];
+    load8<IN>(a.x, 8 * c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, absbits(v[i]));
+  }
+  for (int64_t c = 8 * nv + threadIdx.x; c < n; c += kQThreads)
+    mx = max(mx, absbits(load1<IN>(a.x, c)));
+  return block_max_u32(mx, sh);
+}
+
 // G [T, cols] quantized and summed in one pass (the grouped form of
 // quantize_colsum_kernel: same codes, amax and ring finalize).  Rows of no
 // group are neither read nor written.
 template <int IN, int FMT, int SMODE>
 __global__ __launch_bounds__(kQThreads) void quantize_groupsum_kernel(QArgs a, Groups gr,
                                                                       int strips) {
-  const float s = launch_scale<FMT, SMODE>(a);
+  float s;
+  if constexpr (SMODE == kScaleLocal) {
+    __shared__ uint32_t sh_amax[kQThreads / 64];
+    const float m = __uint_as_float(block_absmax<IN>(a, sh_amax));
+    s = scale_from_amax(m, FmtTraits<FMT>::kMax, 1.0f);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      *a.scale_used = s;
+      *a.amax_out = m;
+    }
+  } else {
+    s = launch_scale<FMT, SMODE>(a);
+  }
   const int chunk = blockIdx.x / strips, strip = blockIdx.x % strips;
   const GroupSpan sp = find_group(gr, kColRowsPerChunk, chunk);
   uint32_t mx = 0;
@@ -223,41 +264,135 @@ __global__ __launch_bounds__(kQThreads) void quantize_groupsum_kernel(QArgs a, G
     }
     chunk_sum_store(cs, a.colsum, chunk, strip, a.cols);
   }
-  finish_launch<FMT, SMODE>(a, mx, s, blockIdx.x, gridDim.x);
+  if constexpr (SMODE != kScaleLocal)
+    finish_launch<FMT, SMODE>(a, mx, s, blockIdx.x, gridDim.x);
 }
 
-// The same sums of pre-quantized codes (decoded; the finalize applies 1/sg).
+// db of one group and a strip of columns by one block (256 threads or more,
+// every thread calls it).  sh: kDbLds bytes of LDS.
+constexpr int kDbLds = 8 * 256 * 4;
+struct DbArgs {
+  uint16_t* db;        // [E][N], null: none
+  const float* ws;     // chunk sums of a quantized-here G, or null: sum g8
+  int32_t most;        // chunks in ws
+  const uint8_t* g8;   // codes of a G that came quantized
+  int32_t g8_e5m2, vec;
+  const float* scale;  // of g8 (the sums are of decoded codes), else null
+  int64_t N;
+};
+
+FP8L_DEV int db_strip(const DbArgs& a) { return a.ws ? 64 : 256; }  // columns (as db_blocks on the host)
+
+FP8L_DEV void db_store(const DbArgs& a, int e, int64_t n, float t) {
+  if (a.scale) t *= 1.0f / *a.scale;
+  a.db[(int64_t)e * a.N + n] = (uint16_t)f32_to_bf16(t);
+}
+
+// From the chunk sums: wave w adds chunks w, w + 4, .., the four sums meet in
+// wave order.  A group without rows gets 0; chunks past ws (offsets that
+// break the contract) are not read.
+FP8L_DEV void db_from_chunks(const DbArgs& a, const Groups& gr, int e, int strip, float* sh) {
+  const GroupSpan sp = group_span(gr, kColRowsPerChunk, e);
+  const int chunks = min(units_of(sp.end - sp.start, kColRowsPerChunk), a.most - sp.before);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t n = (int64_t)strip * 64 + lane;
+  float s = 0.0f;
+  if (n < a.N && w < 4)
+    for (int c = w; c < chunks; c += 4) s += a.ws[(int64_t)(sp.before + c) * a.N + n];
+  if (w < 4) sh[w * 64 + lane] = s;
+  __syncthreads();
+  if (w == 0 && n < a.N)
+    db_store(a, e, n, sh[lane] + sh[64 + lane] + sh[128 + lane] + sh[192 + lane]);
+}
+
+// From the codes, in one go: 16 lanes a row (16 columns each), 4 rows a wave
+// instruction, eight of them in flight; a wave's four row partials meet in an
+// xor tree, the waves' in wave order.  All orders are fixed by the sizes.
 template <int FMT>
-__global__ __launch_bounds__(kQThreads) void groupsum_fp8_kernel(const uint8_t* g8, int64_t cols,
-                                                                 Groups gr, int strips, int vec,
-                                                                 float* ws) {
-  const int chunk = blockIdx.x / strips, strip = blockIdx.x % strips;
-  const GroupSpan sp = find_group(gr, kColRowsPerChunk, chunk);
-  if (sp.e < 0) return;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t c0 = (int64_t)strip * kColStrip + tx * 8;
-  const int64_t r0 = sp.start + (int64_t)sp.unit * kColRowsPerChunk;
-  const int64_t r1 = min<int64_t>(r0 + kColRowsPerChunk, sp.end);
-  float cs[8];
+FP8L_DEV void db_from_codes(const DbArgs& a, const Groups& gr, int e, int strip, float* sh) {
+  const int start = __builtin_amdgcn_readfirstlane(group_edge(gr, e));
+  const int end = max(__builtin_amdgcn_readfirstlane(group_edge(gr, e + 1)), start);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int64_t c0 = (int64_t)strip * 256 + 16 * (lane & 15);
+  const int cnt = (int)min<int64_t>(16, a.N - c0);
+  float s[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 0.0f;
-  const int cnt = (int)max<int64_t>(0, min<int64_t>(8, cols - c0));
+  for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+  if (cnt > 0) {
+    int r = start + 4 * w + (lane >> 4);
+    const uint8_t* p = a.g8 + (int64_t)r * a.N + c0;
+    const int64_t step = (int64_t)4 * nw * a.N;
+    if (a.vec && cnt == 16) {
+      for (; r < end; r += 8 * 4 * nw, p += 8 * step) {
+        uint4 v[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t r = r0 + ty + 8 * k;
-    if (r >= r1 || cnt <= 0) continue;
-    const uint8_t* p = g8 + r * cols + c0;
-    if (vec && cnt == 8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
+        for (int k = 0; k < 8; ++k)  // rows past the end: the first one again, not added
+          v[k] = *reinterpret_cast<const uint4*>(p + (r + 4 * nw * k < end ? k * step : 0));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] += fp8_to_f32<FMT>(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu);
+        for (int k = 0; k < 8; ++k) {
+          if (r + 4 * nw * k >= end) continue;
+          const uint32_t q[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[i] += fp8_to_f32<FMT>((q[i >> 2] >> (8 * (i & 3))) & 0xffu);
+        }
+      }
     } else {
+      for (; r < end; r += 4 * nw, p += step)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < cnt) cs[i] += fp8_to_f32<FMT>(p[i]);
+        for (int i = 0; i < 16; ++i)
+          if (i < cnt) s[i] += fp8_to_f32<FMT>(p[i]);
     }
   }
-  chunk_sum_store(cs, ws, chunk, strip, cols);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    s[i] += __shfl_xor(s[i], 16);
+    s[i] += __shfl_xor(s[i], 32);
+    if (lane < 16) sh[w * 256 + 16 * lane + i] = s[i];
+  }
+  __syncthreads();
+  const int64_t n = (int64_t)strip * 256 + threadIdx.x;
+  if (threadIdx.x < 256 && n < a.N) {
+    float t = sh[threadIdx.x];
+    for (int k = 1; k < nw; ++k) t += sh[k * 256 + threadIdx.x];
+    db_store(a, e, n, t);
+  }
+}
+
+FP8L_DEV void db_block(const DbArgs& a, const Groups& gr, int b, float* sh) {
+  const int width = db_strip(a), strips = (int)((a.N + width - 1) / width);
+  const int e = b / strips, strip = b % strips;
+  if (a.ws) db_from_chunks(a, gr, e, strip, sh);
+  else if (a.g8_e5m2) db_from_codes<kE5M2>(a, gr, e, strip, sh);
+  else db_from_codes<kE4M3>(a, gr, e, strip, sh);
+}
+
+// The whole backward behind the quantize in one launch: dX in blocks
+// [0, nx), dW in [nx, nx + nw), db in the rest (nx and nw multiples of 8, so
+// each problem keeps its XCD order).  All three wait only for the quantize;
+// in one grid the tail of one is filled by the next, and two launches (about
+// 4 us each on the GPU) go.  dX's tiles, with the longer contraction as a
+// rule, come first.
+template <class TX, class TW>
+__global__ __launch_bounds__(TX::kThreads, TX::kBlocks) void grouped_bwd_kernel(
+    GemmArgs gx, GemmArgs gw, Groups gr, GroupStrides sx, GroupStrides sw, GroupedSide side, int nx,
+    int nw, int pad, DbArgs db) {
+  static_assert(TX::kThreads == TW::kThreads, "one block size");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_bwd[];
+  const int b = blockIdx.x;
+  if (b < nx) {
+    int tm, tn;
+    const GroupSpan sp = rows_work(gr, TX::kBM, gx.tiles_n, tm, tn);
+    if (sp.e >= 0) {
+      move_to_rows<false>(gx, sx, sp, tm, TX::kBM);
+      TX::run(gx, 0, tn, smem_bwd);
+    }
+    grouped_side(side);
+  } else if (b < nx + nw) {
+    contract_block<TW>(gw, gr, sw, pad, b - nx, smem_bwd);
+  } else {
+    db_block(db, gr, b - nx - nw, reinterpret_cast<float*>(smem_bwd));
+  }
 }
 
 }  // namespace fp8l

@@ -134,17 +134,17 @@ inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
 }
 
 // The same where the pipelined tiles cannot run (odd sizes, unaligned
-// pointers): the general tile (two blocks per CU; 1.5 us per 128 of K alone,
-// 2.7 for two), or the skinny kernel's form for any alignment, whose pieces
-// take about half as long again.
+// pointers): the general tile (two blocks per CU; 2.5 us per 128 of K alone,
+// 3.3 for two), or the skinny kernel's form for any alignment, whose pieces
+// take 1.6 (64 rows: 2) times as long.
 inline int pick_any(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   const double cus = cu_count(), steps = (double)((K + 127) / 128);
   const double tiles = expected_units(T, E, 128) * (double)((N + 127) / 128);
-  double us = 5 + (tiles <= cus ? 1.5 : 2.7 * (tiles / (2 * cus) + 0.5)) * steps;
+  double us = 5 + (tiles <= cus ? 2.5 : 3.3 * (tiles / (2 * cus) + 0.5)) * steps;
   int best = kTileV1;
   const int mts[3] = {1, 2, 4}, ids[3] = {kTileSkinny16Any, kTileSkinny32Any, kTileSkinny64Any};
   for (int i = 0; skinny && i < 3; ++i) {
-    const double t = 1.5 * skinny_us(mts[i], expected_units(T, E, 16 * mts[i]), N, K);
+    const double t = (i < 2 ? 1.6 : 2.0) * skinny_us(mts[i], expected_units(T, E, 16 * mts[i]), N, K);
     if (t < us) us = t, best = ids[i];
   }
   return best;
@@ -163,18 +163,35 @@ int rows_tile(const GemmArgs& g, const Groups& gr, const GroupStrides& s) {
 
 // Tile of a contract launch, by the mean group (4093 rows in 32 groups, dW of
 // 4096 x 1024: 82 us on 128x256, 88 on 256x256, 116 on 128x128).
+// One resource covers a group's rows of both operands: at most all T rows.
+inline bool contract_fast_ok(const GemmArgs& g) {
+  return aligned16(g.a) && aligned16(g.b) && aligned16(g.c) && g.lda % 16 == 0 &&
+         g.ldb % 16 == 0 && (g.Kc + 256) * g.lda < (1LL << 31) &&
+         (g.Kc + 256) * g.ldb < (1LL << 31);
+}
 inline int contract_tile(const GemmArgs& g, const Groups& gr) {
-  // one resource covers a group's rows of both operands: at most all T rows
-  const bool ok = aligned16(g.a) && aligned16(g.b) && aligned16(g.c) && g.lda % 16 == 0 &&
-                  g.ldb % 16 == 0 && (g.Kc + 256) * g.lda < (1LL << 31) &&
-                  (g.Kc + 256) * g.ldb < (1LL << 31);
-  if (!ok) return kTileV1;
+  if (!contract_fast_ok(g)) return kTileV1;
   const int f = forced_tile();
   if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8) return f;
   const double m128 = (double)((g.Mc + 127) / 128) * gr.E, m256 = (double)((g.Mc + 255) / 256) * gr.E;
   const double n128 = (double)((g.Nc + 127) / 128), n256 = (double)((g.Nc + 255) / 256);
   double us = 0;
   return pick_of(m128 * n128, m128 * n256, m256 * n256, (double)gr.T / gr.E, &us);
+}
+
+// One tile shape for dX and dW in a shared launch: the smallest sum.
+inline int pick_bwd(const GemmArgs& gx, const GemmArgs& gw, const Groups& gr) {
+  const int tiles[3] = {kTile128x128w8, kTile128x256, kTile256x256w8};
+  const int bm[3] = {128, 128, 256}, bn[3] = {128, 256, 256};
+  int best = kTile128x128w8;
+  double us = 1e30;
+  for (int i = 0; i < 3; ++i) {
+    const double x = expected_units(gr.T, gr.E, bm[i]) * (double)((gx.Nc + bn[i] - 1) / bn[i]);
+    const double w = (double)((gw.Mc + bm[i] - 1) / bm[i]) * ((gw.Nc + bn[i] - 1) / bn[i]) * gr.E;
+    const double t = tile_us(tiles[i], x, (double)gx.Kc) + tile_us(tiles[i], w, (double)gr.T / gr.E);
+    if (t < us) us = t, best = tiles[i];
+  }
+  return best;
 }
 
 template <class Tile, bool I8>

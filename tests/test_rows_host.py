@@ -74,7 +74,7 @@ def test_grouped_bwd_refusals(lib):
     assert _bwd(lib, x8=_op(E4, data=Z)) == F.FP8_ERR_NULL
     assert _bwd(lib, w8=_op(E4, scale=Z)) == F.FP8_ERR_NULL
     assert _bwd(lib, ns=5) == F.FP8_ERR_SHAPE
-    assert _bwd(lib, ws=Z) == F.FP8_ERR_NULL
+    assert _bwd(lib, g=_op(BF), ws=Z) == F.FP8_ERR_NULL
     ring = F._Ring(P, 0, 1)
     assert _bwd(lib, g=_op(BF), rg=ctypes.byref(ring)) == F.FP8_ERR_RING
 
