@@ -616,12 +616,12 @@ def _arg(t, what, dtypes, shape, dev, optional=False, numel=None):
     """Data pointer of a checked tensor argument (None when absent)."""
     if t is None and optional:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous()
-            and (shape is None or t.shape == shape) and (numel is None or t.numel() >= numel)):
-        _need(t, what, dtypes, shape=shape, numel=numel, optional=False)
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{what}: must be a GPU tensor on {dev} (got {t.device})")
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == dev and t.is_cuda
+            and t.is_contiguous() and (shape is None or t.shape == shape)
+            and (numel is None or t.numel() >= numel)):
+        return t.data_ptr()
+    _need(t, what, dtypes, shape=shape, numel=numel, optional=False)
+    raise ValueError(f"{what}: must be a GPU tensor on {dev} (got {t.device})")
 
 
 def _shape_of(t, dims, what):
@@ -647,16 +647,26 @@ def _arg_operand(t, what, shape, dev, hp_ok=True, scales=(1,)):
     return _Operand(_arg(t, what, _HP, shape, dev), _TORCH_DT[t.dtype], None), 1
 
 
+# the current stream's handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _arg_stream(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
     return stream.cuda_stream
 
 
+_entry = {}  # C functions by name
+
+
 def _run(name, args, dev):
-    fn = getattr(lib(), name)
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
     if dev.index == torch.cuda.current_device():
         st = fn(*args)
     else:

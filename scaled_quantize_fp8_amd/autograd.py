@@ -123,6 +123,7 @@ class _Fp8GroupedLinearFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, gy):
         x8, w8, sx, sw, offsets = ctx.saved_tensors
         T, K = x8.shape

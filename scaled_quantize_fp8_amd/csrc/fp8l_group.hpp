@@ -120,7 +120,9 @@ FP8L_DEV GroupSpan rows_work(const Groups& g, int per, int tiles_n, int& tm, int
   const int u = pid / tiles_n;
   GroupSpan sp;
   if (g.E <= 64) {
-    const int l = __builtin_ctzll(__ballot(incl > u));
+    const unsigned long long hit = __ballot(incl > u);
+    if (!hit) return GroupSpan{-1, 0, 0, 0, 0};
+    const int l = __builtin_ctzll(hit);
     sp.e = l;
     sp.start = __builtin_amdgcn_readlane(s, l);
     sp.end = __builtin_amdgcn_readlane(t, l);
@@ -128,6 +130,7 @@ FP8L_DEV GroupSpan rows_work(const Groups& g, int per, int tiles_n, int& tm, int
     sp.unit = u - sp.before;
   } else {
     sp = find_group(g, per, u);
+    if (sp.e < 0) return sp;
   }
   tile_coords(pid - sp.before * tiles_n, units_of(sp.end - sp.start, per), tiles_n, tm, tn);
   return sp;

@@ -18,15 +18,15 @@ inline int64_t most_units(int64_t T, int64_t E, int64_t per) {
 }
 
 // Sizes of a grouped call: 32-bit row offsets, and tile numbers of every
-// tile choice below 2^31 (128 is the smallest tile edge).
+// tile choice (units of 16 rows by 16 columns at least) below 2^31.
 inline int check_grouped(int64_t T, int64_t E, int64_t N, int64_t K) {
   if (T < 0 || T > INT32_MAX || E < 1 || E > 65535 || N < 0 || K < 0) return FP8_ERR_SHAPE;
   if (N > INT32_MAX || K > INT32_MAX) return FP8_ERR_SHAPE;
   if (!mul_ok(T, K) || !mul_ok(T, N) || !mul_ok(N, K) || !mul_ok(N * K, E)) return FP8_ERR_SHAPE;
   const int64_t un = (N + 127) / 128, uk = (K + 127) / 128;
   const int64_t u = most_units(T, E, 16);
-  if (u * (un > uk ? un : uk) > INT32_MAX / 2) return FP8_ERR_SHAPE;
-  if (un * uk > INT32_MAX / 4 || (un * uk + 8) * E > INT32_MAX) return FP8_ERR_SHAPE;
+  if (u * (un > uk ? un : uk) > INT32_MAX / 16) return FP8_ERR_SHAPE;
+  if (un * uk > INT32_MAX / 4 || (un * uk + 8) * E > INT32_MAX / 2) return FP8_ERR_SHAPE;
   return FP8_OK;
 }
 
@@ -124,6 +124,7 @@ inline double expected_units(int64_t T, int64_t E, int64_t per) {
 inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   const double u128 = expected_units(T, E, 128), u256 = expected_units(T, E, 256);
   const double n128 = (double)((N + 127) / 128), n256 = (double)((N + 255) / 256);
+  skinny = skinny && (T + 15) / 16 < INT32_MAX / ((N + 15) / 16 + 1);  // tile numbers
   double us = 0;
   int best = pick_of(u128 * n128, u128 * n256, u256 * n256, (double)K, &us);
   for (int mt = 1; skinny && mt <= 4; ++mt) {
@@ -140,6 +141,7 @@ inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
 inline int pick_any(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   const double cus = cu_count(), steps = (double)((K + 127) / 128);
   const double tiles = expected_units(T, E, 128) * (double)((N + 127) / 128);
+  skinny = skinny && (T + 15) / 16 < INT32_MAX / ((N + 15) / 16 + 1);  // tile numbers
   double us = 5 + (tiles <= cus ? 2.5 : 3.3 * (tiles / (2 * cus) + 0.5)) * steps;
   int best = kTileV1;
   const int mts[3] = {1, 2, 4}, ids[3] = {kTileSkinny16Any, kTileSkinny32Any, kTileSkinny64Any};

@@ -7,13 +7,19 @@
 namespace fp8l {
 namespace {
 
-// One tile per block in XCD-major order.
+// One tile per block in XCD-major order; A is moved to the tile's rows, so
+// that one buffer resource covers them however many rows there are.
 template <class Tile>
 __global__ __launch_bounds__(Tile::kThreads, Tile::kBlocks) void i8_gemm_kernel(GemmArgs g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem_i8[];
   int tm, tn;
   tile_coords_xcd(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-  Tile::run(g, tm, tn, smem_i8);
+  const int64_t row = (int64_t)tm * Tile::kBM;
+  g.a += row * g.lda;
+  g.c += row * g.ldc;
+  g.scale_a += row;
+  g.Mc = min<int64_t>(g.Mc - row, Tile::kBM);
+  Tile::run(g, 0, tn, smem_i8);
 }
 
 template <class Tile>
@@ -26,14 +32,9 @@ void launch_i8_t(GemmArgs& g, hipStream_t st) {
                      dim3(Tile::kThreads), Tile::kLds, st, g);
 }
 
-bool i8_fast_ok(const GemmArgs& g) {
-  GroupStrides s = {};
-  return rows_fast_ok<kKContig>(g, s) && (g.Mc + 256) * g.lda < (1LL << 31);
-}
-
 int i8_tile(const GemmArgs& g) {
   const int f = forced_tile();
-  if (!i8_fast_ok(g)) return f == kTileV1 ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
+  if (!rows_fast_ok<kKContig>(g, GroupStrides{})) return f == kTileV1 ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
   if (f == kTileV1 || f >= kTile256x256w8) return f;
   return pick_tile(g.Mc, 1, g.Nc, g.Kc, true);
 }

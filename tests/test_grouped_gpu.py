@@ -322,3 +322,39 @@ def test_wild_offsets_stay_inside_the_operands():
                              F.Quantized(to_dev(w8), O.E4M3, scalar_dev(1)), None, off, O.E4M3, y)
     torch.cuda.synchronize()
     assert (big[:256] == SENTINEL).all() and (big[256 + T:] == SENTINEL).all()
+
+
+def test_small_dynamic_quantize_matches_the_general_one():
+    """The one-launch quantize of a small G gives the codes, scale and amax of
+    the amax-pass form (the same G in front of rows of no group)."""
+    N, K = 64, 48
+    T, off = offsets_of("tail")
+    E, used = len(off) - 1, off[-1]
+    G = bf16((T, N), 1e-2, 5)
+    big = torch.zeros(2048, N, dtype=torch.bfloat16)
+    big[:T] = G
+    big[used:] = float("nan")
+    out = []
+    for g in (G, big):
+        rows = g.shape[0]
+        g8 = torch.zeros(rows, N, dtype=torch.uint8, device=DEV)
+        sg, am = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+        db = _filled(E, N)
+        ws = torch.empty(F.fp8_grouped_db_workspace_bytes(rows, E, N), dtype=torch.uint8,
+                         device=DEV)
+        F.fp8_grouped_linear_bwd(g.to(DEV), O.E5M2, offsets_dev(off), None, None, db=db, db_ws=ws,
+                                 g8_out=g8, sg_used=sg, amax_g=am)
+        out.append((g8[:used].cpu(), sg.cpu(), am.cpu(), db.cpu()))
+    assert T * N <= 65536 < 2048 * N
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+def test_gradients_of_gradients_are_refused():
+    from scaled_quantize_fp8_amd.autograd import Fp8GroupedLinear
+    m = Fp8GroupedLinear(2, 32, 32, device=DEV)
+    x = bf16((8, 32), 1.0, 1).to(DEV).requires_grad_(True)
+    v = bf16((8, 32), 1.0, 2).to(DEV).requires_grad_(True)
+    g, = torch.autograd.grad(m(x, offsets_dev([0, 4, 8])), x, v, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        g.sum().backward()

@@ -252,3 +252,20 @@ def test_calls_on_several_streams():
     torch.cuda.synchronize()
     for (y, _, _), v in zip(outs, want):
         assert torch.equal(y, v)
+
+
+def test_rows_beyond_one_buffer_resource():
+    """X codes of more than 2^31 bytes: the first and the last rows against
+    the oracle (the tiles move their own rows into reach)."""
+    M, N, K = 150_000, 64, 14_400
+    w, sw = _weights((N, K))
+    x8 = torch.zeros(M, K, dtype=torch.int8, device=DEV)
+    sx = torch.ones(M, device=DEV)
+    rows = [0, 1, M // 2, M - 130, M - 1]
+    q = np.random.default_rng(3).integers(-127, 128, (len(rows), K)).astype(np.int8)
+    x8[torch.tensor(rows, device=DEV)] = to_dev(q)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    F.fp8_i8_linear_fwd(F.QuantizedRows(x8, sx), F.QuantizedRows(to_dev(w), to_dev(sw)), None, y)
+    r, p = R.i8_linear(q, np.ones(len(rows), np.float32), w, sw)
+    check_i8(y[torch.tensor(rows, device=DEV)], r, p, "bf16")
+    assert not y[M - 129:M - 1].any() and not y[2:M // 2].any()

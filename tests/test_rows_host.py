@@ -38,7 +38,7 @@ def _bwd(lib, T=8, E=2, N=16, K=16, off=P, g=_op(E5), fmt=F.FP8_E5M2, rg=Z, x8=_
 @pytest.mark.parametrize("call", [_fwd, _bwd])
 def test_grouped_sizes(lib, call):
     for kw in (dict(T=-1), dict(T=1 << 31), dict(E=0), dict(E=-3), dict(E=65536), dict(N=-1),
-               dict(K=-1), dict(N=1 << 31), dict(T=(1 << 31) - 1, N=1 << 20),
+               dict(K=-1), dict(N=1 << 31), dict(T=(1 << 31) - 1, N=1 << 20), dict(T=1 << 28, N=1 << 18),
                dict(N=1 << 30, K=1 << 30, E=65535)):
         assert call(lib, **kw) == F.FP8_ERR_SHAPE, kw
     assert call(lib, off=Z) == F.FP8_ERR_NULL
