@@ -552,7 +552,8 @@ int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_oper
  * The same over ragged groups of rows (offsets, T, E as in
  * fp8_grouped_linear_fwd): w [E, N, K] with scale [E, N], bias [E, N].  Rows
  * behind offsets[E] are not quantized and their rows of x8_out, sx_out and y
- * are left as they were.
+ * are left as they were; of rows before offsets[0] the same holds for y, and
+ * x8_out and sx_out may or may not receive their codes.
  */
 int fp8_i8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
                               fp8_operand_t x, fp8_operand_t w, const void* bias,

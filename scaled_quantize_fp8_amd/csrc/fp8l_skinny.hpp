@@ -22,6 +22,7 @@
 
 #include "fp8l_gemm3.hpp"
 #include "fp8l_grouped.hpp"
+#include "fp8l_i8.hpp"
 
 namespace fp8l {
 
@@ -44,8 +45,13 @@ struct Skinny {
     uint16_t b[4];
   };
   FP8L_DEV static Epi epi(const GemmArgs& g, int row, int64_t j) {
-    Epi e;
+    Epi e = epi_cols(g, j);
     e.sa = g.scale_a[I8 && row < g.Mc ? row : 0];
+    return e;
+  }
+  FP8L_DEV static Epi epi_cols(const GemmArgs& g, int64_t j) {
+    Epi e;
+    e.sa = 1.0f;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       // Nc a multiple of 8: all four columns or none
@@ -230,6 +236,144 @@ struct Skinny {
     }
   }
 };
+
+// The skinny kernel for integer layers whose high-precision X has so few rows
+// that every block quantizes them itself (fp8l_i8.hpp gives the rule and the
+// arithmetic): one launch instead of two.  The block's first pieces of B are
+// in flight meanwhile.  The codes stay in LDS, from where the K loop reads
+// them; the block of the first tile column writes codes and scales out.
+struct FusedX {
+  const void* x;  // row 0 of the tile
+  int8_t* q;
+  float* scale;
+};
+
+template <int IN>
+struct SkinnyFused {
+  static constexpr int kBM = 16, kWaveN = 16, kThreads = 512, kU = 4;
+  static constexpr bool I8 = true;
+  using S = Skinny<kI8, kI8, 1, 1>;
+  static constexpr int kPart = S::kLds;         // partial sums
+  static constexpr int kHead = kPart + 16 * 8 * 4 + 16 * 4;  // + amax per row and wave, + scales
+  // LDS for rows of K codes
+  static int lds(int rows, int64_t K) { return (int)(((kHead + 15) & ~15) + rows * K); }
+
+  FP8L_DEV static void run(const GemmArgs& g, const FusedX& fx, bool write, int tn, int KW,
+                           uint8_t* smem) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
+    const int64_t jb = (int64_t)tn * JW * kWaveN, j0 = jb + jw * kWaveN;
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b, (uint32_t)(g.Nc * g.ldb));
+    const uint32_t ob = (uint32_t)((j0 + r) * g.ldb);
+    const uint32_t K = (uint32_t)g.Kc, pieces = (K + 127) / 128;
+    const int rows = (int)g.Mc;
+    uint32_t* const red = reinterpret_cast<uint32_t*>(smem + kPart);  // [row][wave of the row]
+    float* const sc = reinterpret_cast<float*>(smem + kPart + 16 * 8 * 4);
+    uint8_t* const xs = smem + ((kHead + 15) & ~15);
+    auto load_b = [&](uint32_t p, v8i (&fb)[kU]) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t k0 = (p + u * KW) * 128 + 16 * q, k1 = k0 + 64;
+        fb[u] = S::load2(rb, k0 < K ? ob + k0 : 0x80000000u, k1 < K ? ob + k1 : 0x80000000u);
+      }
+    };
+    v8i fb[kU];
+    load_b(kw, fb);
+    typename S::Epi e0 = S::epi_cols(g, j0 + 4 * q);
+
+    // amax: wpr waves share a row (8, 4, 2 or 1 for 1, 2, up to 4, more rows)
+    const int wpr = rows == 1 ? 8 : (rows == 2 ? 4 : (rows <= 4 ? 2 : 1));
+    const int sub = wave % wpr;
+    for (int i = wave / wpr; i < rows; i += 8 / wpr) {
+      uint32_t mx = 0;
+      for (uint32_t c = 8 * (64 * sub + lane); c < K; c += 512 * wpr) {
+        float v[8];
+        load8<IN>(fx.x, (int64_t)i * K + c, v);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mx = max(mx, absbits(v[t]));
+      }
+      mx = wave_max_u32(mx);
+      if (lane == 0) red[i * 8 + sub] = mx;
+    }
+    __syncthreads();
+    for (int i = wave / wpr; i < rows; i += 8 / wpr) {
+      uint32_t mx = 0;
+      for (int w = 0; w < wpr; ++w) mx = max(mx, red[i * 8 + w]);
+      const float s = row_scale(mx);
+      const bool ok = mx <= 0x7f7fffffu;
+      if (sub == 0 && lane == 0) {
+        sc[i] = s;
+        if (write) fx.scale[i] = s;
+      }
+      for (uint32_t c = 8 * (64 * sub + lane); c < K; c += 512 * wpr) {
+        float v[8];
+        load8<IN>(fx.x, (int64_t)i * K + c, v);
+        const uint2 w = make_uint2(i8x4(v, s, ok), i8x4(v + 4, s, ok));
+        *reinterpret_cast<uint2*>(xs + i * K + c) = w;
+        if (write) *reinterpret_cast<uint2*>(fx.q + (int64_t)i * K + c) = w;
+      }
+    }
+    __syncthreads();
+
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t p = kw; p < pieces; p += KW * kU) {
+      if (p != (uint32_t)kw) load_b(p, fb);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t k0 = (p + u * KW) * 128 + 16 * q, k1 = k0 + 64;
+        v4i a = {0, 0, 0, 0}, b = a;
+        if (r < rows && k0 < K) a = *reinterpret_cast<const v4i*>(xs + r * K + k0);
+        if (r < rows && k1 < K) b = *reinterpret_cast<const v4i*>(xs + r * K + k1);
+        acc = mma_16x16<kI8, kI8>(fb[u], v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, acc);
+      }
+    }
+    if (KW == 1) {
+      e0.sa = sc[r < rows ? r : 0];
+      S::store(g, r, j0 + 4 * q, acc, e0);
+      return;
+    }
+    v4f* const part = reinterpret_cast<v4f*>(smem);
+    part[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave < JW) {
+      const v4f* src = part + wave * KW * 64 + lane;
+      v4f s = src[0];
+      for (int w = 1; w < KW; ++w) {
+        const v4f o = src[w * 64];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[t] = add_sums<true>(s[t], o[t]);
+      }
+      const int64_t j = jb + wave * kWaveN + 4 * q;
+      typename S::Epi e = S::epi_cols(g, j);
+      e.sa = sc[r < rows ? r : 0];
+      S::store(g, r, j, s, e);
+    }
+  }
+};
+
+template <int IN>
+__global__ __launch_bounds__(512, 4) void skinny_fused_kernel(GemmArgs g, FusedX fx, int KW) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_skinny[];
+  SkinnyFused<IN>::run(g, fx, blockIdx.x == 0, blockIdx.x, KW, smem_skinny);
+}
+
+template <int IN>
+__global__ __launch_bounds__(512, 4) void skinny_fused_groups_kernel(GemmArgs g, Groups gr,
+                                                                     GroupStrides st, FusedX fx,
+                                                                     int KW) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_skinny[];
+  int tm, tn;
+  const GroupSpan sp = rows_work(gr, 16, g.tiles_n, tm, tn);
+  if (sp.e < 0) return;
+  const int64_t row = sp.start + 16 * (int64_t)tm;
+  move_to_rows<true>(g, st, sp, tm, 16);
+  constexpr int eb = IN == kInF32 ? 4 : 2;
+  fx.x = reinterpret_cast<const uint8_t*>(fx.x) + row * g.Kc * eb;
+  fx.q += row * g.Kc;
+  fx.scale += row;
+  SkinnyFused<IN>::run(g, fx, tn == 0, tn, KW, smem_skinny);
+}
 
 // Dense: block = (tile column, tile row); consecutive blocks take the tile
 // rows of one column first, so a B with several tile rows is reread from L2.

@@ -19,6 +19,7 @@ GROUPS = {
     "tail": ([5, 0, 40], 0, 23),
     "front and tail": ([16, 33], 7, 9),
     "all empty": ([0, 0, 0], 0, 5),
+    "few": ([20, 0, 1, 2, 16, 17] + [0, 1] * 20, 0, 3),
     "many": ([i * 7 % 5 for i in range(131)], 0, 1),
 }
 

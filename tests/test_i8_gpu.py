@@ -269,3 +269,53 @@ def test_rows_beyond_one_buffer_resource():
     r, p = R.i8_linear(q, np.ones(len(rows), np.float32), w, sw)
     check_i8(y[torch.tensor(rows, device=DEV)], r, p, "bf16")
     assert not y[M - 129:M - 1].any() and not y[2:M // 2].any()
+
+
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("fp16", "fp16"), ("fp32", "bf16")])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 16), (1, 4096, 4096), (2, 1000, 1040), (3, 72, 16384),
+                                   (4, 136, 11008), (4, 8, 144)])
+def test_few_rows_quantized_in_the_product_launch(M, N, K, dt, out):
+    _linear(M, N, K, dt, out, True)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("K", [32, 1536, 4096])
+def test_grouped_few_rows_of_every_type(K, dt):
+    """Codes, scales and outputs of groups of up to 20 rows, a NaN token and a
+    zero token among them, quantized inside the product's launch."""
+    N = 72
+    T, off = offsets_of("few")
+    E = len(off) - 1
+    assert T <= 2 * E
+    x = _x(T, K, dt)
+    x[3, 5] = float("nan")
+    x[21] = 0
+    w, sw = _weights((E, N, K))
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    x8 = torch.full((T, K), 99, dtype=torch.int8, device=DEV)
+    sx = torch.full((T,), -1.0, device=DEV)
+    F.fp8_i8_grouped_linear_fwd(x.to(DEV), F.QuantizedRows(to_dev(w), to_dev(sw)), None,
+                                offsets_dev(off), y, x8, sx)
+    oq, os = R.i8_quantize_rows(f32(x))
+    used = off[-1]
+    assert np.array_equal(x8.cpu().numpy()[:used], oq[:used])
+    assert np.array_equal(sx.cpu().numpy()[:used], os[:used], equal_nan=True)
+    assert (x8[used:] == 99).all() and (sx[used:] == -1).all() and (y[used:] == 7.0).all()
+    for e, i, j in R.spans(off):
+        if i < j:
+            r, p = R.i8_linear(oq[i:j], os[i:j], w[e], sw[e])
+            check_i8(y[i:j], r, p, "bf16", f"group {e}")
+
+
+@pytest.mark.parametrize("T,K", [(1, 16384), (2, 4096), (2, 4112), (4, 512)])
+def test_one_expert(T, K):
+    """A single group: the grouped call equals the dense one bit for bit."""
+    N = 80
+    x = _x(T, K, "bf16").to(DEV)
+    w, sw = _weights((1, N, K))
+    W, off = to_dev(w), offsets_dev([0, T])
+    y, z = (torch.empty(T, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q, s = torch.empty(T, K, dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    F.fp8_i8_grouped_linear_fwd(x, F.QuantizedRows(W, to_dev(sw)), None, off, y, q, s)
+    F.fp8_i8_linear_fwd(x, F.QuantizedRows(W[0], to_dev(sw[0])), None, z, q, s)
+    assert torch.equal(y, z)
