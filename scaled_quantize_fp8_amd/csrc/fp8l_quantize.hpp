@@ -521,8 +521,20 @@ template <int IN>
 FP8L_DEV uint32_t flat_absmax(const void* x, int64_t n, int vec_ok) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t mx = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kBlockChunk + wave * kWaveChunk; base < n;
-       base += (int64_t)gridDim.x * kBlockChunk) {
+  int64_t base = (int64_t)blockIdx.x * kBlockChunk + wave * kWaveChunk;
+  const int64_t stride = (int64_t)gridDim.x * kBlockChunk;
+  // four chunks' loads in flight: the grid of the dynamic pass is small
+  for (; vec_ok && base + 3 * stride + kWaveChunk <= n; base += 4 * stride) {
+    float v[8][8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      load8<IN>(x, base + (k >> 1) * stride + (k & 1) * 512 + 8 * lane, v[k]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = max(mx, absbits(v[k][i]));
+  }
+  for (; base < n; base += stride) {
     const int64_t e0 = base + 8 * lane, e1 = base + 512 + 8 * lane;
     if (vec_ok && base + kWaveChunk <= n) {
       float v0[8], v1[8];
