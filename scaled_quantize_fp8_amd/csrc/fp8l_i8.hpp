@@ -41,9 +41,9 @@ FP8L_DEV uint32_t i8x4(const float v[4], float s, bool ok) {
 }
 
 // One block of NT threads per row, the row read twice (the second time from
-// cache): 1024 threads where rows are few and long (33 rows of 11008: 3.2 us
+// cache): 1024 threads where rows are few and long (33 rows of 11008: 4.7 us
 // against 5.1 with 256), 256 where many rows share the CUs (4096 x 4096 bf16:
-// 12 us, 4.2 TB/s).
+// 12.6 us, 4.0 TB/s).
 template <int IN, int NT>
 __global__ __launch_bounds__(NT) void quantize_rows_kernel(RowsArgs a) {
   __shared__ uint32_t sh[NT / 64];

@@ -18,6 +18,14 @@
 // waves fill the chip: 1 when there are columns enough, up to 8 for a narrow
 // B.  The KW partial sums meet in LDS and are added in wave order (int32:
 // exactly), so results do not depend on timing.
+//
+// Measured: 24 rows over 19 of 64 experts of 1536 -> 6912 (202 MB of weights
+// and outputs) 43 us, 4.7 TB/s, against 71 us on 128x128 tiles; 16 rows over 13
+// of 16 experts of 4096 -> 11008 in integers 103 us, 5.7 TB/s, against 122;
+// one row of 4096 -> 11008 (45 MB) 12.6 us, where start-up and the two
+// memory round trips of a wave weigh as much as the bandwidth.  Four pieces
+// in flight per wave beat eight (128 registers keep two blocks on a CU: 43
+// against 53 us).
 #pragma once
 
 #include "fp8l_gemm3.hpp"

@@ -358,3 +358,21 @@ def test_gradients_of_gradients_are_refused():
     g, = torch.autograd.grad(m(x, offsets_dev([0, 4, 8])), x, v, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiate twice"):
         g.sum().backward()
+
+
+def test_backward_with_different_weight_and_input_formats():
+    """X8 in e4m3 beside W8 in e5m2 (the gradients' products then run as two
+    launches)."""
+    N, K = 96, 144
+    T, off, E, x8, w8, sx, sw = _operands("edges", N, K, O.E4M3, O.E5M2)
+    g8, sg = random_codes((T, N), 5, O.E5M2), np.float32(3.0)
+    dx, dw, db = _filled(T, K), _filled(E, N, K), _filled(E, N)
+    F.fp8_grouped_linear_bwd(F.Quantized(to_dev(g8), O.E5M2, scalar_dev(sg)), O.E5M2,
+                             offsets_dev(off), F.Quantized(to_dev(x8), O.E4M3, scalar_dev(sx)),
+                             F.Quantized(to_dev(w8), O.E5M2, to_dev(sw)), dx, dw, db)
+    check_groups(dx, R.grouped_dx(g8, O.E5M2, w8, O.E5M2, sg, sw, off), off, "dx")
+    dbs = R.grouped_db(O.dequantized(g8, O.E5M2, sg), off)
+    for e, ref in enumerate(R.grouped_dw(g8, O.E5M2, x8, O.E4M3, sg, sx, off)):
+        if ref is not None:
+            check_gemm(bf16_bits(dw[e]), ref, f"dw {e}")
+            check_gemm(bf16_bits(db[e]), dbs[e], f"db {e}")
