@@ -465,7 +465,7 @@ int fp8_gemm_fp8out(int64_t M, int64_t N, int64_t K, fp8_operand_t a, fp8_operan
  * where they do not, the results of the groups concerned are unspecified
  * and no memory outside the operands is touched.
  * Weights are W [E, N, K], one matrix per expert.
- * Limits: T < 2^31, 1 <= E <= 65535 (FP8_ERR_SHAPE otherwise).
+ * Limits: T < 2^31 - 1024, 1 <= E <= 65535 (FP8_ERR_SHAPE otherwise).
  * Results do not depend on scheduling: the same call gives the same bits.
  * ------------------------------------------------------------------------ */
 

@@ -96,11 +96,13 @@ bool enqueue_groupsum(const fp8_operand_t& x, int64_t T, int64_t N, int32_t fmt,
   const bool local = !ring && n <= kLocalMost;
   if (!local && (!ring || !ring->seeded)) enqueue_amax(x.data, x.dtype, n, ring, amax_out, limit, st);
   const int strips = (int)((N + kColStrip - 1) / kColStrip);
-  const dim3 grid((unsigned)(most_units(T, gr.E, kColRowsPerChunk) * strips));
+  const int most = (int)most_units(T, gr.E, kColRowsPerChunk);
+  // the rows before the first group are one more group
+  const dim3 grid((unsigned)(most_units(T, gr.E + 1, kColRowsPerChunk) * strips));
   auto run = [&](auto in, auto f, auto mode) {
     hipLaunchKernelGGL((quantize_groupsum_kernel<decltype(in)::value, decltype(f)::value,
                                                  decltype(mode)::value>),
-                       grid, dim3(kQThreads), 0, st, a, gr, strips);
+                       grid, dim3(kQThreads), 0, st, a, gr, strips, most);
   };
   auto by_mode = [&](auto in, auto f) {
     if (local) run(in, f, std::integral_constant<int, kScaleLocal>{});

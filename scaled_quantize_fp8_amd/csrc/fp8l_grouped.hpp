@@ -199,11 +199,14 @@ FP8L_DEV uint32_t block_absmax(const QArgs& a, uint32_t* sh) {
 }
 
 // G [T, cols] quantized and summed in one pass (the grouped form of
-// quantize_colsum_kernel: same codes, amax and ring finalize).  Rows of no
-// group are neither read nor written.
+// quantize_colsum_kernel: same codes, amax and ring finalize).  The first
+// chunks are the rows before the first group, quantized like the rest but in
+// no sum; rows behind the last group are neither read nor written.  most:
+// chunks that the workspace holds (offsets that break the contract can give
+// more).
 template <int IN, int FMT, int SMODE>
 __global__ __launch_bounds__(kQThreads) void quantize_groupsum_kernel(QArgs a, Groups gr,
-                                                                      int strips) {
+                                                                      int strips, int most) {
   float s;
   if constexpr (SMODE == kScaleLocal) {
     __shared__ uint32_t sh_amax[kQThreads / 64];
@@ -217,7 +220,9 @@ __global__ __launch_bounds__(kQThreads) void quantize_groupsum_kernel(QArgs a, G
     s = launch_scale<FMT, SMODE>(a);
   }
   const int chunk = blockIdx.x / strips, strip = blockIdx.x % strips;
-  const GroupSpan sp = find_group(gr, kColRowsPerChunk, chunk);
+  const int lead_rows = group_edge(gr, 0), lead = units_of(lead_rows, kColRowsPerChunk);
+  const GroupSpan sp = chunk < lead ? GroupSpan{0, 0, lead_rows, chunk, 0}
+                                    : find_group(gr, kColRowsPerChunk, chunk - lead);
   uint32_t mx = 0;
   if (sp.e >= 0) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -262,7 +267,8 @@ __global__ __launch_bounds__(kQThreads) void quantize_groupsum_kernel(QArgs a, G
         }
       }
     }
-    chunk_sum_store(cs, a.colsum, chunk, strip, a.cols);
+    if (chunk >= lead && chunk - lead < most)
+      chunk_sum_store(cs, a.colsum, chunk - lead, strip, a.cols);
   }
   if constexpr (SMODE != kScaleLocal)
     finish_launch<FMT, SMODE>(a, mx, s, blockIdx.x, gridDim.x);
@@ -293,7 +299,9 @@ FP8L_DEV void db_store(const DbArgs& a, int e, int64_t n, float t) {
 // break the contract) are not read.
 FP8L_DEV void db_from_chunks(const DbArgs& a, const Groups& gr, int e, int strip, float* sh) {
   const GroupSpan sp = group_span(gr, kColRowsPerChunk, e);
-  const int chunks = min(units_of(sp.end - sp.start, kColRowsPerChunk), a.most - sp.before);
+  // (before < 0: such offsets can give more chunks than 32 bits count)
+  const int chunks =
+      sp.before < 0 ? 0 : min(units_of(sp.end - sp.start, kColRowsPerChunk), a.most - sp.before);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t n = (int64_t)strip * 64 + lane;
   float s = 0.0f;

@@ -17,10 +17,11 @@ inline int64_t most_units(int64_t T, int64_t E, int64_t per) {
   return (T + live * (per - 1)) / per;
 }
 
-// Sizes of a grouped call: 32-bit row offsets, and tile numbers of every
+// Sizes of a grouped call: 32-bit row numbers, also of the rows of a tile or
+// of loads in flight that end behind the last row, and tile numbers of every
 // tile choice (units of 16 rows by 16 columns at least) below 2^31.
 inline int check_grouped(int64_t T, int64_t E, int64_t N, int64_t K) {
-  if (T < 0 || T > INT32_MAX || E < 1 || E > 65535 || N < 0 || K < 0) return FP8_ERR_SHAPE;
+  if (T < 0 || T > INT32_MAX - 1024 || E < 1 || E > 65535 || N < 0 || K < 0) return FP8_ERR_SHAPE;
   if (N > INT32_MAX || K > INT32_MAX) return FP8_ERR_SHAPE;
   if (!mul_ok(T, K) || !mul_ok(T, N) || !mul_ok(N, K) || !mul_ok(N * K, E)) return FP8_ERR_SHAPE;
   const int64_t un = (N + 127) / 128, uk = (K + 127) / 128;

@@ -350,6 +350,46 @@ def test_small_dynamic_quantize_matches_the_general_one():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt,N", [(torch.bfloat16, 80), (torch.float32, 33)])
+@pytest.mark.parametrize("hist", [None, 16, 100])
+@pytest.mark.parametrize("front", [1, 32, 45])
+def test_rows_before_the_first_group_are_quantized(front, hist, dt, N):
+    """G over [0, offsets[E]), its largest value before the first group: codes,
+    scale, amax and ring are the oracle's with db and without it (in two
+    steps), and no sum holds those rows."""
+    off, T, K = [front, front + 16, front + 16, front + 49], front + 58, 32
+    E, used = len(off) - 1, off[-1]
+    x8, w8 = random_codes((T, K), 1, O.E4M3), random_codes((E, N, K), 2, O.E4M3)
+    for with_db in (True, False):
+        ring = None if hist is None else F.ScaleRing(hist)
+        oring = None if hist is None else O.ScaleRing(hist)
+        for step in range(2):
+            G = bf16((T, N), 1e-2 * (1 + step), 30 + step).to(dt)
+            G[front - 1, N // 2] = 0.5 + step
+            G[used:] = float("nan")
+            g8 = torch.full((T, N), 0xAA, dtype=torch.uint8, device=DEV)
+            sg, ag = (torch.empty(1, dtype=torch.float32, device=DEV) for _ in range(2))
+            dw = _filled(E, N, K)
+            db = _filled(E, N) if with_db else None
+            ws = torch.full((F.fp8_grouped_db_workspace_bytes(T, E, N),), 0xFF, dtype=torch.uint8,
+                            device=DEV)
+            F.fp8_grouped_linear_bwd(G.to(DEV), O.E5M2, offsets_dev(off),
+                                     F.Quantized(to_dev(x8), O.E4M3, scalar_dev(1)),
+                                     F.Quantized(to_dev(w8), O.E4M3, scalar_dev(1)), None, dw, db,
+                                     ws, ring, g8, sg, ag)
+            og, osg, oag = O.quantize_step(f32(G)[:used], O.E5M2, oring)
+            assert np.array_equal(u8(g8)[:used], og) and (u8(g8)[used:] == 0xAA).all()
+            assert f32_scalar(sg) == np.float32(osg) and f32_scalar(ag) == np.float32(oag)
+            if ring is not None:
+                assert_ring_matches(ring, oring)
+            if with_db:
+                for e, ref in enumerate(R.grouped_db(f32(G)[:used].astype(np.float64), off)):
+                    if ref is None or off[e] == off[e + 1]:
+                        assert not db[e].any()
+                    else:
+                        check_gemm(bf16_bits(db[e]), ref, f"db {e}")
+
+
 def test_gradients_of_gradients_are_refused():
     from scaled_quantize_fp8_amd.autograd import Fp8GroupedLinear
     m = Fp8GroupedLinear(2, 32, 32, device=DEV)

@@ -44,6 +44,14 @@ def test_grouped_sizes(lib, call):
     assert call(lib, off=Z) == F.FP8_ERR_NULL
 
 
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_grouped_row_numbers_end_a_tile_below_32_bits(lib, call):
+    """T so large that the rows of a last tile, or of loads in flight behind
+    it, would pass 2^31 is refused whatever the tile numbers are."""
+    for T in ((1 << 31) - 17, (1 << 31) - 256, (1 << 31) - 1024):
+        assert call(lib, T=T, E=1, N=1, K=1) == F.FP8_ERR_SHAPE, T
+
+
 def test_grouped_fwd_refusals(lib):
     assert _fwd(lib, fmt=7) == F.FP8_ERR_DTYPE
     assert _fwd(lib, x=_op(E5)) == F.FP8_ERR_DTYPE
