@@ -284,7 +284,8 @@ void launch_gemm3_t(GemmArgs& g, hipStream_t st) {
 
 // FP8L_TILE forces a tile configuration (for sweeps and tests): 256x256,
 // 256x128, 128x128 or v1 (the general register-staged kernel).  Read at
-// every launch so one process can compare configurations.
+// every launch so one process can compare configurations.  A name that the
+// layer at hand has no kernel for leaves its automatic choice.
 int forced_tile() {
   const char* e = getenv("FP8L_TILE");
   if (!e) return kTileAuto;
@@ -300,6 +301,12 @@ int forced_tile() {
   if (!strcmp(e, "skinny48")) return kTileSkinny48;
   if (!strcmp(e, "skinny64")) return kTileSkinny64;
   return kTileAuto;
+}
+
+// The same for the dense FP8 GEMMs, which take the first six only.
+int forced_dense_tile() {
+  const int t = forced_tile();
+  return t >= kTile128x256 ? kTileAuto : t;
 }
 
 // Tile choice (measured crossovers on the layer shapes; tiles counted over
@@ -422,7 +429,7 @@ bool fast_path_ok(const GemmArgs& g) {
 
 template <int LA, int LB>
 void launch_gemm_l(GemmArgs& g, int fa, int fb, hipStream_t st) {
-  int tile = forced_tile();
+  int tile = forced_dense_tile();
   if (!fast_path_ok<LA, LB>(g)) tile = kTileV1;
   if (tile == kTileAuto) tile = choose_tile(g.Mc, g.Nc, g.Kc, g.batch);
   switch (tile) {
@@ -474,7 +481,8 @@ void launch_pair_t(GemmArgs& dx, GemmArgs& dw, hipStream_t st) {
 // standard recipe's formats (G in e5m2, W8 and X8 in e4m3) and no tile
 // forced; false: the caller launches them one by one.
 bool launch_pair(GemmArgs& dx, GemmArgs& dw, int fmt_g, int fmt_w, int fmt_x, hipStream_t st) {
-  if (fmt_g != kE5M2 || fmt_w != kE4M3 || fmt_x != kE4M3 || forced_tile() != kTileAuto) return false;
+  if (fmt_g != kE5M2 || fmt_w != kE4M3 || fmt_x != kE4M3 || forced_dense_tile() != kTileAuto)
+    return false;
   if (dx.batch != 1 || dw.batch != 1) return false;
   if (!fast_path_ok<kKContig, kCross>(dx) || !fast_path_ok<kCross, kCross>(dw)) return false;
   const int tx = choose_tile(dx.Mc, dx.Nc, dx.Kc, 1), tw = choose_tile(dw.Mc, dw.Nc, dw.Kc, 1);

@@ -129,6 +129,7 @@ inline RingFold fold_of(const fp8_ring_t* r, int32_t fmt, float* amax_out) {
 
 inline int hip_status() { return hipGetLastError() == hipSuccess ? FP8_OK : FP8_ERR_HIP; }
 
+// Tile choices; from kTile128x256 on of the grouped and integer layers only.
 enum { kTileAuto = 0, kTile256x256, kTile256x128, kTile128x128, kTileV1, kTile256x256w8, kTile128x128w8,
        kTile128x256,
        kTileSkinny16, kTileSkinny32, kTileSkinny48, kTileSkinny64,
