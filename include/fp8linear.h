@@ -465,7 +465,12 @@ int fp8_gemm_fp8out(int64_t M, int64_t N, int64_t K, fp8_operand_t a, fp8_operan
  * where they do not, the results of the groups concerned are unspecified
  * and no memory outside the operands is touched.
  * Weights are W [E, N, K], one matrix per expert.
- * Limits: T < 2^31 - 1024, 1 <= E <= 65535 (FP8_ERR_SHAPE otherwise).
+ * Limits (FP8_ERR_SHAPE otherwise): T < 2^31 - 1024, 1 <= E <= 65535, and
+ * each launch's blocks below 2^24 - 8 (a grid takes fewer than 2^32 threads):
+ * (T / 128 + min(E, T)) N / 128 for Y, the same with K for dX, E times the
+ * 128x128 tiles of an expert's dW, E N / 64 for db (of codes E N / 256), and
+ * (T / 32 + min(E + 1, T)) N / 256 for db of a high-precision G, every
+ * quotient rounded up.
  * Results do not depend on scheduling: the same call gives the same bits.
  * ------------------------------------------------------------------------ */
 
@@ -520,6 +525,7 @@ int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
  * output channel (serving).  Codes are int8, scales are quantization
  * multipliers (q ~ x s), as everywhere in this library.  The integer sums
  * are exact: K <= 131071 keeps them inside int32 (FP8_ERR_SHAPE beyond).
+ * Y has fewer than 2^24 - 8 tiles of 128x128 (FP8_ERR_SHAPE otherwise).
  * ------------------------------------------------------------------------ */
 
 /*

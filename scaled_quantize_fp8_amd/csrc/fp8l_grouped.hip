@@ -15,9 +15,9 @@ __global__ __launch_bounds__(256) void grouped_db_kernel(DbArgs a, Groups gr) {
   db_block(a, gr, blockIdx.x, sh);
 }
 
-int db_blocks(const DbArgs& a, const Groups& gr) {
+int64_t db_blocks(const DbArgs& a, const Groups& gr) {
   const int width = a.ws ? 64 : 256;
-  return a.db ? (int)((a.N + width - 1) / width) * gr.E : 0;
+  return a.db ? (a.N + width - 1) / width * gr.E : 0;
 }
 
 template <class Tile>
@@ -26,7 +26,7 @@ void launch_contract(GemmArgs& g, const Groups& gr, const GroupStrides& s, hipSt
   set_lds_limit((const void*)grouped_contract_kernel<Tile>, Tile::kLds, lds_set);
   g.tiles_m = (int32_t)((g.Mc + Tile::kBM - 1) / Tile::kBM);
   g.tiles_n = (int32_t)((g.Nc + Tile::kBN - 1) / Tile::kBN);
-  const int pad = (g.tiles_m * g.tiles_n + 7) & ~7;
+  const int pad = (int)contract_pad(g, Tile::kBM, Tile::kBN);
   hipLaunchKernelGGL((grouped_contract_kernel<Tile>), dim3((unsigned)gr.E * (unsigned)pad),
                      dim3(Tile::kThreads), Tile::kLds, st, g, gr, s, pad);
 }
@@ -69,6 +69,12 @@ void launch_dw(GemmArgs& g, int fa, int fb, const Groups& gr, const GroupStrides
   });
 }
 
+// Blocks of the quantize with column sums; the rows before the first group
+// are one more group.
+int64_t groupsum_blocks(int64_t T, int64_t E, int64_t N) {
+  return most_units(T, E + 1, kColRowsPerChunk) * ((N + kColStrip - 1) / kColStrip);
+}
+
 // The quantize of G with the groups' column sums in the same pass; scale
 // modes as enqueue_quant (fp8l_api.hip).  Returns whether the fold of the
 // ring was left to the caller's next GEMM.
@@ -97,8 +103,7 @@ bool enqueue_groupsum(const fp8_operand_t& x, int64_t T, int64_t N, int32_t fmt,
   if (!local && (!ring || !ring->seeded)) enqueue_amax(x.data, x.dtype, n, ring, amax_out, limit, st);
   const int strips = (int)((N + kColStrip - 1) / kColStrip);
   const int most = (int)most_units(T, gr.E, kColRowsPerChunk);
-  // the rows before the first group are one more group
-  const dim3 grid((unsigned)(most_units(T, gr.E + 1, kColRowsPerChunk) * strips));
+  const dim3 grid((unsigned)groupsum_blocks(T, gr.E, N));
   auto run = [&](auto in, auto f, auto mode) {
     hipLaunchKernelGGL((quantize_groupsum_kernel<decltype(in)::value, decltype(f)::value,
                                                  decltype(mode)::value>),
@@ -123,22 +128,24 @@ bool enqueue_groupsum(const fp8_operand_t& x, int64_t T, int64_t N, int32_t fmt,
 }
 
 // dX, dW and db in one launch with one tile shape, where both GEMMs can take
-// a pipelined tile; false: the caller launches them one by one.
+// a pipelined tile and the grid takes all three; false: the caller launches
+// them one by one.
 template <class TX, class TW>
-void launch_bwd_t(GemmArgs& gx, GemmArgs& gw, const Groups& gr, const GroupStrides& sx,
+bool launch_bwd_t(GemmArgs& gx, GemmArgs& gw, const Groups& gr, const GroupStrides& sx,
                   const GroupStrides& sw, const GroupedSide& side, const DbArgs& db,
                   hipStream_t st) {
-  static std::atomic<bool> lds_set[64];
-  set_lds_limit((const void*)grouped_bwd_kernel<TX, TW>, TX::kLds, lds_set);
   gx.tiles_n = (int32_t)((gx.Nc + TX::kBN - 1) / TX::kBN);
   gw.tiles_m = (int32_t)((gw.Mc + TW::kBM - 1) / TW::kBM);
   gw.tiles_n = (int32_t)((gw.Nc + TW::kBN - 1) / TW::kBN);
   const int64_t nx = (most_units(gr.T, gr.E, TX::kBM) * gx.tiles_n + 7) & ~7LL;
-  const int64_t pad = (gw.tiles_m * gw.tiles_n + 7) & ~7;
-  const int64_t nw = pad * gr.E;
-  hipLaunchKernelGGL((grouped_bwd_kernel<TX, TW>), dim3((unsigned)(nx + nw + db_blocks(db, gr))),
-                     dim3(TX::kThreads), TX::kLds, st, gx, gw, gr, sx, sw, side, (int)nx, (int)nw,
-                     (int)pad, db);
+  const int64_t pad = contract_pad(gw, TW::kBM, TW::kBN);
+  const int64_t nw = pad * gr.E, blocks = nx + nw + db_blocks(db, gr);
+  if (!grid_fits(blocks, TX::kThreads)) return false;
+  static std::atomic<bool> lds_set[64];
+  set_lds_limit((const void*)grouped_bwd_kernel<TX, TW>, TX::kLds, lds_set);
+  hipLaunchKernelGGL((grouped_bwd_kernel<TX, TW>), dim3((unsigned)blocks), dim3(TX::kThreads),
+                     TX::kLds, st, gx, gw, gr, sx, sw, side, (int)nx, (int)nw, (int)pad, db);
+  return true;
 }
 
 bool launch_bwd(GemmArgs& gx, GemmArgs& gw, int fg, int fw, const Groups& gr,
@@ -149,19 +156,20 @@ bool launch_bwd(GemmArgs& gx, GemmArgs& gw, int fg, int fw, const Groups& gr,
   if (tile == kTileV1) return false;
   if (tile != kTile128x128w8 && tile != kTile128x256 && tile != kTile256x256w8)
     tile = pick_bwd(gx, gw, gr);
+  bool done = false;
   by_formats(fg, fw, [&](auto a, auto b) {
     constexpr int FG = decltype(a)::value, FW = decltype(b)::value;
     if (tile == kTile128x128w8)
-      launch_bwd_t<Tile128<kKContig, kCross, FG, FW>, Tile128<kCross, kCross, FG, FW>>(
+      done = launch_bwd_t<Tile128<kKContig, kCross, FG, FW>, Tile128<kCross, kCross, FG, FW>>(
           gx, gw, gr, sx, sw, side, db, st);
     else if (tile == kTile128x256)
-      launch_bwd_t<Tile128x256<kKContig, kCross, FG, FW>, Tile128x256<kCross, kCross, FG, FW>>(
+      done = launch_bwd_t<Tile128x256<kKContig, kCross, FG, FW>, Tile128x256<kCross, kCross, FG, FW>>(
           gx, gw, gr, sx, sw, side, db, st);
     else
-      launch_bwd_t<Tile256<kKContig, kCross, FG, FW>, Tile256<kCross, kCross, FG, FW>>(
+      done = launch_bwd_t<Tile256<kKContig, kCross, FG, FW>, Tile256<kCross, kCross, FG, FW>>(
           gx, gw, gr, sx, sw, side, db, st);
   });
-  return true;
+  return done;
 }
 
 }  // namespace
@@ -184,6 +192,7 @@ int fp8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
                            float* amax_x, float* amax_w, hipStream_t stream) {
   int st = check_grouped(T, E, N, K);
   if (st) return st;
+  if (!rows_grid_fits(T, E, N)) return FP8_ERR_SHAPE;
   if (!valid_fmt(fmt)) return FP8_ERR_DTYPE;
   if (!offsets) return FP8_ERR_NULL;
   const int32_t f8dt = fmt_dtype(fmt);
@@ -303,7 +312,13 @@ int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
   if (db && N > 0) {
     da.db = reinterpret_cast<uint16_t*>(db);
     da.N = N;
+    da.ws = sums ? db_ws : nullptr;
   }
+  // every launch below must fit its grid (see grid_fits)
+  if ((have_dx && !rows_grid_fits(T, E, K)) || !grid_fits(db_blocks(da, gr), 256) ||
+      (have_dw && !grid_fits((((N + kBM - 1) / kBM) * ((K + kBN - 1) / kBN) + 7) * E, kGThreads)) ||
+      (sums && !grid_fits(groupsum_blocks(T, E, N), kQThreads)))
+    return FP8_ERR_SHAPE;
   if (hp) {
     const RowLimit limit = {offsets + E, T, N};
     bool fold = false;
@@ -317,7 +332,6 @@ int fp8_grouped_linear_bwd(int64_t T, int32_t E, int64_t N, int64_t K, const int
     if (fold) side.fold[0] = fold_of(ring_g, fmt_g, amax_g);
     g8 = g8_out;
     sg = sg_used;
-    da.ws = db_ws;
     da.most = (int32_t)most_units(T, E, kColRowsPerChunk);
   } else {
     g8 = reinterpret_cast<const uint8_t*>(g.data);

@@ -31,6 +31,14 @@ inline int check_grouped(int64_t T, int64_t E, int64_t N, int64_t K) {
   return FP8_OK;
 }
 
+// A launch takes fewer than 2^32 threads.  The general tile, which has the
+// fewest per output (256 for 128x128), stands in where a chosen tile's blocks
+// would be too many; a call that is too large for it is refused.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks + 8 < (1LL << 32) / threads; }
+inline bool rows_grid_fits(int64_t T, int64_t E, int64_t N) {
+  return grid_fits(most_units(T, E, kBM) * ((N + kBN - 1) / kBN), kGThreads);
+}
+
 inline void finish_grouped_args(GemmArgs& g, const GroupStrides& s) {
   g.batch = 1;
   g.a_vec = aligned16(g.a) && g.lda % 16 == 0;
@@ -65,6 +73,16 @@ inline int skinny_kw(int64_t waves, int64_t K) {
                     (waves * kw < 1024 && 2 * pieces > kw)))
     kw *= 2;
   return kw;
+}
+
+// Rows of a skinny choice's tiles.
+inline int skinny_rows(int tile) {
+  switch (tile) {
+    case kTileSkinny16: case kTileSkinny16Any: return 16;
+    case kTileSkinny32: case kTileSkinny32Any: return 32;
+    case kTileSkinny48: return 48;
+    default: return 64;
+  }
 }
 
 // Microseconds of a launch of `tiles` tiles with contraction K, from fits to
@@ -125,7 +143,6 @@ inline double expected_units(int64_t T, int64_t E, int64_t per) {
 inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   const double u128 = expected_units(T, E, 128), u256 = expected_units(T, E, 256);
   const double n128 = (double)((N + 127) / 128), n256 = (double)((N + 255) / 256);
-  skinny = skinny && (T + 15) / 16 < INT32_MAX / ((N + 15) / 16 + 1);  // tile numbers
   double us = 0;
   int best = pick_of(u128 * n128, u128 * n256, u256 * n256, (double)K, &us);
   for (int mt = 1; skinny && mt <= 4; ++mt) {
@@ -142,7 +159,6 @@ inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
 inline int pick_any(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   const double cus = cu_count(), steps = (double)((K + 127) / 128);
   const double tiles = expected_units(T, E, 128) * (double)((N + 127) / 128);
-  skinny = skinny && (T + 15) / 16 < INT32_MAX / ((N + 15) / 16 + 1);  // tile numbers
   double us = 5 + (tiles <= cus ? 2.5 : 3.3 * (tiles / (2 * cus) + 0.5)) * steps;
   int best = kTileV1;
   const int mts[3] = {1, 2, 4}, ids[3] = {kTileSkinny16Any, kTileSkinny32Any, kTileSkinny64Any};
@@ -153,15 +169,36 @@ inline int pick_any(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   return best;
 }
 
+// The tile itself, or the general one where its grid would be too large.
+inline int tile_that_fits(int tile, int64_t T, int64_t E, int64_t N, int64_t K) {
+  int64_t blocks = 0;
+  switch (tile) {
+    case kTile128x128w8: blocks = most_units(T, E, 128) * ((N + 127) / 128); break;
+    case kTile128x256: blocks = most_units(T, E, 128) * ((N + 255) / 256); break;
+    case kTile256x256w8: blocks = most_units(T, E, 256) * ((N + 255) / 256); break;
+    case kTileV1: return tile;
+    default: {  // skinny, of skinny_rows() rows
+      const int64_t units = most_units(T, E, skinny_rows(tile)), cols = (N + 15) / 16;
+      const int jw = 8 / skinny_kw(units * cols, K);
+      blocks = units * ((cols + jw - 1) / jw);
+    }
+  }
+  return grid_fits(blocks, tile == kTile128x256 ? 256 : 512) ? tile : kTileV1;
+}
+
 // Tile of a rows launch.
 template <int LB>
 int rows_tile(const GemmArgs& g, const Groups& gr, const GroupStrides& s) {
   const int f = forced_tile();
+  int tile;
   if (!rows_fast_ok<LB>(g, s))
-    return f == kTileV1 ? f : pick_any(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
-  if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8) return f;
-  if (LB == kKContig && f >= kTileSkinny16) return f;
-  return pick_tile(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
+    tile = f == kTileV1 ? f : pick_any(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
+  else if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8 ||
+           (LB == kKContig && f >= kTileSkinny16))
+    tile = f;
+  else
+    tile = pick_tile(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
+  return tile_that_fits(tile, gr.T, gr.E, g.Nc, g.Kc);
 }
 
 // Tile of a contract launch, by the mean group (4093 rows in 32 groups, dW of
@@ -172,14 +209,22 @@ inline bool contract_fast_ok(const GemmArgs& g) {
          g.ldb % 16 == 0 && (g.Kc + 256) * g.lda < (1LL << 31) &&
          (g.Kc + 256) * g.ldb < (1LL << 31);
 }
+// Blocks of one group: its tiles of bm x bn, rounded up to 8.
+inline int64_t contract_pad(const GemmArgs& g, int bm, int bn) {
+  return ((((g.Mc + bm - 1) / bm) * ((g.Nc + bn - 1) / bn)) + 7) & ~7LL;
+}
 inline int contract_tile(const GemmArgs& g, const Groups& gr) {
   if (!contract_fast_ok(g)) return kTileV1;
-  const int f = forced_tile();
-  if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8) return f;
-  const double m128 = (double)((g.Mc + 127) / 128) * gr.E, m256 = (double)((g.Mc + 255) / 256) * gr.E;
-  const double n128 = (double)((g.Nc + 127) / 128), n256 = (double)((g.Nc + 255) / 256);
-  double us = 0;
-  return pick_of(m128 * n128, m128 * n256, m256 * n256, (double)gr.T / gr.E, &us);
+  int tile = forced_tile();
+  if (tile == kTileV1) return tile;
+  if (tile != kTile128x128w8 && tile != kTile128x256 && tile != kTile256x256w8) {
+    const double m128 = (double)((g.Mc + 127) / 128) * gr.E, m256 = (double)((g.Mc + 255) / 256) * gr.E;
+    const double n128 = (double)((g.Nc + 127) / 128), n256 = (double)((g.Nc + 255) / 256);
+    double us = 0;
+    tile = pick_of(m128 * n128, m128 * n256, m256 * n256, (double)gr.T / gr.E, &us);
+  }
+  const int bm = tile == kTile256x256w8 ? 256 : 128, bn = tile == kTile128x128w8 ? 128 : 256;
+  return grid_fits(contract_pad(g, bm, bn) * gr.E, tile == kTile128x256 ? 256 : 512) ? tile : kTileV1;
 }
 
 // One tile shape for dX and dW in a shared launch: the smallest sum.

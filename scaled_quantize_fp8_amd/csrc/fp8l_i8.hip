@@ -36,9 +36,12 @@ void launch_i8_t(GemmArgs& g, hipStream_t st) {
 
 int i8_tile(const GemmArgs& g) {
   const int f = forced_tile();
-  if (!rows_fast_ok<kKContig>(g, GroupStrides{})) return f == kTileV1 ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
-  if (f == kTileV1 || f >= kTile256x256w8) return f;
-  return pick_tile(g.Mc, 1, g.Nc, g.Kc, true);
+  int tile;
+  if (!rows_fast_ok<kKContig>(g, GroupStrides{}))
+    tile = f == kTileV1 ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
+  else
+    tile = f == kTileV1 || f >= kTile256x256w8 ? f : pick_tile(g.Mc, 1, g.Nc, g.Kc, true);
+  return tile_that_fits(tile, g.Mc, 1, g.Nc, g.Kc);
 }
 
 // Calls f(integral_constant) for a high-precision input type.
@@ -173,7 +176,8 @@ int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_oper
                       hipStream_t stream) {
   if (M < 0 || N < 0 || K < 0) return FP8_ERR_SHAPE;
   if (!mul_ok(M, K) || !mul_ok(N, K) || !mul_ok(M, N)) return FP8_ERR_SHAPE;
-  if (((M + 127) / 128) > INT32_MAX / ((N + 127) / 128 + 1)) return FP8_ERR_SHAPE;
+  if (((M + 127) / 128) > INT32_MAX / ((N + 127) / 128 + 1) || !rows_grid_fits(M, 1, N))
+    return FP8_ERR_SHAPE;
   const int st = check_i8(M, N, K, x, w, out_dtype, y, x8_out, sx_out);
   if (st) return st;
   GemmArgs g = i8_args(M, N, K, x, w, bias, out_dtype, y, x8_out, sx_out);
@@ -209,6 +213,7 @@ int fp8_i8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const 
                               hipStream_t stream) {
   int st = check_grouped(T, E, N, K);
   if (st) return st;
+  if (!rows_grid_fits(T, E, N)) return FP8_ERR_SHAPE;
   if (!offsets) return FP8_ERR_NULL;
   if ((st = check_i8(T, N, K, x, w, out_dtype, y, x8_out, sx_out))) return st;
   GemmArgs g = i8_args(T, N, K, x, w, bias, out_dtype, y, x8_out, sx_out);

@@ -319,3 +319,19 @@ def test_one_expert(T, K):
     F.fp8_i8_grouped_linear_fwd(x, F.QuantizedRows(W, to_dev(sw)), None, off, y, q, s)
     F.fp8_i8_linear_fwd(x, F.QuantizedRows(W[0], to_dev(sw[0])), None, z, q, s)
     assert torch.equal(y, z)
+
+
+def test_a_grid_larger_than_2_to_the_32_threads():
+    """2^30 output channels of one weight each: the tile that few rows take
+    would need 2^32 threads, so the general one runs."""
+    N = (1 << 30) + 5
+    i = torch.arange(N, dtype=torch.int32, device=DEV)
+    w = (i % 251 - 125).to(torch.int8)
+    sw = torch.full((N,), 0.5, device=DEV)
+    y = torch.full((1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    F.fp8_i8_linear_fwd(F.QuantizedRows(torch.full((1, 1), 3, dtype=torch.int8, device=DEV),
+                                        torch.full((1,), 2.0, device=DEV)),
+                        F.QuantizedRows(w.view(N, 1), sw), None, y)
+    # 3 w / (2 * 0.5): at most 375, rounded once
+    for c in range(0, N, 1 << 28):
+        assert torch.equal(y[0, c:c + (1 << 28)], (3 * w[c:c + (1 << 28)].float()).to(torch.bfloat16))

@@ -220,3 +220,29 @@ def test_int8_module_refuses_gradients():
     torch.nn.Module.__init__(m)
     with pytest.raises(RuntimeError, match="no gradient"):
         m.forward(torch.zeros(2, 4, requires_grad=True))
+
+
+# ---------------------------------------------------------------- launch sizes
+
+MANY = dict(T=65535, E=65535)  # one row per expert: every expert has its own tiles
+
+
+def test_products_of_too_many_tiles_are_refused(lib):
+    """A grid takes fewer than 2^32 threads: sizes whose general tiles (256
+    threads for 128x128) pass that are refused before anything is enqueued."""
+    assert _fwd(lib, **MANY, N=32896) == F.FP8_ERR_SHAPE        # 65535 x 257 tiles
+    assert _fwd(lib, **MANY, N=32896, x=_op(BF), w=_op(BF)) == F.FP8_ERR_SHAPE
+    assert _glin(lib, M=65535, E=65535, N=32896) == F.FP8_ERR_SHAPE
+    assert _lin(lib, M=1, N=1 << 31, K=1) == F.FP8_ERR_SHAPE    # 2^24 tiles
+    assert _lin(lib, M=(1 << 31) - 128, N=1, K=1) == F.FP8_ERR_SHAPE
+
+
+def test_gradients_of_too_many_tiles_are_refused(lib):
+    alone = dict(dx=Z, dw=Z, db=Z)
+    assert _bwd(lib, **MANY, N=16, K=32896, **{**alone, "dx": P}) == F.FP8_ERR_SHAPE
+    assert _bwd(lib, T=8, E=65535, N=2048, K=2048, **{**alone, "dw": P}) == F.FP8_ERR_SHAPE
+    # db: 64 columns a block from the chunk sums, 256 from codes
+    assert _bwd(lib, T=8, E=65535, N=16448, K=16, g=_op(BF), **{**alone, "db": P}) == F.FP8_ERR_SHAPE
+    assert _bwd(lib, T=8, E=65535, N=65792, K=16, **{**alone, "db": P}) == F.FP8_ERR_SHAPE
+    # the quantize's chunks of 32 rows by 256 columns
+    assert _bwd(lib, T=1 << 29, E=1, N=8, K=16, g=_op(BF), **{**alone, "db": P}) == F.FP8_ERR_SHAPE
