@@ -300,6 +300,9 @@ int forced_tile() {
   if (!strcmp(e, "skinny32")) return kTileSkinny32;
   if (!strcmp(e, "skinny48")) return kTileSkinny48;
   if (!strcmp(e, "skinny64")) return kTileSkinny64;
+  if (!strcmp(e, "skinny16any")) return kTileSkinny16Any;  // any size and alignment
+  if (!strcmp(e, "skinny32any")) return kTileSkinny32Any;
+  if (!strcmp(e, "skinny64any")) return kTileSkinny64Any;
   return kTileAuto;
 }
 

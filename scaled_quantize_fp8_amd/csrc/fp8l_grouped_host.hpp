@@ -192,7 +192,8 @@ int rows_tile(const GemmArgs& g, const Groups& gr, const GroupStrides& s) {
   const int f = forced_tile();
   int tile;
   if (!rows_fast_ok<LB>(g, s))
-    tile = f == kTileV1 ? f : pick_any(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
+    tile = f == kTileV1 || (LB == kKContig && f >= kTileSkinny16Any) ? f
+                        : pick_any(gr.T, gr.E, g.Nc, g.Kc, LB == kKContig);
   else if (f == kTileV1 || f == kTile128x128w8 || f == kTile128x256 || f == kTile256x256w8 ||
            (LB == kKContig && f >= kTileSkinny16))
     tile = f;

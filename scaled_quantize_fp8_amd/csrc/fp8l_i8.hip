@@ -38,7 +38,7 @@ int i8_tile(const GemmArgs& g) {
   const int f = forced_tile();
   int tile;
   if (!rows_fast_ok<kKContig>(g, GroupStrides{}))
-    tile = f == kTileV1 ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
+    tile = f == kTileV1 || f >= kTileSkinny16Any ? f : pick_any(g.Mc, 1, g.Nc, g.Kc, true);
   else
     tile = f == kTileV1 || f >= kTile256x256w8 ? f : pick_tile(g.Mc, 1, g.Nc, g.Kc, true);
   return tile_that_fits(tile, g.Mc, 1, g.Nc, g.Kc);
