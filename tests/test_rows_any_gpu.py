@@ -148,3 +148,23 @@ def test_int8_groups(N, K, by, tile, monkeypatch):
         if i < j:
             check_i8(y[i:j], *R.i8_linear(oq[i:j], os[i:j], w[e], sw[e], f32(b)[e]), "bf16", f"group {e}")
     assert (y[OFF[-1]:] == SENTINEL).all() and (x8[OFF[-1]:] == 99).all() and (sx[OFF[-1]:] == -1).all()
+
+
+@pytest.mark.parametrize("by_x,by_w", [(0, 0), (0, 1), (3, 0)])
+@pytest.mark.parametrize("N,K", [(130, 1040), (77, 96)])
+def test_general_tile_with_one_operand_unaligned(N, K, by_x, by_w, monkeypatch):
+    """Both operands on 16-byte boundaries, or one of them off."""
+    _tile(monkeypatch, "v1")
+    x8, w8, sw, b, refs = _fp8(N, K, O.E4M3)
+    y = _filled((T, N), 0)
+    F.fp8_grouped_linear_fwd(F.Quantized(_off(x8, by_x), O.E4M3, scalar_dev(1.5)),
+                             F.Quantized(_off(w8, by_w), O.E4M3, to_dev(sw)), b.to(DEV),
+                             offsets_dev(OFF), O.E4M3, y)
+    check_groups(y, refs, OFF, "y")
+    for e in (2, 5):  # the dense layers' general tile
+        i, j = OFF[e], OFF[e + 1]
+        c = _filled((j - i, N), 0)
+        F.fp8_gemm(F.Quantized(_off(x8[i:j], by_x), O.E4M3, scalar_dev(1.5)),
+                   F.Quantized(_off(w8[e], by_w), O.E4M3, scalar_dev(sw[e])), c)
+        check_gemm(bf16_bits(c), R.grouped_fwd(x8[i:j], w8[e][None], O.E4M3, np.float32(1.5),
+                                               sw[e:e + 1], [0, j - i])[0], f"dense {e}")
