@@ -200,10 +200,6 @@ __global__ __launch_bounds__(64) void ring_fold2_kernel(RingFold f0, RingFold f1
   ring_fold_wave(f1);
 }
 
-void enqueue_fold(const RingFold& f, hipStream_t st) {
-  hipLaunchKernelGGL(ring_fold_kernel, dim3(1), dim3(64), 0, st, f);
-}
-
 // One quantize.  may_defer: the caller launches a GEMM on the codes next,
 // on the same stream, which folds the ring when this returns true.
 bool enqueue_quant(const void* x, int32_t in_dtype, int64_t n, int32_t fmt, uint8_t* q,
@@ -219,7 +215,8 @@ bool enqueue_quant(const void* x, int32_t in_dtype, int64_t n, int32_t fmt, uint
     enqueue_quant_in<kInF16>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only, limit);
   else
     enqueue_quant_in<kInBF16>(x, n, fmt, q, ring, scale_used, amax_out, cs, st, groups_only, limit);
-  if (fold_after) enqueue_fold(fold_of(ring, fmt, amax_out), st);
+  if (fold_after)
+    hipLaunchKernelGGL(ring_fold_kernel, dim3(1), dim3(64), 0, st, fold_of(ring, fmt, amax_out));
   return defer;
 }
 
@@ -1008,7 +1005,7 @@ int fp8_gemm(int64_t batch, int64_t M, int64_t N, int64_t K, fp8_operand_t a, in
   if (batch < 0 || M < 0 || N < 0 || K < 0 || stride_a < 0 || stride_b < 0 || stride_c < 0)
     return FP8_ERR_SHAPE;
   if (batch > 65535) return FP8_ERR_SHAPE;
-  if (!is_fp8_dtype(a.dtype) || !is_fp8_dtype(b.dtype)) return FP8_ERR_DTYPE;
+  if (!is_f8(a.dtype) || !is_f8(b.dtype)) return FP8_ERR_DTYPE;
   if ((layout_a != FP8_K_CONTIG && layout_a != FP8_K_STRIDED) ||
       (layout_b != FP8_K_CONTIG && layout_b != FP8_K_STRIDED))
     return FP8_ERR_DTYPE;
@@ -1070,7 +1067,7 @@ int fp8_gemm_fp8out(int64_t M, int64_t N, int64_t K, fp8_operand_t a, fp8_operan
                     float* scale_used, float* amax_out, hipStream_t stream) {
   if (M < 0 || N < 0 || K < 0) return FP8_ERR_SHAPE;
   if (!mul_ok(M, K) || !mul_ok(N, K) || !mul_ok(M, N)) return FP8_ERR_SHAPE;
-  if (!is_fp8_dtype(a.dtype) || !is_fp8_dtype(b.dtype) || !valid_fmt(fmt_out)) return FP8_ERR_DTYPE;
+  if (!is_f8(a.dtype) || !is_f8(b.dtype) || !valid_fmt(fmt_out)) return FP8_ERR_DTYPE;
   int bias_kind = kBiasNone;
   if (bias.data) {
     if (bias.dtype == FP8_DT_BF16) bias_kind = kBiasBF16;

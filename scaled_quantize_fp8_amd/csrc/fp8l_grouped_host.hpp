@@ -281,15 +281,15 @@ void launch_rows(GemmArgs& g, const Groups& gr, const GroupStrides& s, const Gro
                  int tile, hipStream_t st) {
   if constexpr (LB == kKContig) {
     if (tile == kTileSkinny16Any)
-      return launch_skinny_groups<Skinny<FA, FB, 1, 1, true>>(g, gr, s, side, st);
+      return launch_skinny_groups<Skinny<FA, FB, 1, true>>(g, gr, s, side, st);
     if (tile == kTileSkinny32Any)
-      return launch_skinny_groups<Skinny<FA, FB, 2, 1, true>>(g, gr, s, side, st);
+      return launch_skinny_groups<Skinny<FA, FB, 2, true>>(g, gr, s, side, st);
     if (tile == kTileSkinny64Any)
-      return launch_skinny_groups<Skinny<FA, FB, 4, 1, true>>(g, gr, s, side, st);
-    if (tile == kTileSkinny16) return launch_skinny_groups<Skinny<FA, FB, 1, 1>>(g, gr, s, side, st);
-    if (tile == kTileSkinny32) return launch_skinny_groups<Skinny<FA, FB, 2, 1>>(g, gr, s, side, st);
-    if (tile == kTileSkinny48) return launch_skinny_groups<Skinny<FA, FB, 3, 1>>(g, gr, s, side, st);
-    if (tile == kTileSkinny64) return launch_skinny_groups<Skinny<FA, FB, 4, 1>>(g, gr, s, side, st);
+      return launch_skinny_groups<Skinny<FA, FB, 4, true>>(g, gr, s, side, st);
+    if (tile == kTileSkinny16) return launch_skinny_groups<Skinny<FA, FB, 1>>(g, gr, s, side, st);
+    if (tile == kTileSkinny32) return launch_skinny_groups<Skinny<FA, FB, 2>>(g, gr, s, side, st);
+    if (tile == kTileSkinny48) return launch_skinny_groups<Skinny<FA, FB, 3>>(g, gr, s, side, st);
+    if (tile == kTileSkinny64) return launch_skinny_groups<Skinny<FA, FB, 4>>(g, gr, s, side, st);
   }
   if (tile == kTile256x256w8)
     launch_rows_t<Tile256<kKContig, LB, FA, FB>, FA == kI8>(g, gr, s, side, st);

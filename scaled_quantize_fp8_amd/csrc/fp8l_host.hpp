@@ -50,7 +50,6 @@ inline bool is_f8(int32_t dt) { return dt == FP8_DT_E4M3 || dt == FP8_DT_E5M2; }
 inline bool valid_fmt(int32_t f) { return f == FP8_E4M3 || f == FP8_E5M2; }
 inline int32_t fmt_dtype(int32_t f) { return f == FP8_E4M3 ? FP8_DT_E4M3 : FP8_DT_E5M2; }
 inline int dtype_fmt(int32_t dt) { return dt == FP8_DT_E4M3 ? kE4M3 : kE5M2; }
-inline bool is_fp8_dtype(int32_t dt) { return dt == FP8_DT_E4M3 || dt == FP8_DT_E5M2; }
 
 // a * b fits in int64 (a, b >= 0)
 inline bool mul_ok(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / 4 / a; }
@@ -144,7 +143,5 @@ bool enqueue_quant(const void* x, int32_t in_dtype, int64_t n, int32_t fmt, uint
 // dynamic one, whose amax lands in amax_out.
 void enqueue_amax(const void* x, int32_t dt, int64_t n, const fp8_ring_t* ring, float* amax_out,
                   const RowLimit& limit, hipStream_t st);
-// One-wave launch that folds a ring whose groups a deferring launch filled.
-void enqueue_fold(const RingFold& f, hipStream_t st);
 
 }  // namespace fp8l

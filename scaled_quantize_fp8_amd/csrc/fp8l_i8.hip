@@ -192,13 +192,13 @@ int fp8_i8_linear_fwd(int64_t M, int64_t N, int64_t K, fp8_operand_t x, fp8_oper
   if (is_hp(x.dtype)) enqueue_rows(x.data, x.dtype, M, K, x8_out, sx_out, nullptr, stream);
   if (M > 0 && N > 0) {
     const int tile = i8_tile(g);
-    if (tile == kTileSkinny16Any) launch_skinny<Skinny<kI8, kI8, 1, 1, true>>(g, stream);
-    else if (tile == kTileSkinny32Any) launch_skinny<Skinny<kI8, kI8, 2, 1, true>>(g, stream);
-    else if (tile == kTileSkinny64Any) launch_skinny<Skinny<kI8, kI8, 4, 1, true>>(g, stream);
-    else if (tile == kTileSkinny16) launch_skinny<Skinny<kI8, kI8, 1, 1>>(g, stream);
-    else if (tile == kTileSkinny32) launch_skinny<Skinny<kI8, kI8, 2, 1>>(g, stream);
-    else if (tile == kTileSkinny48) launch_skinny<Skinny<kI8, kI8, 3, 1>>(g, stream);
-    else if (tile == kTileSkinny64) launch_skinny<Skinny<kI8, kI8, 4, 1>>(g, stream);
+    if (tile == kTileSkinny16Any) launch_skinny<Skinny<kI8, kI8, 1, true>>(g, stream);
+    else if (tile == kTileSkinny32Any) launch_skinny<Skinny<kI8, kI8, 2, true>>(g, stream);
+    else if (tile == kTileSkinny64Any) launch_skinny<Skinny<kI8, kI8, 4, true>>(g, stream);
+    else if (tile == kTileSkinny16) launch_skinny<Skinny<kI8, kI8, 1>>(g, stream);
+    else if (tile == kTileSkinny32) launch_skinny<Skinny<kI8, kI8, 2>>(g, stream);
+    else if (tile == kTileSkinny48) launch_skinny<Skinny<kI8, kI8, 3>>(g, stream);
+    else if (tile == kTileSkinny64) launch_skinny<Skinny<kI8, kI8, 4>>(g, stream);
     else if (tile == kTile128x256) launch_i8_t<Tile128x256<kKContig, kKContig, kI8, kI8>>(g, stream);
     else if (tile == kTile256x256w8) launch_i8_t<Tile256<kKContig, kKContig, kI8, kI8>>(g, stream);
     else if (tile == kTile128x128w8) launch_i8_t<Tile128<kKContig, kKContig, kI8, kI8>>(g, stream);

@@ -4,7 +4,7 @@
 //
 // With a handful of rows the matrix pipes idle and the time is that of
 // reading B once from HBM.  So there is no LDS staging and no barrier in the
-// K loop: every wave reads its own 16 NT rows of B straight into MFMA
+// K loop: every wave reads its own 16 rows of B straight into MFMA
 // operand registers, many 16-byte loads in flight, and A (small, in L2) the
 // same way.  The MFMA does not care which K position sits in which lane as
 // long as A and B agree, so a lane takes bytes [16 q, 16 q + 16) and
@@ -39,9 +39,9 @@ template <int MT, bool I8, bool ANY>
 constexpr int skinny_unroll() { return MT == 1 ? 4 : ((MT == 4 || ANY) && (I8 || (ANY && MT == 4)) ? 1 : 2); }
 
 // ANY: rows of any alignment and sizes of any kind, through load16_any.
-template <int FA, int FB, int MT, int NT, bool ANY = false>
+template <int FA, int FB, int MT, bool ANY = false>
 struct Skinny {
-  static constexpr int kBM = 16 * MT, kWaveN = 16 * NT, kThreads = 512, kLds = 8 * MT * NT * 1024;
+  static constexpr int kBM = 16 * MT, kWaveN = 16, kThreads = 512, kLds = 8 * MT * 1024;
   static constexpr bool I8 = FA == kI8;
   static constexpr int kU = skinny_unroll<MT, I8, ANY>();
 
@@ -156,7 +156,7 @@ struct Skinny {
     return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
 
-  // Tile column tn (of 16 NT 8 / KW columns) of the rows g.a .. (g.Mc of them).
+  // Tile column tn (of 16 * 8 / KW columns) of the rows g.a .. (g.Mc of them).
   FP8L_DEV static void run(const GemmArgs& g, int tn, int KW, uint8_t* smem) {
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -166,23 +166,20 @@ struct Skinny {
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.Mc * g.lda));
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b, (uint32_t)(g.Nc * g.ldb));
     // row offsets; rows past the end lie past the buffer and read as zeros
-    uint32_t oa[MT], ob[NT];
+    uint32_t oa[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) oa[m] = (uint32_t)((16 * m + r) * g.lda);
+    const uint32_t ob = (uint32_t)((j0 + r) * g.ldb);
+    v4f acc[MT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) ob[n] = (uint32_t)((j0 + 16 * n + r) * g.ldb);
-    v4f acc[MT][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     // the epilogue's operands, in flight with the first pieces (with KW > 1
     // another wave may finish the fragment; it then finds them in cache)
     Epi e0 = epi(g, r, j0 + 4 * q);
     const uint32_t K = (uint32_t)g.Kc;
     const uint32_t pieces = (K + 127) / 128;
     for (uint32_t p = kw; p < pieces; p += KW * kU) {
-      v8i fa[kU][MT], fb[kU][NT];
+      v8i fa[kU][MT], fb[kU][1];
       if constexpr (ANY) {
         int64_t k[2 * kU];
 #pragma unroll
@@ -190,16 +187,14 @@ struct Skinny {
           k[2 * u] = (int64_t)(p + u * KW) * 128 + 16 * q;
           k[2 * u + 1] = k[2 * u] + 64;
         }
-        load_any<NT>(g.b, g.ldb, j0 + r, g.Nc, g.Kc, k, fb);
+        load_any<1>(g.b, g.ldb, j0 + r, g.Nc, g.Kc, k, fb);
         load_any<MT>(g.a, g.lda, r, g.Mc, g.Kc, k, fa);
       } else {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const uint32_t k0 = (p + u * KW) * 128 + 16 * q, k1 = k0 + 64;
           // bytes past K (the next row's) and pieces past the last: zeros
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            fb[u][n] = load2(rb, k0 < K ? ob[n] + k0 : 0x80000000u, k1 < K ? ob[n] + k1 : 0x80000000u);
+          fb[u][0] = load2(rb, k0 < K ? ob + k0 : 0x80000000u, k1 < K ? ob + k1 : 0x80000000u);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
             fa[u][m] = load2(ra, k0 < K ? oa[m] + k0 : 0x80000000u, k1 < K ? oa[m] + k1 : 0x80000000u);
@@ -208,38 +203,32 @@ struct Skinny {
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) acc[m][n] = mma_16x16<FA, FB>(fb[u][n], fa[u][m], acc[m][n]);
+        for (int m = 0; m < MT; ++m) acc[m] = mma_16x16<FA, FB>(fb[u][0], fa[u][m], acc[m]);
     }
     if (KW == 1) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (m + n > 0) e0 = epi(g, 16 * m + r, j0 + 16 * n + 4 * q);
-          store(g, 16 * m + r, j0 + 16 * n + 4 * q, acc[m][n], e0);
-        }
+      for (int m = 0; m < MT; ++m) {
+        if (m > 0) e0 = epi(g, 16 * m + r, j0 + 4 * q);
+        store(g, 16 * m + r, j0 + 4 * q, acc[m], e0);
+      }
       return;
     }
     // partial sums: [wave][fragment][lane] x 16 bytes
     v4f* const part = reinterpret_cast<v4f*>(smem);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) part[(wave * MT * NT + n * MT + m) * 64 + lane] = acc[m][n];
+    for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = acc[m];
     __syncthreads();
-    for (int f = wave; f < JW * MT * NT; f += 8) {
-      const int fj = f / (MT * NT), fn = f % (MT * NT) / MT, fm = f % MT;
-      const v4f* src = part + (fj * KW * MT * NT + f % (MT * NT)) * 64 + lane;
+    for (int f = wave; f < JW * MT; f += 8) {
+      const int fj = f / MT, fm = f % MT;
+      const v4f* src = part + (fj * KW * MT + fm) * 64 + lane;
       v4f s = src[0];
       for (int w = 1; w < KW; ++w) {
-        const v4f o = src[w * MT * NT * 64];
+        const v4f o = src[w * MT * 64];
 #pragma unroll
         for (int t = 0; t < 4; ++t) s[t] = add_sums<I8>(s[t], o[t]);
       }
       const int row = 16 * fm + r;
-      const int64_t j = jb + fj * kWaveN + 16 * fn + 4 * q;
+      const int64_t j = jb + fj * kWaveN + 4 * q;
       store(g, row, j, s, epi(g, row, j));
     }
   }
@@ -260,7 +249,7 @@ template <int IN>
 struct SkinnyFused {
   static constexpr int kBM = 16, kWaveN = 16, kThreads = 512, kU = 4;
   static constexpr bool I8 = true;
-  using S = Skinny<kI8, kI8, 1, 1>;
+  using S = Skinny<kI8, kI8, 1>;
   static constexpr int kPart = S::kLds;         // partial sums
   static constexpr int kHead = kPart + 16 * 8 * 4 + 16 * 4;  // + amax per row and wave, + scales
   // LDS for rows of K codes
