@@ -86,13 +86,19 @@ inline int skinny_rows(int tile) {
 }
 
 // Microseconds of a launch of `tiles` tiles with contraction K, from fits to
-// a sweep of the integer GEMM over 64 .. 4096 rows of six layer shapes
-// (within about 15%): a fixed part per launch and per round of tiles on the
-// CUs (first stages, epilogue), and a part per unit of K.  One round at
-// K = 1536 / 4096 / 11008:
-//   128x128, one block per CU:    13 / 25 /  55 us
-//   128x256, one block per CU:    20 / 40 / 100, two: 37 / 88 / 223
-//   256x256:                      32 / 64 / 150
+// a sweep of the integer GEMM over 64 .. 4096 rows of six layer shapes: a
+// fixed part per launch and per round of tiles on the CUs (first stages,
+// epilogue), and a part per unit of K.  Measured on a card somewhat faster
+// than the sweep's, K = 1536 / 4096 / 11008, against the model:
+//   128x128, one block per CU, a full round:  14 / 23 /  49 us (14 / 25 /  55)
+//   256x256, a full round:                    35 / 67 / 163    (32 / 64 / 151)
+//   256x256, half the CUs:                    29 / 47 / 107    (as a full one)
+//   128x256, one block per CU:                25 / 43 / 104    (20 / 41 /  96)
+//   128x256, two blocks per CU:               36 / 74 / 196    (47 / 109 / 278)
+// The quarter round added to 128x256 stands for uneven last rounds and ragged
+// groups; on full rounds it and the slope put the model 23 to 47% too high
+// (256 to 2048 tiles more than one per CU), so that tile is taken where it
+// wins clearly only.  FP8 and crosswise operands take the same fit.
 inline double tile_us(int tile, double tiles, double K) {
   const double cus = cu_count();
   switch (tile) {
@@ -155,7 +161,8 @@ inline int pick_tile(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
 // The same where the pipelined tiles cannot run (odd sizes, unaligned
 // pointers): the general tile (two blocks per CU; 2.5 us per 128 of K alone,
 // 3.3 for two), or the skinny kernel's form for any alignment, whose pieces
-// take 1.6 (64 rows: 2) times as long.
+// take 1.6 (64 rows: 2) times as long.  The 64-row form is for many rows of a
+// narrow W (8192 x 129 x 4097: 76 us, 83 with 32 rows, 85 on the general tile).
 inline int pick_any(int64_t T, int64_t E, int64_t N, int64_t K, bool skinny) {
   const double cus = cu_count(), steps = (double)((K + 127) / 128);
   const double tiles = expected_units(T, E, 128) * (double)((N + 127) / 128);

@@ -34,7 +34,9 @@
 
 namespace fp8l {
 
-// K pieces of 128 bytes loaded at once.
+// K pieces of 128 bytes loaded at once: as many as the 128 registers of two
+// blocks per CU hold (64 integer rows of any alignment still spill 13, in
+// groups 6).
 template <int MT, bool I8, bool ANY>
 constexpr int skinny_unroll() { return MT == 1 ? 4 : ((MT == 4 || ANY) && (I8 || (ANY && MT == 4)) ? 1 : 2); }
 
