@@ -566,6 +566,99 @@ int fp8_i8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const 
                               int32_t out_dtype, void* y, int8_t* x8_out, float* sx_out,
                               hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Routing of tokens to a mixture's experts, and the exchange of their rows:
+ * what stands before and behind the experts' linear layers.  Each of T tokens
+ * gets k slots; slot (t, i) holds an expert, a weight and the place of its row
+ * among the rows sorted by expert (the rows that the grouped calls take).
+ * Limits (FP8_ERR_SHAPE otherwise): 1 <= E <= 1024, 1 <= k <= 64, T k <= 2^30.
+ * Results do not depend on scheduling: the same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* Scores of a token's logits z: softmax(z), or 1 / (1 + exp(-z)) of each. */
+typedef enum { FP8_ROUTE_SOFTMAX = 0, FP8_ROUTE_SIGMOID = 1 } fp8_route_score_t;
+
+/* Bytes of the workspace of fp8_route_plan, and of fp8_route_fwd with places;
+ * 0 where none is needed (at most 2048 slots) or the sizes are refused. */
+size_t fp8_route_workspace_bytes(int64_t T, int32_t E, int32_t k);
+
+/*
+ * The choice of experts.  p = score(logits[t]); c = p + bias (bias NULL: p).
+ *   groups      the E experts are cut into `groups` groups of consecutive ones
+ *               (groups divides E); a group's score is the sum of its
+ *               group_top (1 or 2) largest c, or of those there are; only the
+ *               groups_kept best groups' experts can be chosen.  1, 1: no limit.
+ *   idx         device int32 [T, k] out: the k largest c, best first.  A tie
+ *               (of experts or groups) goes to the lowest index; the order is
+ *               that of c held in 64 bits, without a bias that of the logits.
+ *   weights     device float [T, k] out: scale p[idx], with renorm divided by
+ *               the sum of the token's chosen p (the bias plays no part).
+ *   An expert whose logit or bias is -inf is never chosen: a slot that finds
+ *   none gets idx -1 and weight 0 (a padded token: a row of -inf).  A row that
+ *   holds a NaN, also in the bias, or for softmax +inf, gets 0 .. k-1 with NaN
+ *   weights.
+ *   offsets, pos  both or neither: the places as fp8_route_plan gives them,
+ *               with its workspace ws.
+ *   logits      [T, E] F32, F16 or BF16; bias float [E] or NULL.
+ * Errors: FP8_ERR_SHAPE also for k > E, groups that do not divide E,
+ * groups_kept outside [1, groups] or too few for k experts, group_top;
+ * FP8_ERR_DTYPE for an unknown dtype or score.
+ */
+int fp8_route_fwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t dtype,
+                  const float* bias, int32_t score, int32_t groups, int32_t groups_kept,
+                  int32_t group_top, int32_t renorm, float scale, int32_t* idx, float* weights,
+                  int32_t* offsets, int32_t* pos, void* ws, hipStream_t stream);
+
+/*
+ * Gradient of the weights with respect to the logits, the choice held fixed:
+ * dlogits [T, E] of the logits' type from dweights float [T, k] and the
+ * forward's logits and idx (slots with idx -1 take no part; an index that
+ * stands twice in a row counts for each slot).  Sums in 32 bits, one rounding.
+ */
+int fp8_route_bwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t dtype,
+                  int32_t score, int32_t renorm, float scale, const int32_t* idx,
+                  const float* dweights, void* dlogits, hipStream_t stream);
+
+/*
+ * Places of the slots' rows when rows are sorted by expert, in the order of
+ * the slots: pos[t, i] = offsets[e] + the number of earlier slots of e
+ * (e = idx[t, i]), -1 for a slot outside [0, E); offsets int32 [E + 1], the
+ * form the grouped calls take.  idx may come from anywhere (k > E too).
+ *   ws  fp8_route_workspace_bytes(T, E, k) bytes (NULL where that is 0), 4-byte
+ *       aligned; its contents need not survive the call.
+ */
+int fp8_route_plan(int64_t T, int32_t E, int32_t k, const int32_t* idx, int32_t* offsets,
+                   int32_t* pos, void* ws, hipStream_t stream);
+
+/*
+ * Rows into expert order: out[pos[t, i]] = x[t] for every slot with a place in
+ * [0, R).  Rows are row_bytes bytes (values of any type, codes, scales; fewer
+ * than 2^24); x has T of them, out R.  Rows of out that no slot names are left as
+ * they were.
+ */
+int fp8_route_gather(int64_t T, int32_t k, int64_t row_bytes, int64_t R, const void* x,
+                     const int32_t* pos, void* out, hipStream_t stream);
+
+/*
+ * Back to tokens: out[t] = sum_i weights[t, i] y[pos[t, i]] over the slots with
+ * a place in [0, R), in slot order in 32 bits, rounded once; zeros for a token
+ * without any.  weights NULL: ones (the gradient of fp8_route_gather).
+ * y [R, D], out [T, D] of dtype F32, F16 or BF16; D <= 2^22.
+ */
+int fp8_route_combine(int64_t T, int32_t k, int64_t D, int64_t R, const void* y, int32_t dtype,
+                      const int32_t* pos, const float* weights, void* out, hipStream_t stream);
+
+/*
+ * Gradients of fp8_route_combine: dy[pos[t, i]] = weights[t, i] dout[t] (rows
+ * that no slot names are left as they were) and dweights[t, i] =
+ * dout[t] . y[pos[t, i]] in 32 bits (0 without a place).  dy or dweights may be
+ * NULL (not computed; y is needed for dweights only).  A place named by two
+ * slots makes that row of dy unspecified.
+ */
+int fp8_route_combine_bwd(int64_t T, int32_t k, int64_t D, int64_t R, const void* dout,
+                          const void* y, int32_t dtype, const int32_t* pos, const float* weights,
+                          void* dy, float* dweights, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,7 @@ FP8_DT_F32, FP8_DT_F16, FP8_DT_BF16, FP8_DT_E4M3, FP8_DT_E5M2, FP8_DT_I8 = 0, 1,
 FP8_OK, FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_DTYPE, FP8_ERR_RING, FP8_ERR_HIP = range(6)
 FP8_K_CONTIG, FP8_K_STRIDED = 0, 1
 FP8_QUANT_ROWS, FP8_QUANT_TRANSPOSED, FP8_QUANT_DUAL = 0, 1, 2
+FP8_ROUTE_SOFTMAX, FP8_ROUTE_SIGMOID = 0, 1
 
 _TORCH_DT = {torch.float32: FP8_DT_F32, torch.float16: FP8_DT_F16, torch.bfloat16: FP8_DT_BF16}
 _FMT_DT = {FP8_E4M3: FP8_DT_E4M3, FP8_E5M2: FP8_DT_E5M2}
@@ -36,7 +37,8 @@ C_SYMBOLS = (
     "fp8_linear_bwd_dw", "fp8_gemm", "fp8_quantize_2d", "fp8_gemm_fp8out", "fp8_linear_bwd",
     "fp8_linear_bwd_dw_noalloc", "fp8_grouped_db_workspace_bytes", "fp8_grouped_linear_fwd",
     "fp8_grouped_linear_bwd", "fp8_i8_quantize_rows", "fp8_i8_linear_fwd",
-    "fp8_i8_grouped_linear_fwd",
+    "fp8_i8_grouped_linear_fwd", "fp8_route_workspace_bytes", "fp8_route_fwd", "fp8_route_bwd",
+    "fp8_route_plan", "fp8_route_gather", "fp8_route_combine", "fp8_route_combine_bwd",
 )
 
 
@@ -101,6 +103,19 @@ def lib() -> ctypes.CDLL:
         L.fp8_i8_linear_fwd.argtypes = [i64, i64, i64, op, op, vp, i32, vp, vp, vp, vp]
         L.fp8_i8_grouped_linear_fwd.argtypes = [i64, i32, i64, i64, vp, op, op, vp, i32, vp, vp, vp,
                                                 vp]
+        f32 = ctypes.c_float
+        L.fp8_route_workspace_bytes.restype = sz
+        L.fp8_route_workspace_bytes.argtypes = [i64, i32, i32]
+        L.fp8_route_fwd.argtypes = [i64, i32, i32, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp,
+                                    vp, vp, vp, vp]
+        L.fp8_route_bwd.argtypes = [i64, i32, i32, vp, i32, i32, i32, f32, vp, vp, vp, vp]
+        L.fp8_route_plan.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp]
+        L.fp8_route_gather.argtypes = [i64, i32, i64, i64, vp, vp, vp, vp]
+        L.fp8_route_combine.argtypes = [i64, i32, i64, i64, vp, i32, vp, vp, vp, vp]
+        L.fp8_route_combine_bwd.argtypes = [i64, i32, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp]
+        for name in ("fp8_route_fwd", "fp8_route_bwd", "fp8_route_plan", "fp8_route_gather",
+                     "fp8_route_combine", "fp8_route_combine_bwd"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("fp8_grouped_linear_fwd", "fp8_grouped_linear_bwd", "fp8_i8_quantize_rows",
                      "fp8_i8_linear_fwd", "fp8_i8_grouped_linear_fwd"):
             getattr(L, name).restype = ctypes.c_int
@@ -135,6 +150,10 @@ def fp8_db_workspace_bytes(M: int, N: int) -> int:
 
 def fp8_grouped_db_workspace_bytes(T: int, E: int, N: int) -> int:
     return lib().fp8_grouped_db_workspace_bytes(T, E, N)
+
+
+def fp8_route_workspace_bytes(T: int, E: int, k: int) -> int:
+    return lib().fp8_route_workspace_bytes(T, E, k)
 
 
 # ---------------------------------------------------------------- marshalling
@@ -868,3 +887,168 @@ def fp8_i8_grouped_linear_fwd(x, w, bias, offsets, y, x8_out=None, sx_out=None, 
 def bind_fp8_i8_grouped_linear_fwd(x, w, bias, offsets, y, x8_out=None, sx_out=None, stream=None):
     return _bind_run("fp8_i8_grouped_linear_fwd", *_i8_grouped_args(x, w, bias, offsets, y, x8_out,
                                                                     sx_out, stream))
+
+
+# ---------------------------------------------------------------- routing to experts
+
+def _arg_places(T, k, E, offsets, pos, ws, dev):
+    """Pointers of a call that places rows: offsets, pos, workspace."""
+    op = _arg(offsets, "offsets", _I32, (E + 1,), dev)
+    pp = _arg(pos, "pos", _I32, (T, k), dev)
+    need = fp8_route_workspace_bytes(T, E, k)
+    if need == 0:
+        return op, pp, None
+    if not isinstance(ws, torch.Tensor) or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor of {need} bytes")
+    if ws.device != dev:
+        raise ValueError(f"ws: must be a GPU tensor on {dev} (got {ws.device})")
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {ws.numel() * ws.element_size()} bytes, at least {need} needed")
+    if ws.data_ptr() % 4:
+        raise ValueError("ws: must be 4-byte aligned")
+    return op, pp, ws.data_ptr()
+
+
+def _route_fwd_args(logits, idx, weights, bias, score, groups, groups_kept, group_top, renorm,
+                    scale, offsets, pos, ws, stream):
+    T, E = _shape_of(logits, 2, "logits")
+    k = _shape_of(idx, 2, "idx")[1]
+    dev = _gpu_of(logits, "logits")
+    zp = _arg(logits, "logits", _HP, None, dev)
+    places = (None, None, None)
+    if offsets is not None or pos is not None:
+        places = _arg_places(T, k, E, offsets, pos, ws, dev)
+    return (T, E, k, zp, _TORCH_DT[logits.dtype], _arg(bias, "bias", _F32, (E,), dev, True), score,
+            groups, groups_kept, group_top, int(bool(renorm)), scale,
+            _arg(idx, "idx", _I32, (T, k), dev), _arg(weights, "weights", _F32, (T, k), dev),
+            *places, _arg_stream(stream, dev)), dev
+
+
+def fp8_route_fwd(logits, idx, weights, bias=None, score=FP8_ROUTE_SOFTMAX, groups=1,
+                  groups_kept=1, group_top=1, renorm=True, scale=1.0, offsets=None, pos=None,
+                  ws=None, stream=None):
+    """The k experts of each token and their weights: logits [T, E], idx int32
+    [T, k], weights float32 [T, k], bias float32 [E] or None (added to the
+    scores for the choice only).  With offsets int32 [E + 1] and pos int32
+    [T, k] also the places of the rows sorted by expert (ws: any tensor of
+    fp8_route_workspace_bytes bytes, None where that is 0)."""
+    _run("fp8_route_fwd", *_route_fwd_args(logits, idx, weights, bias, score, groups, groups_kept,
+                                           group_top, renorm, scale, offsets, pos, ws, stream))
+
+
+def bind_fp8_route_fwd(logits, idx, weights, bias=None, score=FP8_ROUTE_SOFTMAX, groups=1,
+                       groups_kept=1, group_top=1, renorm=True, scale=1.0, offsets=None, pos=None,
+                       ws=None, stream=None):
+    return _bind_run("fp8_route_fwd", *_route_fwd_args(
+        logits, idx, weights, bias, score, groups, groups_kept, group_top, renorm, scale, offsets,
+        pos, ws, stream))
+
+
+def _route_bwd_args(logits, idx, dweights, dlogits, score, renorm, scale, stream):
+    T, E = _shape_of(logits, 2, "logits")
+    k = _shape_of(idx, 2, "idx")[1]
+    dev = _gpu_of(logits, "logits")
+    return (T, E, k, _arg(logits, "logits", _HP, None, dev), _TORCH_DT[logits.dtype], score,
+            int(bool(renorm)), scale, _arg(idx, "idx", _I32, (T, k), dev),
+            _arg(dweights, "dweights", _F32, (T, k), dev),
+            _arg(dlogits, "dlogits", (logits.dtype,), (T, E), dev), _arg_stream(stream, dev)), dev
+
+
+def fp8_route_bwd(logits, idx, dweights, dlogits, score=FP8_ROUTE_SOFTMAX, renorm=True, scale=1.0,
+                  stream=None):
+    """dlogits [T, E] (of logits' type) from dweights float32 [T, k] and the
+    forward's logits, idx and settings."""
+    _run("fp8_route_bwd", *_route_bwd_args(logits, idx, dweights, dlogits, score, renorm, scale,
+                                           stream))
+
+
+def bind_fp8_route_bwd(logits, idx, dweights, dlogits, score=FP8_ROUTE_SOFTMAX, renorm=True,
+                       scale=1.0, stream=None):
+    return _bind_run("fp8_route_bwd", *_route_bwd_args(logits, idx, dweights, dlogits, score,
+                                                       renorm, scale, stream))
+
+
+def _route_plan_args(idx, offsets, pos, ws, stream):
+    T, k = _shape_of(idx, 2, "idx")
+    E = _shape_of(offsets, 1, "offsets")[0] - 1
+    dev = _gpu_of(idx, "idx")
+    return (T, E, k, _arg(idx, "idx", _I32, None, dev),
+            *_arg_places(T, k, E, offsets, pos, ws, dev), _arg_stream(stream, dev)), dev
+
+
+def fp8_route_plan(idx, offsets, pos, ws=None, stream=None):
+    """Places of the rows sorted by expert, of idx int32 [T, k] from anywhere:
+    offsets int32 [E + 1], pos int32 [T, k] (-1: no expert)."""
+    _run("fp8_route_plan", *_route_plan_args(idx, offsets, pos, ws, stream))
+
+
+def bind_fp8_route_plan(idx, offsets, pos, ws=None, stream=None):
+    return _bind_run("fp8_route_plan", *_route_plan_args(idx, offsets, pos, ws, stream))
+
+
+def _route_gather_args(x, pos, out, stream):
+    T, D = _shape_of(x, 2, "x")
+    k = _shape_of(pos, 2, "pos")[1]
+    R = _shape_of(out, 2, "out")[0]
+    dev = _gpu_of(x, "x")
+    return (T, k, D * x.element_size(), R, _arg(x, "x", (x.dtype,), None, dev),
+            _arg(pos, "pos", _I32, (T, k), dev), _arg(out, "out", (x.dtype,), (R, D), dev),
+            _arg_stream(stream, dev)), dev
+
+
+def fp8_route_gather(x, pos, out, stream=None):
+    """out[pos[t, i]] = x[t]: x [T, D] and out [R, D] of one type, whichever
+    (values, codes, scales).  Rows of out that no slot names stay as they
+    were."""
+    _run("fp8_route_gather", *_route_gather_args(x, pos, out, stream))
+
+
+def bind_fp8_route_gather(x, pos, out, stream=None):
+    return _bind_run("fp8_route_gather", *_route_gather_args(x, pos, out, stream))
+
+
+def _route_combine_args(y, pos, weights, out, stream):
+    R, D = _shape_of(y, 2, "y")
+    T, k = _shape_of(pos, 2, "pos")
+    dev = _gpu_of(y, "y")
+    yp = _arg(y, "y", _HP, None, dev)
+    return (T, k, D, R, yp, _TORCH_DT[y.dtype], _arg(pos, "pos", _I32, None, dev),
+            _arg(weights, "weights", _F32, (T, k), dev, True),
+            _arg(out, "out", (y.dtype,), (T, D), dev), _arg_stream(stream, dev)), dev
+
+
+def fp8_route_combine(y, pos, weights, out, stream=None):
+    """out[t] = sum_i weights[t, i] y[pos[t, i]]: y [R, D], out [T, D] of y's
+    type, weights float32 [T, k] or None (ones: the gradient of
+    fp8_route_gather)."""
+    _run("fp8_route_combine", *_route_combine_args(y, pos, weights, out, stream))
+
+
+def bind_fp8_route_combine(y, pos, weights, out, stream=None):
+    return _bind_run("fp8_route_combine", *_route_combine_args(y, pos, weights, out, stream))
+
+
+def _route_combine_bwd_args(dout, y, pos, weights, dy, dweights, stream):
+    T, D = _shape_of(dout, 2, "dout")
+    k = _shape_of(pos, 2, "pos")[1]
+    dev = _gpu_of(dout, "dout")
+    gp = _arg(dout, "dout", _HP, None, dev)
+    R = _shape_of(dy if y is None else y, 2, "y")[0]
+    dt = (dout.dtype,)
+    return (T, k, D, R, gp, _arg(y, "y", dt, (R, D), dev, dweights is None), _TORCH_DT[dout.dtype],
+            _arg(pos, "pos", _I32, (T, k), dev), _arg(weights, "weights", _F32, (T, k), dev),
+            _arg(dy, "dy", dt, (R, D), dev, True),
+            _arg(dweights, "dweights", _F32, (T, k), dev, True), _arg_stream(stream, dev)), dev
+
+
+def fp8_route_combine_bwd(dout, y, pos, weights, dy=None, dweights=None, stream=None):
+    """The gradients of fp8_route_combine that are given a buffer:
+    dy[pos[t, i]] = weights[t, i] dout[t] (other rows stay as they were) and
+    dweights[t, i] = dout[t] . y[pos[t, i]] (y is needed for these only)."""
+    _run("fp8_route_combine_bwd", *_route_combine_bwd_args(dout, y, pos, weights, dy, dweights,
+                                                           stream))
+
+
+def bind_fp8_route_combine_bwd(dout, y, pos, weights, dy=None, dweights=None, stream=None):
+    return _bind_run("fp8_route_combine_bwd", *_route_combine_bwd_args(dout, y, pos, weights, dy,
+                                                                       dweights, stream))

@@ -1,0 +1,634 @@
+// Routing of tokens to a mixture's experts, and the exchange of their rows.
+//
+// Choice.  With p[e] = softmax(z)[e] or sigmoid(z[e]) and c = p + b (b: a bias
+// that balances the experts; without it c = p):
+//   groups     E / G consecutive experts each; a group's score is the sum of
+//              its one or two largest c; the best `kept` groups stay
+//   experts    the k largest c in them, best first
+// Ties go to the lowest index, and the order is that of scores held in 64
+// bits (without a bias that of the logits, which is the scores' order).  An
+// expert with c or z = -inf is never chosen: a slot that finds none has index
+// -1 and weight 0.  A row that holds a NaN (softmax: or +inf) chooses 0 .. k-1
+// with NaN weights.
+//
+// Weights.  w[i] = s p[idx[i]], or s p[idx[i]] / sum_j p[idx[j]].  The quotient
+// is taken of scores scaled by the largest chosen one, so it stands where all
+// chosen scores underflow:
+//   softmax   q[i] = exp(z[i] - m) / sum,   m the largest chosen logit
+//   sigmoid   n[i] = exp(min(z[i], 0) - m) / (1 + exp(-|z[i]|)), q = n / sum n,
+//             m the largest chosen min(z, 0)
+//
+// Gradient.  With d[i] = s dw[i] and q as above (plain weights: q = p):
+//   softmax, quotient   dz[i] = q[i] (d[i] - sum_j q[j] d[j])
+//   sigmoid, quotient   the same times 1 - p[i]
+//   sigmoid, plain      dz[i] = p[i] (1 - p[i]) d[i]
+//   softmax, plain      dz[e] = (p d at the chosen) - p[e] sum_j p[j] d[j]
+// All other logits get 0; the bias has no gradient.
+#pragma once
+
+#include "fp8l_quantize.hpp"
+
+namespace fp8l {
+
+constexpr int kRThreads = 256;
+constexpr int kRouteMaxE = 1024, kRouteMaxK = 64;
+enum { kSoftmax = 0, kSigmoid = 1 };
+
+struct RouteArgs {
+  const void* z;      // [T][E]
+  const float* bias;  // [E] or null
+  int32_t* idx;       // [T][k]
+  float* w;           // [T][k]
+  int32_t T, E, k, score, groups, kept, group_top, renorm;
+  float scale;
+};
+
+// ---------------------------------------------------------------- lanes
+
+// Lane groups of L (16 or 64) consecutive lanes hold one row.  All-reduce
+// steps inside 16 lanes are DPP: xor 1, xor 2, then the mirrors of 8 and of 16
+// lanes (quads, then eights are uniform by then, so these act as xor 4 and
+// xor 8).  Every step adds the same two numbers in both its lanes, so all
+// lanes end with the same bits: equal scores stay equal.
+template <int STEP>
+FP8L_DEV uint32_t lane_step(uint32_t v) {
+  if constexpr (STEP == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);
+  else if constexpr (STEP == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);
+  else if constexpr (STEP == 4) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);
+  else if constexpr (STEP == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false);
+  else return (uint32_t)__shfl_xor((int)v, STEP);
+}
+template <int STEP>
+FP8L_DEV float lane_step(float v) { return __uint_as_float(lane_step<STEP>(__float_as_uint(v))); }
+template <int STEP>
+FP8L_DEV int lane_step(int v) { return (int)lane_step<STEP>((uint32_t)v); }
+template <int STEP>
+FP8L_DEV double lane_step(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint64_t lo = lane_step<STEP>((uint32_t)u), hi = lane_step<STEP>((uint32_t)(u >> 32));
+  return __longlong_as_double((long long)(lo | (hi << 32)));
+}
+// f(step tag) for steps 1, 2, .. L / 2
+template <int L, int STEP = 1, class F>
+FP8L_DEV void lane_steps(F&& f) {
+  if constexpr (STEP < L) {
+    f(std::integral_constant<int, STEP>{});
+    lane_steps<L, 2 * STEP>(f);
+  }
+}
+template <int L>
+FP8L_DEV float lanes_max(float v) {
+  lane_steps<L>([&](auto s) { v = fmaxf(v, lane_step<decltype(s)::value>(v)); });
+  return v;
+}
+template <int L, class S>
+FP8L_DEV S lanes_sum(S v) {
+  lane_steps<L>([&](auto s) { v += lane_step<decltype(s)::value>(v); });
+  return v;
+}
+template <int L>
+FP8L_DEV bool lanes_any(bool b) {
+  const uint64_t m = __ballot(b);
+  if constexpr (L == 64) return m != 0;
+  return (m >> (threadIdx.x & 63 & ~(L - 1)) & ((1ull << (L & 63)) - 1)) != 0;
+}
+
+// LDS written by lanes of this wave, before lanes of it read (a wave's LDS
+// accesses run in order; this keeps the compiler from moving them).
+FP8L_DEV void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Largest of the row's values c[V] (lane l holds indices l V ..), the lowest
+// index on a tie; its index in `at` (unspecified where all are -inf).
+template <int L, int V, class S>
+FP8L_DEV S row_best(const S (&c)[V], int sl, int& at) {
+  S best = c[0];
+  at = sl * V;
+#pragma unroll
+  for (int v = 1; v < V; ++v)
+    if (c[v] > best) best = c[v], at = sl * V + v;
+  lane_steps<L>([&](auto s) {
+    const S o = lane_step<decltype(s)::value>(best);
+    const int oa = lane_step<decltype(s)::value>(at);
+    if (o > best || (o == best && oa < at)) best = o, at = oa;
+  });
+  return best;
+}
+
+template <int V, class S>
+FP8L_DEV void strike(S (&c)[V], int sl, int at) {
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (at == sl * V + v) c[v] = -(S)INFINITY;
+}
+
+// LDS of one row: its scores, then the marks of the kept groups.
+template <int L, int V>
+constexpr int route_row_lds() { return L * V * 9; }
+
+// c of the experts in groups that are not kept becomes -inf.  g: the values
+// that the groups are scored by.
+template <int L, int V, class S>
+FP8L_DEV void keep_groups(const RouteArgs& a, S (&c)[V], const S (&g)[V], int sl, uint8_t* row) {
+  S* const sc = reinterpret_cast<S*>(row);
+  uint8_t* const mark = row + L * V * 8;
+  const int n = a.E / a.groups;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sc[sl * V + v] = g[v];
+  wave_fence();
+  S gs[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int q = sl * V + v;
+    gs[v] = -(S)INFINITY;
+    if (q < a.groups) {
+      S hi = -(S)INFINITY, lo = -(S)INFINITY;
+      for (int i = q * n; i < q * n + n; ++i) {
+        const S x = sc[i];
+        if (x > hi) lo = hi, hi = x;
+        else if (x > lo) lo = x;
+      }
+      gs[v] = a.group_top == 2 && lo > -(S)INFINITY ? hi + lo : hi;
+    }
+    mark[q] = 0;
+  }
+  wave_fence();
+  for (int i = 0; i < a.kept; ++i) {
+    int at;
+    if (row_best<L>(gs, sl, at) > -(S)INFINITY && at / V == sl) mark[at] = 1;
+    strike(gs, sl, at);
+  }
+  wave_fence();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = sl * V + v;
+    if (e < a.E && !mark[e / n]) c[v] = -(S)INFINITY;
+  }
+  wave_fence();
+}
+
+// The scores p of a row in S; m: its largest logit.
+template <int L, int V, class S>
+FP8L_DEV void row_scores(const RouteArgs& a, const float (&z)[V], float m, S (&p)[V]) {
+  if (a.score == kSigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = (S)1 / ((S)1 + exp(-(S)z[v]));
+    return;
+  }
+  S sum = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    p[v] = exp((S)z[v] - (S)m);
+    sum += p[v];
+  }
+  sum = lanes_sum<L>(sum);
+#pragma unroll
+  for (int v = 0; v < V; ++v) p[v] = p[v] / sum;
+}
+
+// The chosen experts of a row: slot i's in lane i (-1: none).
+template <int L, int V, class S>
+FP8L_DEV int choose(const RouteArgs& a, const float (&z)[V], const float (&b)[V], float m, int sl,
+                    uint8_t* row) {
+  S c[V], g[V];
+  const S none = -(S)INFINITY;
+  const bool by_score = a.bias || (a.groups > 1 && a.group_top == 2);
+  if (by_score) row_scores<L>(a, z, m, g);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool off = z[v] == -INFINITY;
+    if (by_score) g[v] = off ? none : g[v] + (S)b[v];
+    else g[v] = (S)z[v];
+    c[v] = a.bias ? g[v] : (S)z[v];
+  }
+  if (a.groups > 1 && a.kept < a.groups) keep_groups<L>(a, c, g, sl, row);
+  int mine = -1;
+  for (int i = 0; i < a.k; ++i) {
+    int at;
+    const S best = row_best<L>(c, sl, at);
+    if (sl == i && best > none) mine = at;
+    strike(c, sl, at);
+  }
+  return mine;
+}
+
+// Weights of a row's slots: slot i's in lane i.  zi: the chosen one's logit.
+template <int L, int V>
+FP8L_DEV float slot_weight(const RouteArgs& a, const float (&z)[V], float m, bool live, float zi) {
+  float q;
+  if (a.score == kSoftmax) {
+    const float top = a.renorm ? lanes_max<L>(live ? zi : -INFINITY) : m;
+    q = live ? expf(zi - top) : 0.0f;
+    float sum;
+    if (a.renorm) {
+      sum = lanes_sum<L>(q);
+    } else {
+      sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum += expf(z[v] - m);
+      sum = lanes_sum<L>(sum);
+    }
+    q = live ? q / sum : 0.0f;
+  } else {
+    const float lo = fminf(zi, 0.0f);
+    const float top = a.renorm ? lanes_max<L>(live ? lo : -INFINITY) : 0.0f;
+    q = live ? expf(lo - top) / (1.0f + expf(-fabsf(zi))) : 0.0f;
+    if (a.renorm) {
+      const float sum = lanes_sum<L>(q);
+      q = live ? q / sum : 0.0f;
+    }
+  }
+  return q;
+}
+
+// One row per L lanes, V experts per lane: E <= L V, k <= L.
+template <int IN, int L, int V>
+__global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRThreads / L * route_row_lds<L, V>()];
+  const int sl = threadIdx.x % L;
+  uint8_t* const row_lds = lds + threadIdx.x / L * route_row_lds<L, V>();
+  const int64_t t0 = (int64_t)blockIdx.x * (kRThreads / L) + threadIdx.x / L;
+  const bool there = t0 < a.T;
+  const int64_t t = there ? t0 : a.T - 1;
+  float z[V], b[V];
+  bool bad = false;
+  float m = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = sl * V + v;
+    z[v] = e < a.E ? load1<IN>(a.z, t * a.E + e) : -INFINITY;
+    b[v] = a.bias && e < a.E ? a.bias[e] : 0.0f;
+    bad = bad || z[v] != z[v] || b[v] != b[v] || (a.score == kSoftmax && z[v] == INFINITY);
+    m = fmaxf(m, z[v]);
+  }
+  m = lanes_max<L>(m);
+  bad = lanes_any<L>(bad);
+  int mine = choose<L, V, double>(a, z, b, m, sl, row_lds);
+  if (bad) mine = sl;
+  const bool live = sl < a.k && mine >= 0;
+  const float zi = live ? load1<IN>(a.z, t * a.E + mine) : 0.0f;
+  float w = a.scale * slot_weight<L>(a, z, m, live, zi);
+  if (bad) w = __uint_as_float(0x7fc00000u);
+  if (there && sl < a.k) {
+    a.idx[t * a.k + sl] = mine;
+    a.w[t * a.k + sl] = w;
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+
+struct RouteBwdArgs {
+  RouteArgs r;        // z, idx, k, E, T, score, renorm, scale; w unused
+  const float* dw;    // [T][k]
+  void* dz;           // [T][E], z's type
+};
+
+template <int IN>
+FP8L_DEV void store1(void* p, int64_t i, float v) {
+  if constexpr (IN == kInF32) reinterpret_cast<float*>(p)[i] = v;
+  else if constexpr (IN == kInF16) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_f16(v);
+  else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
+}
+
+template <int IN, int L, int V>
+__global__ __launch_bounds__(kRThreads) void route_bwd_kernel(RouteBwdArgs a) {
+  const RouteArgs& r = a.r;
+  const int sl = threadIdx.x % L;
+  const int64_t t0 = (int64_t)blockIdx.x * (kRThreads / L) + threadIdx.x / L;
+  const bool there = t0 < r.T;
+  const int64_t t = there ? t0 : r.T - 1;
+  float z[V];
+  float m = -INFINITY;
+  const bool dense = r.score == kSoftmax && !r.renorm;  // every logit gets a part
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = sl * V + v;
+    z[v] = dense && e < r.E ? load1<IN>(r.z, t * r.E + e) : -INFINITY;
+    m = fmaxf(m, z[v]);
+  }
+  if (dense) m = lanes_max<L>(m);
+  int e = -1;
+  float d = 0.0f;
+  if (sl < r.k) {
+    e = r.idx[t * r.k + sl];
+    if (e < 0 || e >= r.E) e = -1;
+    else d = r.scale * a.dw[t * r.k + sl];
+  }
+  const bool live = e >= 0;
+  const float zi = live ? load1<IN>(r.z, t * r.E + e) : 0.0f;
+  const float q = slot_weight<L>(r, z, m, live, zi);
+  float part = live ? q * d : 0.0f;
+  const float dot = r.renorm || dense ? lanes_sum<L>(part) : 0.0f;
+  if (r.renorm) part = live ? q * (d - dot) : 0.0f;
+  // 1 - p = sigmoid(-z)
+  if (r.score == kSigmoid) part = live ? part / (1.0f + expf(zi)) : 0.0f;
+  float g[V];
+  if (dense) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum += g[v] = expf(z[v] - m);
+    sum = lanes_sum<L>(sum);
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = m == -INFINITY && dot == 0.0f ? 0.0f : -dot * (g[v] / sum);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = 0.0f;
+  }
+  for (int i = 0; i < r.k; ++i) {
+    const int src = (threadIdx.x & 63 & ~(L - 1)) + i;
+    const int ei = __shfl(e, src);
+    const float pi = __shfl(part, src);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (ei == sl * V + v) g[v] += pi;
+  }
+  if (!there) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (sl * V + v < r.E) store1<IN>(a.dz, t * r.E + sl * V + v, g[v]);
+}
+
+// ---------------------------------------------------------------- places
+
+// Rows sorted by expert, in the order of the slots (a stable counting sort):
+// slot j = t k + i with expert e goes to offsets[e] + the number of earlier
+// slots of e.  Slots of no expert get -1.  The slots are cut into chunks; a
+// first launch counts each chunk's experts, the second adds up what lies
+// before its chunk and places the chunk's slots.  One chunk needs one launch.
+// Nothing is counted by atomics across blocks: places do not depend on timing.
+struct PlanArgs {
+  const int32_t* idx;
+  int32_t* offsets;  // [E + 1]
+  int32_t* pos;      // [n]
+  int32_t* counts;   // [chunks][E]
+  int32_t n, E, chunk, chunks;
+};
+
+FP8L_DEV int slot_expert(const PlanArgs& a, int j) {
+  if (j >= a.n) return a.E;
+  const int e = a.idx[j];
+  return e >= 0 && e < a.E ? e : a.E;
+}
+
+__global__ __launch_bounds__(kRThreads) void plan_count_kernel(PlanArgs a) {
+  __shared__ int32_t h[kRouteMaxE + 1];
+  for (int e = threadIdx.x; e <= a.E; e += kRThreads) h[e] = 0;
+  __syncthreads();
+  const int j0 = blockIdx.x * a.chunk;
+  for (int j = j0 + threadIdx.x; j < min(j0 + a.chunk, a.n); j += kRThreads)
+    atomicAdd(&h[slot_expert(a, j)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kRThreads) a.counts[blockIdx.x * a.E + e] = h[e];
+}
+
+// Lanes of the wave with the same key (< 2^bits).
+FP8L_DEV uint64_t same_key(int key, int bits) {
+  uint64_t peers = ~0ull;
+  for (int i = 0; i < bits; ++i) {
+    const uint64_t m = __ballot((key >> i) & 1);
+    peers &= (key >> i) & 1 ? m : ~m;
+  }
+  return peers;
+}
+
+__global__ __launch_bounds__(kRThreads) void plan_place_kernel(PlanArgs a) {
+  constexpr int NW = kRThreads / 64, PER = kRouteMaxE / kRThreads;
+  __shared__ int32_t next[NW][kRouteMaxE + 1];  // each wave's next place of an expert
+  __shared__ int32_t wave_total[NW];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int e = tid; e < NW * (kRouteMaxE + 1); e += kRThreads) (&next[0][0])[e] = 0;
+  __syncthreads();
+  // wave w's slots: the w-th quarter of the chunk
+  const int per = a.chunk / NW;
+  const int j0 = blockIdx.x * a.chunk + wave * per;
+  for (int j = j0 + lane; j < j0 + per; j += 64) atomicAdd(&next[wave][slot_expert(a, j)], 1);
+  __syncthreads();
+  // thread's experts: PER consecutive ones
+  int before[PER], total[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    before[i] = total[i] = 0;
+    if (e < a.E) {
+      if (a.chunks == 1) {
+        for (int w = 0; w < NW; ++w) total[i] += next[w][e];
+      } else {
+        for (int c = 0; c < a.chunks; ++c) {
+          const int n = a.counts[c * a.E + e];
+          if (c < (int)blockIdx.x) before[i] += n;
+          total[i] += n;
+        }
+      }
+    }
+    sum += total[i];
+  }
+  // exclusive prefix over the threads
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) wave_total[wave] = incl;
+  __syncthreads();
+  int first = incl - sum;
+  for (int w = 0; w < wave; ++w) first += wave_total[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    if (e < a.E) {
+      if (blockIdx.x == 0) {
+        a.offsets[e] = first;
+        if (e == a.E - 1) a.offsets[a.E] = first + total[i];
+      }
+      int at = first + before[i];
+      for (int w = 0; w < NW; ++w) {
+        const int n = next[w][e];
+        next[w][e] = at;
+        at += n;
+      }
+    }
+    first += total[i];
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(a.E);
+  for (int j = j0 + lane; j - lane < j0 + per; j += 64) {
+    const int e = slot_expert(a, j);
+    const uint64_t peers = same_key(e, bits);
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    const int at = next[wave][e] + rank;
+    wave_fence();
+    if (rank == 0) next[wave][e] += __popcll(peers);
+    wave_fence();
+    if (j < a.n) a.pos[j] = e < a.E ? at : -1;
+  }
+}
+
+// ---------------------------------------------------------------- rows
+
+// A row's pieces of U bytes (U: the widest that sizes and pointers allow) go
+// to `width` neighbouring threads (a power of two up to the block's), the
+// block's 256 / width tokens side by side, further pieces over blockIdx.y.
+struct RowGrid {
+  int32_t width_log, pieces;
+};
+
+template <int U>
+struct Bytes;
+template <> struct Bytes<16> { typedef uint4 T; };
+template <> struct Bytes<8> { typedef uint2 T; };
+template <> struct Bytes<4> { typedef uint32_t T; };
+template <> struct Bytes<2> { typedef uint16_t T; };
+template <> struct Bytes<1> { typedef uint8_t T; };
+
+struct GatherArgs {
+  const uint8_t* x;    // [T] rows
+  uint8_t* out;        // [R] rows
+  const int32_t* pos;  // [T][k]
+  int32_t T, k, R;
+  int64_t row;         // bytes
+  RowGrid grid;
+};
+
+template <int U>
+__global__ __launch_bounds__(kRThreads) void gather_kernel(GatherArgs a) {
+  typedef typename Bytes<U>::T P;
+  const int piece = blockIdx.y * (1 << a.grid.width_log) + (threadIdx.x & ((1 << a.grid.width_log) - 1));
+  if (piece >= a.grid.pieces) return;
+  const int per = kRThreads >> a.grid.width_log;
+  const int64_t at = (int64_t)piece * U;
+  for (int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.grid.width_log); t < a.T;
+       t += (int64_t)gridDim.x * per) {
+    const P v = *reinterpret_cast<const P*>(a.x + t * a.row + at);
+    for (int i = 0; i < a.k; ++i) {
+      const int p = a.pos[t * a.k + i];
+      if (p >= 0 && p < a.R) *reinterpret_cast<P*>(a.out + p * a.row + at) = v;
+    }
+  }
+}
+
+struct CombineArgs {
+  const void* y;       // [R][D]
+  const int32_t* pos;  // [T][k]
+  const float* w;      // [T][k], null: ones
+  void* out;           // [T][D]
+  int32_t T, k, R;
+  int64_t D;
+  RowGrid grid;
+};
+
+// A piece of N values of a row: N = 8 with 16-byte (fp32: 32-byte) accesses, or 1.
+template <int IN, int N>
+FP8L_DEV void load_n(const void* p, int64_t i, float (&v)[N]) {
+  if constexpr (N == 8) load8<IN>(p, i, v);
+  else v[0] = load1<IN>(p, i);
+}
+template <int IN, int N>
+FP8L_DEV void store_n(void* p, int64_t i, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    store1<IN>(p, i, v[0]);
+  } else if constexpr (IN == kInF32) {
+    float4* const q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = IN == kInF16 ? f32_to_f16(v[2 * j]) | (f32_to_f16(v[2 * j + 1]) << 16)
+                          : pk_bf16(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// out[t] = sum_i w[t, i] y[pos[t, i]], in slot order in 32 bits, rounded once.
+template <int IN, int N>
+__global__ __launch_bounds__(kRThreads) void combine_kernel(CombineArgs a) {
+  const int piece = blockIdx.y * (1 << a.grid.width_log) + (threadIdx.x & ((1 << a.grid.width_log) - 1));
+  if (piece >= a.grid.pieces) return;
+  const int per = kRThreads >> a.grid.width_log;
+  const int64_t at = (int64_t)piece * N;
+  for (int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.grid.width_log); t < a.T;
+       t += (int64_t)gridDim.x * per) {
+    float acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    for (int i = 0; i < a.k; ++i) {
+      const int p = a.pos[t * a.k + i];
+      if (p < 0 || p >= a.R) continue;
+      const float w = a.w ? a.w[t * a.k + i] : 1.0f;
+      float v[N];
+      load_n<IN>(a.y, p * a.D + at, v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = __builtin_fmaf(w, v[j], acc[j]);
+    }
+    store_n<IN>(a.out, t * a.D + at, acc);
+  }
+}
+
+struct CombineBwdArgs {
+  const void* dout;    // [T][D]
+  const void* y;       // [R][D]
+  const int32_t* pos;
+  const float* w;
+  void* dy;            // [R][D] or null
+  float* dw;           // [T][k] or null
+  int32_t T, k, R;
+  int64_t D;
+};
+
+// dy[pos[t, i]] = w[t, i] dout[t] and dw[t, i] = dout[t] . y[pos[t, i]]: one
+// wave per token, eight slots at a time.
+template <int IN, int N>
+__global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a) {
+  constexpr int S = 8;
+  const int lane = threadIdx.x & 63;
+  const int64_t pieces = a.D / N;
+  for (int64_t t = (int64_t)blockIdx.x * (kRThreads / 64) + (threadIdx.x >> 6); t < a.T;
+       t += (int64_t)gridDim.x * (kRThreads / 64)) {
+    for (int i0 = 0; i0 < a.k; i0 += S) {
+      int p[S];
+      float w[S], dot[S];
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const bool in = i0 + s < a.k;
+        p[s] = in ? a.pos[t * a.k + i0 + s] : -1;
+        if (p[s] >= a.R) p[s] = -1;
+        w[s] = in ? a.w[t * a.k + i0 + s] : 0.0f;
+        dot[s] = 0.0f;
+      }
+      for (int64_t c = lane; c < pieces; c += 64) {
+        float g[N];
+        load_n<IN>(a.dout, t * a.D + c * N, g);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if (p[s] < 0) continue;
+          const int64_t at = p[s] * a.D + c * N;
+          if (a.dw) {
+            float v[N];
+            load_n<IN>(a.y, at, v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) dot[s] = __builtin_fmaf(g[j], v[j], dot[s]);
+          }
+          if (a.dy) {
+            float v[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = w[s] * g[j];
+            store_n<IN>(a.dy, at, v);
+          }
+        }
+      }
+      if (a.dw) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const float d = lanes_sum<64>(dot[s]);
+          if (lane == 0 && i0 + s < a.k) a.dw[t * a.k + i0 + s] = d;
+        }
+      }
+    }
+  }
+}
+
+}  // namespace fp8l
