@@ -84,7 +84,8 @@ typedef enum {
   FP8_DT_BF16 = 2,
   FP8_DT_E4M3 = 3,
   FP8_DT_E5M2 = 4,
-  FP8_DT_I8 = 5 /* 8-bit integers with one scale per row (fp8_i8_* only) */
+  FP8_DT_I8 = 5, /* 8-bit integers with one scale per row (fp8_i8_* only) */
+  FP8_DT_MX4 = 6 /* 4-bit floating point with block scales (fp8_mx4_* only) */
 } fp8_dtype_t;
 
 /*
@@ -658,6 +659,70 @@ int fp8_route_combine(int64_t T, int32_t k, int64_t D, int64_t R, const void* y,
 int fp8_route_combine_bwd(int64_t T, int32_t k, int64_t D, int64_t R, const void* dout,
                           const void* y, int32_t dtype, const int32_t* pos, const float* weights,
                           void* dy, float* dweights, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Linear layers in microscaled 4-bit floating point (serving): blocks of 32
+ * values along K share a power of two, elements are E2M1 (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives) [MX: OCP Microscaling Formats v1.0, MXFP4].
+ * A matrix [rows, K] is, with B = ceil(K / 32):
+ *   codes   [rows][16 B] bytes, 16-byte aligned: element 2 j of a row in the
+ *           low half of its byte j; elements past K are zeros.
+ *   scales  [ceil(K / 128)][rows][4] bytes, 4-byte aligned: byte i of word
+ *           [s][r] is the biased exponent (scale 2^(e - 127), 255: NaN) of
+ *           block 4 s + i of row r; bytes past block B are 0.  (Row-major
+ *           scales [rows][4 ceil(K / 128)] take this order when words are
+ *           transposed.)
+ * Limits (FP8_ERR_SHAPE otherwise): K < 2^24, rows ceil(K / 128) < 2^29; a
+ * pointer aligned less than stated is FP8_ERR_SHAPE too.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of the codes and of the scales of a matrix (0 for refused sizes). */
+size_t fp8_mx4_code_bytes(int64_t rows, int64_t K);
+size_t fp8_mx4_scale_bytes(int64_t rows, int64_t K);
+
+/*
+ * Quantize: a block's exponent is that of its largest magnitude less 2 (not
+ * below 2^-127), its elements x / scale rounded to nearest, ties to even,
+ * saturating at 6.  A block that holds a NaN or an infinity gets the scale NaN
+ * and zeros.  x [mats][rows][K] F32, F16 or BF16; the matrices' codes and
+ * scales lie one after the other (mats <= 65535).
+ */
+int fp8_mx4_quantize(const void* x, int32_t in_dtype, int64_t mats, int64_t rows, int64_t K,
+                     uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* The values of codes and scales, rounded once to out_dtype: out
+ * [mats][rows][K] F32, F16 or BF16. */
+int fp8_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t mats, int64_t rows,
+                       int64_t K, void* out, int32_t out_dtype, hipStream_t stream);
+
+/*
+ * Y = X W^T (+ bias) of the quantized values, summed in 32 bits, one rounding.
+ *   x         F32 / F16 / BF16 [M, K]: quantized here, codes to x4_out and
+ *             scales to sx_out (both required); or x_dtype FP8_DT_MX4: codes
+ *             with x_scales (x4_out, sx_out unused).
+ *   w         codes of [N, K] with w_scales.
+ *   bias      [N] of out_dtype, or NULL.
+ *   y         [M, N], out_dtype FP8_DT_BF16 or FP8_DT_F16.
+ * A NaN scale gives NaN in the outputs of its row of x or w, nowhere else.
+ */
+int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x_dtype,
+                       const uint8_t* x_scales, const uint8_t* w, const uint8_t* w_scales,
+                       const void* bias, int32_t out_dtype, void* y, uint8_t* x4_out,
+                       uint8_t* sx_out, hipStream_t stream);
+
+/*
+ * The same over ragged groups of rows (offsets, T, E as in
+ * fp8_grouped_linear_fwd): E matrices w [N, K] one after the other, with their
+ * scales likewise, bias [E, N].  Rows behind offsets[E] are not quantized and
+ * their rows of y are left as they were (of x4_out and sx_out too); of rows
+ * before offsets[0] the same holds for y, and x4_out and sx_out may or may not
+ * receive their codes.
+ */
+int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
+                               const void* x, int32_t x_dtype, const uint8_t* x_scales,
+                               const uint8_t* w, const uint8_t* w_scales, const void* bias,
+                               int32_t out_dtype, void* y, uint8_t* x4_out, uint8_t* sx_out,
+                               hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,7 @@ from ._build import LIB_PATH
 
 FP8_E4M3, FP8_E5M2 = 0, 1
 FP8_DT_F32, FP8_DT_F16, FP8_DT_BF16, FP8_DT_E4M3, FP8_DT_E5M2, FP8_DT_I8 = 0, 1, 2, 3, 4, 5
+FP8_DT_MX4 = 6
 FP8_OK, FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_DTYPE, FP8_ERR_RING, FP8_ERR_HIP = range(6)
 FP8_K_CONTIG, FP8_K_STRIDED = 0, 1
 FP8_QUANT_ROWS, FP8_QUANT_TRANSPOSED, FP8_QUANT_DUAL = 0, 1, 2
@@ -39,6 +40,8 @@ C_SYMBOLS = (
     "fp8_grouped_linear_bwd", "fp8_i8_quantize_rows", "fp8_i8_linear_fwd",
     "fp8_i8_grouped_linear_fwd", "fp8_route_workspace_bytes", "fp8_route_fwd", "fp8_route_bwd",
     "fp8_route_plan", "fp8_route_gather", "fp8_route_combine", "fp8_route_combine_bwd",
+    "fp8_mx4_code_bytes", "fp8_mx4_scale_bytes", "fp8_mx4_quantize", "fp8_mx4_dequantize",
+    "fp8_mx4_linear_fwd", "fp8_mx4_grouped_linear_fwd",
 )
 
 
@@ -113,8 +116,16 @@ def lib() -> ctypes.CDLL:
         L.fp8_route_gather.argtypes = [i64, i32, i64, i64, vp, vp, vp, vp]
         L.fp8_route_combine.argtypes = [i64, i32, i64, i64, vp, i32, vp, vp, vp, vp]
         L.fp8_route_combine_bwd.argtypes = [i64, i32, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp]
+        L.fp8_mx4_code_bytes.restype = L.fp8_mx4_scale_bytes.restype = sz
+        L.fp8_mx4_code_bytes.argtypes = L.fp8_mx4_scale_bytes.argtypes = [i64, i64]
+        L.fp8_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+        L.fp8_mx4_dequantize.argtypes = [vp, vp, i64, i64, i64, vp, i32, vp]
+        L.fp8_mx4_linear_fwd.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+        L.fp8_mx4_grouped_linear_fwd.argtypes = [i64, i32, i64, i64, vp, vp, i32, vp, vp, vp, vp,
+                                                 i32, vp, vp, vp, vp]
         for name in ("fp8_route_fwd", "fp8_route_bwd", "fp8_route_plan", "fp8_route_gather",
-                     "fp8_route_combine", "fp8_route_combine_bwd"):
+                     "fp8_route_combine", "fp8_route_combine_bwd", "fp8_mx4_quantize",
+                     "fp8_mx4_dequantize", "fp8_mx4_linear_fwd", "fp8_mx4_grouped_linear_fwd"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("fp8_grouped_linear_fwd", "fp8_grouped_linear_bwd", "fp8_i8_quantize_rows",
                      "fp8_i8_linear_fwd", "fp8_i8_grouped_linear_fwd"):
@@ -150,6 +161,14 @@ def fp8_db_workspace_bytes(M: int, N: int) -> int:
 
 def fp8_grouped_db_workspace_bytes(T: int, E: int, N: int) -> int:
     return lib().fp8_grouped_db_workspace_bytes(T, E, N)
+
+
+def fp8_mx4_code_bytes(rows: int, K: int) -> int:
+    return lib().fp8_mx4_code_bytes(rows, K)
+
+
+def fp8_mx4_scale_bytes(rows: int, K: int) -> int:
+    return lib().fp8_mx4_scale_bytes(rows, K)
 
 
 def fp8_route_workspace_bytes(T: int, E: int, k: int) -> int:
@@ -887,6 +906,150 @@ def fp8_i8_grouped_linear_fwd(x, w, bias, offsets, y, x8_out=None, sx_out=None, 
 def bind_fp8_i8_grouped_linear_fwd(x, w, bias, offsets, y, x8_out=None, sx_out=None, stream=None):
     return _bind_run("fp8_i8_grouped_linear_fwd", *_i8_grouped_args(x, w, bias, offsets, y, x8_out,
                                                                     sx_out, stream))
+
+
+# ---------------------------------------------------------------- 4-bit floating point
+
+@dataclass
+class QuantizedMx4:
+    """Operand in microscaled 4-bit floating point: uint8 codes
+    [.., rows, 16 ceil(k / 32)] (two to a byte), uint8 scales
+    [.., ceil(k / 128), rows, 4] (biased exponents, four blocks of 32 values to
+    a word), and k, the values in a row."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+
+    @staticmethod
+    def empty(*shape, device="cuda"):
+        """Buffers for a matrix, or a stack of matrices, of the given shape."""
+        *lead, rows, k = shape
+        return QuantizedMx4(
+            torch.empty(*lead, rows, 16 * (-(-k // 32)), dtype=torch.uint8, device=device),
+            torch.empty(*lead, -(-k // 128), rows, 4, dtype=torch.uint8, device=device), k)
+
+
+def _mx4_shapes(lead, rows, k):
+    return (*lead, rows, 16 * (-(-k // 32))), (*lead, -(-k // 128), rows, 4)
+
+
+def _mx4_pointers(codes, scales, what, lead, rows, k, dev):
+    sc, ss = _mx4_shapes(lead, rows, k)
+    return _arg(codes, f"{what}.codes", _U8, sc, dev), _arg(scales, f"{what}.scale", _U8, ss, dev)
+
+
+def _mx4_quantize_args(x, codes, scales, stream):
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x: expected a matrix or a stack of matrices")
+    dev, (*lead, rows, k) = x.device, x.shape
+    mats = 1
+    for d in lead:
+        mats *= d
+    return (_arg(x, "x", _HP, None, dev), _TORCH_DT[x.dtype], mats, rows, k,
+            *_mx4_pointers(codes, scales, "out", lead, rows, k, dev), _arg_stream(stream, dev)), dev
+
+
+def fp8_mx4_quantize(x, codes, scales, stream=None):
+    """x [.., rows, k] to 4-bit codes and block exponents (the buffers of
+    QuantizedMx4.empty(*x.shape))."""
+    _run("fp8_mx4_quantize", *_mx4_quantize_args(x, codes, scales, stream))
+
+
+def bind_fp8_mx4_quantize(x, codes, scales, stream=None):
+    return _bind_run("fp8_mx4_quantize", *_mx4_quantize_args(x, codes, scales, stream))
+
+
+def _mx4_dequantize_args(q, out, stream):
+    if not isinstance(q, QuantizedMx4):
+        raise TypeError("q: expected a QuantizedMx4 operand")
+    if not isinstance(out, torch.Tensor) or out.dim() < 2:
+        raise ValueError("out: expected a matrix or a stack of matrices")
+    dev, (*lead, rows, k) = out.device, out.shape
+    if k != q.cols:
+        raise ValueError(f"out: rows of {k} values, q has {q.cols}")
+    mats = 1
+    for d in lead:
+        mats *= d
+    return (*_mx4_pointers(q.codes, q.scale, "q", lead, rows, k, dev), mats, rows, k,
+            _arg(out, "out", _HP, None, dev), _TORCH_DT[out.dtype], _arg_stream(stream, dev)), dev
+
+
+def fp8_mx4_dequantize(q, out, stream=None):
+    """The values of q (QuantizedMx4), rounded once to out's type."""
+    _run("fp8_mx4_dequantize", *_mx4_dequantize_args(q, out, stream))
+
+
+def bind_fp8_mx4_dequantize(q, out, stream=None):
+    return _bind_run("fp8_mx4_dequantize", *_mx4_dequantize_args(q, out, stream))
+
+
+def _mx4_args(x, w, bias, y, x4_out, sx_out, lead, bshape, dev):
+    """C arguments shared by the dense and the grouped call: x, its type and
+    scales, w and its scales, bias, out dtype, y, x4_out, sx_out."""
+    N, k = w.codes.shape[-2], w.cols
+    if isinstance(x, QuantizedMx4):
+        M = _shape_of(x.codes, 2, "x.codes")[0]
+        if x.cols != k:
+            raise ValueError(f"x: rows of {x.cols} values, w has {k}")
+        xp, xs = _mx4_pointers(x.codes, x.scale, "x", (), M, k, dev)
+        dt, qp, sp = FP8_DT_MX4, None, None
+    else:
+        M = _shape_of(x, 2, "x")[0]
+        xp, xs, dt = _arg(x, "x", _HP, (M, k), dev), None, _TORCH_DT[x.dtype]
+        sc, ss = _mx4_shapes((), M, k)
+        qp, sp = _arg(x4_out, "x4_out", _U8, sc, dev), _arg(sx_out, "sx_out", _U8, ss, dev)
+    wp, wsp = _mx4_pointers(w.codes, w.scale, "w", lead, N, k, dev)
+    return (xp, dt, xs, wp, wsp, _arg(bias, "bias", _OUT16 if y is None else (y.dtype,), bshape, dev,
+                                      True),
+            _TORCH_DT.get(getattr(y, "dtype", None), -1), _arg(y, "y", _OUT16, (M, N), dev), qp, sp)
+
+
+def _mx4_linear_args(x, w, bias, y, x4_out, sx_out, stream):
+    if not isinstance(w, QuantizedMx4):
+        raise TypeError("w: expected a QuantizedMx4 operand")
+    N = _shape_of(w.codes, 2, "w.codes")[0]
+    xc = x.codes if isinstance(x, QuantizedMx4) else x
+    dev = _gpu_of(xc, "x")
+    M = _shape_of(xc, 2, "x")[0]
+    return (M, N, w.cols, *_mx4_args(x, w, bias, y, x4_out, sx_out, (), (N,), dev),
+            _arg_stream(stream, dev)), dev
+
+
+def fp8_mx4_linear_fwd(x, w, bias, y, x4_out=None, sx_out=None, stream=None):
+    """y = x w^T (+ bias) in 4-bit floating point.  x: [M, k] tensor (quantized
+    here into x4_out and sx_out, the buffers of QuantizedMx4.empty(M, k)) or
+    QuantizedMx4; w: QuantizedMx4 of [N, k]; y bf16 or fp16 [M, N]; bias of y's
+    dtype [N] or None."""
+    _run("fp8_mx4_linear_fwd", *_mx4_linear_args(x, w, bias, y, x4_out, sx_out, stream))
+
+
+def bind_fp8_mx4_linear_fwd(x, w, bias, y, x4_out=None, sx_out=None, stream=None):
+    return _bind_run("fp8_mx4_linear_fwd", *_mx4_linear_args(x, w, bias, y, x4_out, sx_out, stream))
+
+
+def _mx4_grouped_args(x, w, bias, offsets, y, x4_out, sx_out, stream):
+    if not isinstance(w, QuantizedMx4):
+        raise TypeError("w: expected a QuantizedMx4 operand")
+    E, N, _ = _shape_of(w.codes, 3, "w.codes")
+    xc = x.codes if isinstance(x, QuantizedMx4) else x
+    dev = _gpu_of(xc, "x")
+    T = _shape_of(xc, 2, "x")[0]
+    return (T, E, N, w.cols, _arg(offsets, "offsets", _I32, (E + 1,), dev),
+            *_mx4_args(x, w, bias, y, x4_out, sx_out, (E,), (E, N), dev),
+            _arg_stream(stream, dev)), dev
+
+
+def fp8_mx4_grouped_linear_fwd(x, w, bias, offsets, y, x4_out=None, sx_out=None, stream=None):
+    """fp8_mx4_linear_fwd over experts: w QuantizedMx4 of [E, N, k], bias
+    [E, N], offsets as in fp8_grouped_linear_fwd.  Rows behind the last
+    expert's are left as they were in y, x4_out and sx_out."""
+    _run("fp8_mx4_grouped_linear_fwd", *_mx4_grouped_args(x, w, bias, offsets, y, x4_out, sx_out,
+                                                          stream))
+
+
+def bind_fp8_mx4_grouped_linear_fwd(x, w, bias, offsets, y, x4_out=None, sx_out=None, stream=None):
+    return _bind_run("fp8_mx4_grouped_linear_fwd", *_mx4_grouped_args(x, w, bias, offsets, y,
+                                                                      x4_out, sx_out, stream))
 
 
 # ---------------------------------------------------------------- routing to experts

@@ -13,8 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libfp8linear.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = [os.path.join(CSRC, f) for f in ("fp8l_api.hip", "fp8l_grouped.hip", "fp8l_i8.hip", "fp8l_route.hip",
-                                           "fp8l_version.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fp8l_api.hip", "fp8l_grouped.hip", "fp8l_i8.hip", "fp8l_mx4.hip",
+                                           "fp8l_route.hip", "fp8l_version.hip")]
 OBJ_DIR = os.path.join(HERE, "_build")  # objects; not tracked
 PROBE_LIB_PATH = os.path.join(HERE, "libfp8probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "fp8l_probe.hip")]

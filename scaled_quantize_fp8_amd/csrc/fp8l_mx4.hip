@@ -1,0 +1,212 @@
+// C entry points of the linear layers in microscaled 4-bit floating point,
+// dense and over ragged groups of rows.  Checks run before the first launch;
+// nothing is allocated.
+#include <type_traits>
+
+#include "fp8l_grouped_host.hpp"
+#include "fp8l_mx4.hpp"
+
+namespace fp8l {
+namespace {
+
+// 256 rows of codes stay below 2^31 bytes, a matrix' scale words below 2^29:
+// the offsets inside a buffer resource.
+constexpr int64_t kMxMaxK = (1 << 24) - 1;
+constexpr int64_t kMxMaxWords = 1 << 29;
+
+int64_t mx_blocks(int64_t K) { return (K + 31) / 32; }
+int64_t mx_steps(int64_t K) { return (K + 127) / 128; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+int check_mx(int64_t rows, int64_t K) {
+  if (rows < 0 || K < 0 || K > kMxMaxK || rows > INT32_MAX) return FP8_ERR_SHAPE;
+  return mx_steps(K) > 0 && rows >= kMxMaxWords / mx_steps(K) ? FP8_ERR_SHAPE : FP8_OK;
+}
+
+template <class F>
+void by_type(int32_t dt, F&& f) {
+  if (dt == FP8_DT_F32) f(std::integral_constant<int, kInF32>{});
+  else if (dt == FP8_DT_F16) f(std::integral_constant<int, kInF16>{});
+  else f(std::integral_constant<int, kInBF16>{});
+}
+
+// Tiles of 16 rows (fewer where there are no more), walked along K by as many
+// blocks as give the chip about 16 per CU.
+dim3 quant_grid(int64_t mats, int64_t rows, int64_t steps, int32_t* rows_log) {
+  int log = 0;
+  while (log < 4 && (1 << log) < rows) ++log;
+  *rows_log = log;
+  const int64_t bx = (rows + (1 << log) - 1) >> log, cap = 1 << 20;
+  const int64_t across = 16 >> log, most = (steps + across - 1) / across;
+  int64_t by = (16 * cu_count() + bx * mats - 1) / (bx * mats);
+  by = by < most ? by : most;
+  return dim3((unsigned)(bx < cap ? bx : cap), (unsigned)(by < 65535 ? by : 65535), (unsigned)mats);
+}
+
+void enqueue_mx_quantize(const void* x, int32_t dt, int64_t mats, int64_t rows, int64_t K,
+                         uint8_t* codes, uint8_t* scales, const int32_t* valid, hipStream_t st) {
+  if (mats == 0 || rows == 0 || K == 0) return;
+  MxQuantArgs a = {x, codes, reinterpret_cast<uint32_t*>(scales), rows, K, (int32_t)mx_steps(K),
+                   (int32_t)mx_blocks(K), 0, 0, valid};
+  a.vec = aligned16(x) && K % 8 == 0;
+  const dim3 grid = quant_grid(mats, rows, a.steps, &a.rows_log);
+  by_type(dt, [&](auto in) {
+    hipLaunchKernelGGL((mx4_quantize_kernel<decltype(in)::value>), grid, dim3(kMxThreads), 0, st, a);
+  });
+}
+
+int check_linear(int64_t M, int64_t N, int64_t K, const void* x, int32_t x_dtype,
+                 const uint8_t* x_scales, const uint8_t* w, const uint8_t* w_scales,
+                 int32_t out_dtype, const void* y, const uint8_t* x4_out, const uint8_t* sx_out) {
+  if (out_dtype != FP8_DT_BF16 && out_dtype != FP8_DT_F16) return FP8_ERR_DTYPE;
+  if (!is_hp(x_dtype) && x_dtype != FP8_DT_MX4) return FP8_ERR_DTYPE;
+  const bool hp = is_hp(x_dtype);
+  const void* const xc = hp ? x4_out : x;
+  const uint8_t* const xs = hp ? sx_out : x_scales;
+  if (M > 0 && K > 0 && (!x || !xc || !xs)) return FP8_ERR_NULL;
+  if (N > 0 && K > 0 && (!w || !w_scales)) return FP8_ERR_NULL;
+  if (M > 0 && N > 0 && !y) return FP8_ERR_NULL;
+  if (!aligned16(xc) || !aligned4(xs) || !aligned16(w) || !aligned4(w_scales)) return FP8_ERR_SHAPE;
+  return FP8_OK;
+}
+
+MxArgs mx_args(int64_t M, int64_t N, int64_t K, const void* x, int32_t x_dtype,
+               const uint8_t* x_scales, const uint8_t* w, const uint8_t* w_scales, const void* bias,
+               int32_t out_dtype, void* y, const uint8_t* x4_out, const uint8_t* sx_out) {
+  MxArgs g = {};
+  g.a = is_hp(x_dtype) ? x4_out : reinterpret_cast<const uint8_t*>(x);
+  g.sa = reinterpret_cast<const uint32_t*>(is_hp(x_dtype) ? sx_out : x_scales);
+  g.b = w;
+  g.sb = reinterpret_cast<const uint32_t*>(w_scales);
+  g.ld = 16 * mx_blocks(K);
+  g.sa_step = M;
+  g.sb_step = N;
+  g.M = M;
+  g.N = N;
+  g.steps = (int32_t)mx_steps(K);
+  g.c = reinterpret_cast<uint16_t*>(y);
+  g.ldc = N;
+  g.bias = reinterpret_cast<const uint16_t*>(bias);
+  g.out_f16 = out_dtype == FP8_DT_F16;
+  g.c_vec = aligned16(y) && N % 8 == 0;
+  return g;
+}
+
+// Rows of a tile by the number of rows (of a group on average).
+int skinny_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 4; }
+
+template <class F>
+void by_count(int mt, F&& f) {
+  if (mt == 1) f(std::integral_constant<int, 1>{});
+  else if (mt == 2) f(std::integral_constant<int, 2>{});
+  else if (mt == 3) f(std::integral_constant<int, 3>{});
+  else f(std::integral_constant<int, 4>{});
+}
+
+// Tile columns of a skinny launch and the waves that split K in it.
+int skinny_cols(MxArgs& g, int64_t units) {
+  const int64_t cols = (g.N + 15) / 16;
+  const int kw = skinny_kw(units * cols, g.ld);
+  g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
+  return kw;
+}
+
+}  // namespace
+}  // namespace fp8l
+
+using namespace fp8l;
+
+extern "C" {
+
+size_t fp8_mx4_code_bytes(int64_t rows, int64_t K) {
+  return check_mx(rows, K) ? 0 : (size_t)(rows * mx_blocks(K) * 16);
+}
+
+size_t fp8_mx4_scale_bytes(int64_t rows, int64_t K) {
+  return check_mx(rows, K) ? 0 : (size_t)(rows * mx_steps(K) * 4);
+}
+
+int fp8_mx4_quantize(const void* x, int32_t in_dtype, int64_t mats, int64_t rows, int64_t K,
+                     uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  if (mats < 0 || mats > 65535) return FP8_ERR_SHAPE;
+  const int st = check_mx(rows, K);
+  if (st) return st;
+  if (!is_hp(in_dtype)) return FP8_ERR_DTYPE;
+  if (mats == 0 || rows == 0 || K == 0) return FP8_OK;
+  if (!x || !codes || !scales) return FP8_ERR_NULL;
+  if (!aligned16(codes) || !aligned4(scales)) return FP8_ERR_SHAPE;
+  enqueue_mx_quantize(x, in_dtype, mats, rows, K, codes, scales, nullptr, stream);
+  return hip_status();
+}
+
+int fp8_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t mats, int64_t rows,
+                       int64_t K, void* out, int32_t out_dtype, hipStream_t stream) {
+  if (mats < 0 || mats > 65535) return FP8_ERR_SHAPE;
+  const int st = check_mx(rows, K);
+  if (st) return st;
+  if (!is_hp(out_dtype)) return FP8_ERR_DTYPE;
+  if (mats == 0 || rows == 0 || K == 0) return FP8_OK;
+  if (!codes || !scales || !out) return FP8_ERR_NULL;
+  if (!aligned16(codes) || !aligned4(scales)) return FP8_ERR_SHAPE;
+  MxDequantArgs a = {codes, reinterpret_cast<const uint32_t*>(scales), out, rows, K,
+                     (int32_t)mx_steps(K), (int32_t)mx_blocks(K), 0, 0};
+  a.vec = aligned16(out) && K % 8 == 0;
+  const dim3 grid = quant_grid(mats, rows, a.steps, &a.rows_log);
+  by_type(out_dtype, [&](auto in) {
+    hipLaunchKernelGGL((mx4_dequantize_kernel<decltype(in)::value>), grid, dim3(kMxThreads), 0,
+                       stream, a);
+  });
+  return hip_status();
+}
+
+int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x_dtype,
+                       const uint8_t* x_scales, const uint8_t* w, const uint8_t* w_scales,
+                       const void* bias, int32_t out_dtype, void* y, uint8_t* x4_out,
+                       uint8_t* sx_out, hipStream_t stream) {
+  int st = check_mx(M, K);
+  if (st || (st = check_mx(N, K))) return st;
+  if (!mul_ok(M, N) || !grid_fits(((M + 63) / 64) * ((N + 15) / 16), 512)) return FP8_ERR_SHAPE;
+  if ((st = check_linear(M, N, K, x, x_dtype, x_scales, w, w_scales, out_dtype, y, x4_out, sx_out)))
+    return st;
+  if (is_hp(x_dtype)) enqueue_mx_quantize(x, x_dtype, 1, M, K, x4_out, sx_out, nullptr, stream);
+  if (M == 0 || N == 0) return hip_status();
+  MxArgs g = mx_args(M, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
+  by_count(skinny_tiles(M), [&](auto mt) {
+    constexpr int MT = decltype(mt)::value;
+    const int64_t units = (M + 16 * MT - 1) / (16 * MT);
+    const int kw = skinny_cols(g, units);
+    hipLaunchKernelGGL((mx4_skinny_kernel<MT>), dim3((unsigned)(units * g.tiles_n)), dim3(512),
+                       kw > 1 ? MxSkinny<MT>::kLds : 0, stream, g, kw);
+  });
+  return hip_status();
+}
+
+int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const int32_t* offsets,
+                               const void* x, int32_t x_dtype, const uint8_t* x_scales,
+                               const uint8_t* w, const uint8_t* w_scales, const void* bias,
+                               int32_t out_dtype, void* y, uint8_t* x4_out, uint8_t* sx_out,
+                               hipStream_t stream) {
+  int st = check_grouped(T, E, N, K);
+  if (st || (st = check_mx(T, K)) || (st = check_mx(N, K))) return st;
+  if (!grid_fits(most_units(T, E, 64) * ((N + 15) / 16), 512)) return FP8_ERR_SHAPE;
+  if (!offsets) return FP8_ERR_NULL;
+  if ((st = check_linear(T, N, K, x, x_dtype, x_scales, w, w_scales, out_dtype, y, x4_out, sx_out)))
+    return st;
+  if (is_hp(x_dtype))
+    enqueue_mx_quantize(x, x_dtype, 1, T, K, x4_out, sx_out, offsets + E, stream);
+  if (T == 0 || N == 0) return hip_status();
+  MxArgs g = mx_args(T, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
+  const MxStrides s = {N * g.ld, N * g.steps, N};
+  const Groups gr = {offsets, E, (int32_t)T};
+  by_count(skinny_tiles((T + E - 1) / E), [&](auto mt) {
+    constexpr int MT = decltype(mt)::value;
+    const int64_t units = most_units(T, E, 16 * MT);
+    const int kw = skinny_cols(g, units);
+    const int64_t most = (units * g.tiles_n + 7) & ~7LL;
+    hipLaunchKernelGGL((mx4_skinny_groups_kernel<MT>), dim3((unsigned)most), dim3(512),
+                       kw > 1 ? MxSkinny<MT>::kLds : 0, stream, g, gr, s, kw);
+  });
+  return hip_status();
+}
+
+}  // extern "C"

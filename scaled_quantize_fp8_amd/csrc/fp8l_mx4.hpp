@@ -1,0 +1,338 @@
+// Linear layers in microscaled 4-bit floating point: blocks of 32 values
+// along K share a power of two (E8M0, a biased exponent in a byte), elements
+// are E2M1 (sign, two exponent bits, one of significand: 0, 0.5, 1, 1.5, 2,
+// 3, 4, 6) [MX: OCP Microscaling Formats specification v1.0].
+//
+//   quantize  amax of a block = 1.f 2^a:  scale 2^(a - 2) (2 is E2M1's largest
+//             exponent), not below 2^-127; elements x / scale, rounded to
+//             nearest, ties to even, saturating at 6.  x / scale is exact in
+//             32 bits, so the codes are those of the definition.  A block that
+//             holds a NaN or an infinity gets the scale NaN (0xFF) and zeros.
+//   product   Y[m, n] = sum over blocks of 2^(ex + ew) sum_32 qx qw (+ b[n]),
+//             by the scaled MFMA, summed in 32 bits, rounded once.
+//
+// Layout of a matrix [rows, K], with B = ceil(K / 32) blocks a row:
+//   codes   [rows][16 B] bytes, element 2 j of a row in byte j's low half;
+//           elements past K are zeros, so every row is whole blocks and any K
+//           takes the same path.
+//   scales  [ceil(B / 4)][rows][4] bytes: one 32-bit word holds the four
+//           blocks of a step of 128 values, and the words of neighbouring rows
+//           lie side by side, so that a wave fetches its rows' scales of a
+//           step as one contiguous piece (row-major scales would touch a line
+//           per row for 4 bytes of it).  Bytes past B are zeros.
+#pragma once
+
+#include "fp8l_gemm3.hpp"
+#include "fp8l_grouped.hpp"
+#include "fp8l_values.hpp"
+
+namespace fp8l {
+
+constexpr int kMxThreads = 256;
+
+struct MxQuantArgs {
+  const void* x;       // [mats][rows][K]
+  uint8_t* codes;
+  uint32_t* scales;    // words
+  int64_t rows, K;
+  int32_t steps, blocks;  // ceil(K / 128), ceil(K / 32)
+  int32_t vec;            // 16-byte loads of whole pieces of 8 values
+  int32_t rows_log;       // rows of a block's tile: 1 << rows_log (0..4)
+  const int32_t* valid;   // device row count, or null: all rows
+};
+
+// Biased exponent of a block's scale from the bits of its amax, 255: NaN.
+FP8L_DEV uint32_t mx_scale(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23) - 2;
+  return amax_bits > 0x7f7fffffu ? 255u : (uint32_t)max(e, 0);
+}
+// 1 / scale, exact (2^(127 - e) with e <= 252 is a normal number).
+FP8L_DEV float mx_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+
+// Eight values already divided by their scale to eight codes.
+FP8L_DEV uint32_t mx_codes8(const float v[8], float inv) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * inv, v[1] * inv, 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * inv, v[3] * inv, 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * inv, v[5] * inv, 1.0f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * inv, v[7] * inv, 1.0f, 3);
+  return w;
+}
+
+// 16 lanes hold a step of 128 values, 8 each: four lanes a block, whose amax
+// they share by two DPP steps, then the four blocks' exponents meet in a word.
+// A block of 256 threads walks its tile of rows along K.
+template <int IN>
+__global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a) {
+  const int sl = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int per = 1 << a.rows_log;           // rows of the tile
+  const int across = 16 >> a.rows_log;       // steps side by side
+  const int64_t rows = a.valid ? min<int64_t>(max(*a.valid, 0), a.rows) : a.rows;
+  const int64_t mat = blockIdx.z;
+  const int64_t row_bytes = (int64_t)a.blocks * 16;
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += (int64_t)gridDim.x * per) {
+    const int64_t r = r0 + (grp & (per - 1));
+    for (int64_t s = (int64_t)blockIdx.y * across + (grp >> a.rows_log); s < a.steps;
+         s += (int64_t)gridDim.y * across) {
+      const int64_t k = s * 128 + 8 * sl;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      if (r < rows) {
+        const int64_t at = (mat * a.rows + r) * a.K + k;
+        if (a.vec) {
+          if (k < a.K) load8<IN>(a.x, at, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (k + i < a.K) v[i] = load1<IN>(a.x, at + i);
+        }
+      }
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = max(mx, absbits(v[i]));
+      mx = max(mx, (uint32_t)__builtin_amdgcn_mov_dpp((int)mx, 0xB1, 0xF, 0xF, false));
+      mx = max(mx, (uint32_t)__builtin_amdgcn_mov_dpp((int)mx, 0x4E, 0xF, 0xF, false));
+      const bool inside = 4 * s + (sl >> 2) < a.blocks;
+      const uint32_t e = inside ? mx_scale(mx) : 0u;
+      uint32_t word = e << (8 * (sl >> 2));
+      word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)word, 0x141, 0xF, 0xF, false);
+      word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)word, 0x140, 0xF, 0xF, false);
+      if (r < rows) {
+        if (inside)
+          *reinterpret_cast<uint32_t*>(a.codes + (mat * a.rows + r) * row_bytes + s * 64 + 4 * sl) =
+              e == 255u ? 0u : mx_codes8(v, mx_inverse(e));
+        if (sl == 0) a.scales[(mat * a.steps + s) * a.rows + r] = word;
+      }
+    }
+  }
+}
+
+struct MxDequantArgs {
+  const uint8_t* codes;
+  const uint32_t* scales;
+  void* out;            // [mats][rows][K]
+  int64_t rows, K;
+  int32_t steps, blocks, vec, rows_log;
+};
+
+// The values of the codes, rounded once to the output's type.
+template <int IN>
+__global__ __launch_bounds__(kMxThreads) void mx4_dequantize_kernel(MxDequantArgs a) {
+  const int sl = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int per = 1 << a.rows_log, across = 16 >> a.rows_log;
+  const int64_t mat = blockIdx.z;
+  const int64_t row_bytes = (int64_t)a.blocks * 16;
+  for (int64_t r = (int64_t)blockIdx.x * per + (grp & (per - 1)); r < a.rows;
+       r += (int64_t)gridDim.x * per) {
+    for (int64_t s = (int64_t)blockIdx.y * across + (grp >> a.rows_log); s < a.steps;
+         s += (int64_t)gridDim.y * across) {
+      const int64_t k = s * 128 + 8 * sl;
+      if (k >= a.K) continue;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(
+          a.codes + (mat * a.rows + r) * row_bytes + s * 64 + 4 * sl);
+      const uint32_t word = a.scales[(mat * a.steps + s) * a.rows + r];
+      const uint32_t e = (word >> (8 * (sl >> 2))) & 255u;
+      float v[8];
+      const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+      const f32x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+      const f32x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+      const f32x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+      v[0] = p0.x; v[1] = p0.y; v[2] = p1.x; v[3] = p1.y;
+      v[4] = p2.x; v[5] = p2.y; v[6] = p3.x; v[7] = p3.y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = e == 255u ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(v[i], (int)e - 127);
+      const int64_t at = (mat * a.rows + r) * a.K + k;
+      if (a.vec) {
+        store8<IN>(a.out, at, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (k + i < a.K) store1<IN>(a.out, at + i, v[i]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+
+// A tile's problem: operands moved to its rows of X and columns of Y.
+struct MxArgs {
+  const uint8_t* a;      // codes of X, [M][ld]
+  const uint32_t* sa;    // its scale words, step s at sa + s * sa_step
+  const uint8_t* b;      // codes of W, [N][ld]
+  const uint32_t* sb;
+  int64_t ld, sa_step, sb_step;
+  int64_t M, N;          // rows and columns from here on
+  int32_t steps;         // ceil(K / 128)
+  uint16_t* c;           // [M][ldc], bf16 or fp16
+  int64_t ldc;
+  const uint16_t* bias;  // in c's type, or null
+  int32_t out_f16, c_vec;
+  int32_t tiles_m, tiles_n;
+};
+
+struct MxStrides {  // from one group's W to the next
+  int64_t b, sb, bias;
+};
+
+FP8L_DEV void mx_move(MxArgs& g, int64_t row, int64_t rows, int64_t col) {
+  g.a += row * g.ld;
+  g.sa += row;
+  g.M = rows;
+  g.b += col * g.ld;
+  g.sb += col;
+  g.N -= col;
+  g.c += row * g.ldc + col;
+  if (g.bias) g.bias += col;
+}
+
+FP8L_DEV float mx_half(const MxArgs& g, uint32_t h) {
+  return g.out_f16 ? f16_to_f32(h) : bf16_to_f32(h);
+}
+FP8L_DEV uint2 mx_pack4(const MxArgs& g, const float v[4]) {
+  if (g.out_f16)
+    return make_uint2(f32_to_f16(v[0]) | (f32_to_f16(v[1]) << 16),
+                      f32_to_f16(v[2]) | (f32_to_f16(v[3]) << 16));
+  return make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+}
+
+// Few rows (decoding): as the other formats' skinny kernels, a wave reads 16
+// rows of W straight into MFMA operands, no LDS and no barrier in the loop;
+// KW waves of a block share a tile column and split K, their partial sums
+// meet in LDS in wave order.  The 16x16x128 MFMA takes a block of 32 values
+// and its scale per lane (lane q 16 + r: row r, block q of the step).  A piece
+// is two steps: 128 bytes, a whole line, of every row.
+template <int MT>
+struct MxSkinny {
+  static constexpr int kBM = 16 * MT, kWaveN = 16, kThreads = 512, kLds = 8 * MT * 1024;
+  static constexpr int kU = MT == 1 ? 4 : (MT == 2 ? 3 : 2);  // pieces in flight
+
+  FP8L_DEV static v8i load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+    const v4i a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+    return v8i{a.x, a.y, a.z, a.w, 0, 0, 0, 0};
+  }
+  FP8L_DEV static v4f mma(v8i b, v8i a, v4f c, uint32_t sb, uint32_t sa) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 4, 4, 0, (int)sb, 0, (int)sa);
+  }
+  FP8L_DEV static void store(const MxArgs& g, int row, int64_t j, v4f acc) {
+    if (row >= g.M || j >= g.N) return;
+    float v[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v[t] = acc[t];
+      if (g.bias && j + t < g.N) v[t] += mx_half(g, g.bias[j + t]);
+    }
+    const uint2 w = mx_pack4(g, v);
+    uint16_t* const dst = g.c + row * g.ldc + j;
+    if (g.c_vec) {
+      *reinterpret_cast<uint2*>(dst) = w;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (j + t < g.N) dst[t] = (uint16_t)((t < 2 ? w.x : w.y) >> (16 * (t & 1)));
+    }
+  }
+
+  // g: moved to the tile's rows (at most kBM) and the block's first column.
+  FP8L_DEV static void run(const MxArgs& g, int KW, uint8_t* smem) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
+    const int j0 = jw * kWaveN;
+    const int cols = (int)min<int64_t>(g.N, JW * kWaveN);  // rows of W in reach
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.M * g.ld));
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b, (uint32_t)(cols * g.ld));
+    // scale words of rows past the end are those of other rows (or zeros past
+    // the last step): they meet zero codes or rows that are not stored
+    const __amdgpu_buffer_rsrc_t rsa =
+        make_rsrc(g.sa, (uint32_t)(((int64_t)(g.steps - 1) * g.sa_step + g.M) * 4));
+    const __amdgpu_buffer_rsrc_t rsb =
+        make_rsrc(g.sb, (uint32_t)(((int64_t)(g.steps - 1) * g.sb_step + cols) * 4));
+    const uint32_t ld = (uint32_t)g.ld;
+    v4f acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t pieces = ((uint32_t)g.steps + 1) / 2;
+    for (uint32_t p = kw; p < pieces; p += KW * kU) {
+      v8i fb[2 * kU], fa[2 * kU][MT];
+      uint32_t eb[2 * kU], ea[2 * kU][MT];
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u) {
+        const uint32_t s = 2 * (p + (u >> 1) * KW) + (u & 1);
+        const uint32_t k = s * 64 + 16 * q;
+        const bool in = k < ld;  // blocks and steps past the last: zeros
+        fb[u] = load16(rb, in ? (uint32_t)(j0 + r) * ld + k : 0x80000000u);
+        eb[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+            rsb, in ? (s * (uint32_t)g.sb_step + j0 + r) * 4 : 0x80000000u, 0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          fa[u][m] = load16(ra, in ? (uint32_t)(16 * m + r) * ld + k : 0x80000000u);
+          ea[u][m] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+              rsa, in ? (s * (uint32_t)g.sa_step + 16 * m + r) * 4 : 0x80000000u, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m] = mma(fb[u], fa[u][m], acc[m], eb[u] >> (8 * q), ea[u][m] >> (8 * q));
+    }
+    if (KW == 1) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) store(g, 16 * m + r, j0 + 4 * q, acc[m]);
+      return;
+    }
+    // partial sums: [wave][fragment][lane] x 16 bytes
+    v4f* const part = reinterpret_cast<v4f*>(smem);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = acc[m];
+    __syncthreads();
+    for (int f = wave; f < JW * MT; f += 8) {
+      const int fj = f / MT, fm = f % MT;
+      const v4f* src = part + (fj * KW * MT + fm) * 64 + lane;
+      v4f s = src[0];
+      for (int w = 1; w < KW; ++w) {
+        const v4f o = src[w * MT * 64];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[t] += o[t];
+      }
+      store(g, 16 * fm + r, fj * kWaveN + 4 * q, s);
+    }
+  }
+};
+
+// Move to the group's tile: rows from tm bm on, columns from tn bn on.
+FP8L_DEV void mx_group(MxArgs& g, const MxStrides& st, const GroupSpan& sp, int tm, int bm) {
+  g.b += sp.e * st.b;
+  g.sb += sp.e * st.sb;
+  if (g.bias) g.bias += sp.e * st.bias;
+  const int64_t row = sp.start + (int64_t)tm * bm;
+  mx_move(g, row, min<int64_t>(sp.end - row, bm), 0);
+}
+
+template <int MT>
+__global__ __launch_bounds__(512) void mx4_skinny_kernel(MxArgs g, int kw) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_mx[];
+  using S = MxSkinny<MT>;
+  const int tm = blockIdx.x / g.tiles_n, tn = blockIdx.x % g.tiles_n;
+  const int64_t row = (int64_t)tm * S::kBM;
+  mx_move(g, row, min<int64_t>(g.M - row, S::kBM), (int64_t)tn * (8 / kw) * S::kWaveN);
+  S::run(g, kw, smem_mx);
+}
+
+template <int MT>
+__global__ __launch_bounds__(512) void mx4_skinny_groups_kernel(MxArgs g, Groups gr, MxStrides st,
+                                                                int kw) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_mx[];
+  using S = MxSkinny<MT>;
+  int tm, tn;
+  const GroupSpan sp = rows_work(gr, S::kBM, g.tiles_n, tm, tn);
+  if (sp.e < 0) return;
+  mx_group(g, st, sp, tm, S::kBM);
+  mx_move(g, 0, g.M, (int64_t)tn * (8 / kw) * S::kWaveN);
+  S::run(g, kw, smem_mx);
+}
+
+}  // namespace fp8l

@@ -26,7 +26,7 @@
 // All other logits get 0; the bias has no gradient.
 #pragma once
 
-#include "fp8l_quantize.hpp"
+#include "fp8l_values.hpp"
 
 namespace fp8l {
 
@@ -285,13 +285,6 @@ struct RouteBwdArgs {
   void* dz;           // [T][E], z's type
 };
 
-template <int IN>
-FP8L_DEV void store1(void* p, int64_t i, float v) {
-  if constexpr (IN == kInF32) reinterpret_cast<float*>(p)[i] = v;
-  else if constexpr (IN == kInF16) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_f16(v);
-  else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
-}
-
 template <int IN, int L, int V>
 __global__ __launch_bounds__(kRThreads) void route_bwd_kernel(RouteBwdArgs a) {
   const RouteArgs& r = a.r;
@@ -519,7 +512,7 @@ struct CombineArgs {
   RowGrid grid;
 };
 
-// A piece of N values of a row: N = 8 with 16-byte (fp32: 32-byte) accesses, or 1.
+// A piece of N values of a row: N = 8 with 16-byte accesses, or 1.
 template <int IN, int N>
 FP8L_DEV void load_n(const void* p, int64_t i, float (&v)[N]) {
   if constexpr (N == 8) load8<IN>(p, i, v);
@@ -527,20 +520,8 @@ FP8L_DEV void load_n(const void* p, int64_t i, float (&v)[N]) {
 }
 template <int IN, int N>
 FP8L_DEV void store_n(void* p, int64_t i, const float (&v)[N]) {
-  if constexpr (N == 1) {
-    store1<IN>(p, i, v[0]);
-  } else if constexpr (IN == kInF32) {
-    float4* const q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = IN == kInF16 ? f32_to_f16(v[2 * j]) | (f32_to_f16(v[2 * j + 1]) << 16)
-                          : pk_bf16(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  if constexpr (N == 8) store8<IN>(p, i, v);
+  else store1<IN>(p, i, v[0]);
 }
 
 // out[t] = sum_i w[t, i] y[pos[t, i]], in slot order in 32 bits, rounded once.
