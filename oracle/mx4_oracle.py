@@ -39,7 +39,7 @@ def nearest(v):
 
 
 def exponent(amax) -> int:
-    """Biased exponent of a block's scale."""
+    """Biased exponent of the scale of a block with this amax (not finite: NaN)."""
     if not np.isfinite(amax):
         return 255
     if amax == 0:
@@ -54,16 +54,12 @@ def quantize(x):
     rows, K = x.shape
     B = -(-K // 32)
     x = np.pad(x, ((0, 0), (0, B * 32 - K))).reshape(rows, B, 32)
-    codes = np.zeros(x.shape, np.int64)
-    exps = np.zeros((rows, B), np.int64)
-    for r in range(rows):
-        for b in range(B):
-            v = x[r, b]
-            top = np.max(np.abs(v)) if np.isfinite(v).all() else np.inf
-            exps[r, b] = e = exponent(top)
-            if e != 255:
-                codes[r, b] = nearest(np.abs(v) / 2.0 ** (e - 127)) + 8 * np.signbit(v)
-    return codes, exps
+    finite = np.isfinite(x).all(2)
+    x = np.where(finite[..., None], x, 0.0)
+    exps = np.vectorize(exponent, otypes=[np.int64])(np.where(finite, np.abs(x).max(2, initial=0.0), np.inf))
+    scale = 2.0 ** (np.where(finite, exps, 127) - 127.0)[..., None]
+    codes = nearest(np.abs(x) / scale) + 8 * np.signbit(x)
+    return np.where(finite[..., None], codes, 0), exps
 
 
 def values(codes, exps):

@@ -4,7 +4,7 @@
 #include <type_traits>
 
 #include "fp8l_grouped_host.hpp"
-#include "fp8l_mx4.hpp"
+#include "fp8l_mx4_tile.hpp"
 
 namespace fp8l {
 namespace {
@@ -92,23 +92,58 @@ MxArgs mx_args(int64_t M, int64_t N, int64_t K, const void* x, int32_t x_dtype,
   return g;
 }
 
-// Rows of a tile by the number of rows (of a group on average).
-int skinny_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 4; }
-
-template <class F>
-void by_count(int mt, F&& f) {
-  if (mt == 1) f(std::integral_constant<int, 1>{});
-  else if (mt == 2) f(std::integral_constant<int, 2>{});
-  else if (mt == 3) f(std::integral_constant<int, 3>{});
-  else f(std::integral_constant<int, 4>{});
+template <int WGM>
+void launch_tile(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st) {
+  using T = MxTile<WGM>;
+  static std::atomic<bool> set_dense[64], set_groups[64];
+  g.tiles_n = (int32_t)((g.N + T::kBN - 1) / T::kBN);
+  if (gr) {
+    set_lds_limit((const void*)mx4_tile_groups_kernel<WGM>, T::kLds, set_groups);
+    const int64_t most = (most_units(gr->T, gr->E, T::kBM) * g.tiles_n + 7) & ~7LL;
+    hipLaunchKernelGGL((mx4_tile_groups_kernel<WGM>), dim3((unsigned)most), dim3(T::kThreads),
+                       T::kLds, st, g, *gr, s);
+  } else {
+    set_lds_limit((const void*)mx4_tile_kernel<WGM>, T::kLds, set_dense);
+    g.tiles_m = (int32_t)((g.M + T::kBM - 1) / T::kBM);
+    hipLaunchKernelGGL((mx4_tile_kernel<WGM>), dim3((unsigned)g.tiles_m * (unsigned)g.tiles_n),
+                       dim3(T::kThreads), T::kLds, st, g);
+  }
 }
 
-// Tile columns of a skinny launch and the waves that split K in it.
-int skinny_cols(MxArgs& g, int64_t units) {
+template <int MT>
+void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st) {
+  const int64_t units = gr ? most_units(gr->T, gr->E, 16 * MT) : (g.M + 16 * MT - 1) / (16 * MT);
   const int64_t cols = (g.N + 15) / 16;
   const int kw = skinny_kw(units * cols, g.ld);
+  const int lds = kw > 1 ? MxSkinny<MT>::kLds : 0;
   g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
-  return kw;
+  if (gr)
+    hipLaunchKernelGGL((mx4_skinny_groups_kernel<MT>),
+                       dim3((unsigned)((units * g.tiles_n + 7) & ~7LL)), dim3(512), lds, st, g, *gr,
+                       s, kw);
+  else
+    hipLaunchKernelGGL((mx4_skinny_kernel<MT>), dim3((unsigned)(units * g.tiles_n)), dim3(512), lds,
+                       st, g, kw);
+}
+
+// The kernel for `rows` rows per group on average.
+int mx_tile(int64_t rows, int64_t E, int64_t N) {
+  const int f = forced_tile();
+  if (f == kTile256x256w8 || f == kTile128x256 || (f >= kTileSkinny16 && f <= kTileSkinny64)) return f;
+  if (rows <= 64) return kTileSkinny16 + (int)((rows + 15) / 16) - 1;
+  const int64_t t256 = (rows + 255) / 256 * E * ((N + 255) / 256);
+  return t256 >= cu_count() / 2 ? kTile256x256w8 : kTile128x256;
+}
+
+void launch_product(MxArgs& g, int64_t rows, const Groups* gr, const MxStrides& s, hipStream_t st) {
+  switch (mx_tile(rows, gr ? gr->E : 1, g.N)) {
+    case kTileSkinny16: return launch_skinny<1>(g, gr, s, st);
+    case kTileSkinny32: return launch_skinny<2>(g, gr, s, st);
+    case kTileSkinny48: return launch_skinny<3>(g, gr, s, st);
+    case kTileSkinny64: return launch_skinny<4>(g, gr, s, st);
+    case kTile128x256: return launch_tile<1>(g, gr, s, st);
+    default: return launch_tile<2>(g, gr, s, st);
+  }
 }
 
 }  // namespace
@@ -171,13 +206,7 @@ int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x
   if (is_hp(x_dtype)) enqueue_mx_quantize(x, x_dtype, 1, M, K, x4_out, sx_out, nullptr, stream);
   if (M == 0 || N == 0) return hip_status();
   MxArgs g = mx_args(M, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
-  by_count(skinny_tiles(M), [&](auto mt) {
-    constexpr int MT = decltype(mt)::value;
-    const int64_t units = (M + 16 * MT - 1) / (16 * MT);
-    const int kw = skinny_cols(g, units);
-    hipLaunchKernelGGL((mx4_skinny_kernel<MT>), dim3((unsigned)(units * g.tiles_n)), dim3(512),
-                       kw > 1 ? MxSkinny<MT>::kLds : 0, stream, g, kw);
-  });
+  launch_product(g, M, nullptr, MxStrides{}, stream);
   return hip_status();
 }
 
@@ -198,14 +227,7 @@ int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const
   MxArgs g = mx_args(T, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
   const MxStrides s = {N * g.ld, N * g.steps, N};
   const Groups gr = {offsets, E, (int32_t)T};
-  by_count(skinny_tiles((T + E - 1) / E), [&](auto mt) {
-    constexpr int MT = decltype(mt)::value;
-    const int64_t units = most_units(T, E, 16 * MT);
-    const int kw = skinny_cols(g, units);
-    const int64_t most = (units * g.tiles_n + 7) & ~7LL;
-    hipLaunchKernelGGL((mx4_skinny_groups_kernel<MT>), dim3((unsigned)most), dim3(512),
-                       kw > 1 ? MxSkinny<MT>::kLds : 0, stream, g, gr, s, kw);
-  });
+  launch_product(g, (T + E - 1) / E, &gr, s, stream);
   return hip_status();
 }
 

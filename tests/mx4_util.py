@@ -2,6 +2,8 @@
 
 from __future__ import annotations
 
+from functools import lru_cache
+
 import numpy as np
 import torch
 
@@ -16,11 +18,16 @@ HALF = {"bf16": (2.0 ** -8, 2.0 ** -134), "fp16": (2.0 ** -11, 2.0 ** -25)}
 SUM_REL = 2.0 ** -10
 
 
-def matrix(rows, K, seed, spread=2.0):
-    """Codes, exponents and values of a matrix whose blocks' sizes differ."""
+@lru_cache(maxsize=None)
+def _matrix(rows, K, seed, spread=2.0):
+    """Codes and exponents of a matrix whose rows' sizes differ."""
     rng = np.random.default_rng(seed)
     v = rng.standard_normal((rows, K)) * 2.0 ** rng.uniform(-spread, spread, (rows, 1))
     return X.quantize(np.float32(v))
+
+
+def matrix(rows, K, seed, spread=2.0):
+    return tuple(a.copy() for a in _matrix(rows, K, seed, spread))
 
 
 def operand(codes, exps, K):

@@ -109,7 +109,7 @@ def test_stack_unaligned_and_empty():
         F.fp8_mx4_dequantize(e, torch.empty(shape, device=DEV))
 
 
-TILES = [None]
+TILES = ["skinny16", "skinny32", "skinny48", "skinny64", "128x256", "256x256w8", None]
 SIZES = [(1, 16, 32), (1, 1, 1), (3, 40, 96), (16, 64, 128), (17, 33, 160), (33, 77, 1003),
          (64, 130, 512), (100, 260, 288), (130, 17, 2048), (5, 300, 4100), (300, 520, 640)]
 

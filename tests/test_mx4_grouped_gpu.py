@@ -12,7 +12,7 @@ from tests.rows_util import GROUPS, offsets_dev, offsets_of, outside
 
 pytestmark = pytest.mark.gpu
 
-TILES = [None]
+TILES = ["skinny16", "skinny32", "skinny48", "skinny64", "128x256", "256x256w8", None]
 
 
 def _weights(E, N, K):
