@@ -11,7 +11,7 @@ namespace {
 constexpr int kMaxChunks = 512;
 int plan_chunk(int64_t slots) {
   int64_t c = (slots + kMaxChunks - 1) / kMaxChunks;
-  c = (c + kRThreads - 1) / kRThreads * kRThreads;
+  c = (c + kPlaceThreads - 1) / kPlaceThreads * kPlaceThreads;
   return (int)(c < 2048 ? 2048 : c);
 }
 int64_t plan_chunks(int64_t slots) {
@@ -65,7 +65,8 @@ void enqueue_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* 
                 plan_chunk(n), (int32_t)plan_chunks(n)};
   if (a.chunks > 1)
     hipLaunchKernelGGL(plan_count_kernel, dim3(a.chunks), dim3(kRThreads), 0, st, a);
-  hipLaunchKernelGGL(plan_place_kernel, dim3(a.chunks), dim3(kRThreads), 0, st, a);
+  hipLaunchKernelGGL(plan_place_kernel, dim3(a.chunks), dim3(kPlaceThreads),
+                     place_lds<kPlaceThreads>(E), st, a);
 }
 
 int check_plan(int64_t T, int32_t k, int32_t E, const int32_t* offsets, const int32_t* pos,
@@ -123,12 +124,17 @@ int fp8_route_fwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t d
   if (T > 0 && (!logits || !idx || !weights)) return FP8_ERR_NULL;
   if ((offsets || pos) && (st = check_plan(T, k, E, offsets, pos, ws))) return st;
   RouteArgs a = {logits, bias, idx, weights, (int32_t)T, E, k, score == FP8_ROUTE_SIGMOID,
-                 groups, groups_kept, group_top, renorm != 0, scale};
+                 groups, groups_kept, group_top, renorm != 0, scale, 0, 0};
   if (T > 0)
     by_type(dtype, [&](auto in) {
       by_row(E, k, [&](auto l, auto v) {
         constexpr int IN = decltype(in)::value, L = decltype(l)::value, V = decltype(v)::value;
         constexpr int per = kRThreads / L;
+        const int size = dtype == FP8_DT_F32 ? 4 : 2, n = E / groups;
+        a.vec = E % V == 0 && E * size % 16 == 0 && aligned16(logits) && aligned16(bias);
+        // whole groups in 2^j lanes, or no limit by groups
+        if (L == 16 && (groups == 1 || groups_kept == groups)) a.lanes = 16;
+        else if (L == 16 && n % V == 0 && (n / V & (n / V - 1)) == 0) a.lanes = n / V;
         hipLaunchKernelGGL((route_kernel<IN, L, V>), dim3((unsigned)((T + per - 1) / per)),
                            dim3(kRThreads), 0, stream, a);
       });

@@ -41,6 +41,8 @@ struct RouteArgs {
   float* w;           // [T][k]
   int32_t T, E, k, score, groups, kept, group_top, renorm;
   float scale;
+  int32_t vec;    // a lane's experts by wide loads
+  int32_t lanes;  // lanes of a group for the choice in 32 bits, 0: not that way
 };
 
 // ---------------------------------------------------------------- lanes
@@ -169,6 +171,64 @@ FP8L_DEV void keep_groups(const RouteArgs& a, S (&c)[V], const S (&g)[V], int sl
   wave_fence();
 }
 
+template <int N>
+FP8L_DEV uint32_t turn_lane(uint32_t v) {  // row_ror:N
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int N>
+FP8L_DEV int turn_lane(int v) { return (int)turn_lane<N>((uint32_t)v); }
+template <int N>
+FP8L_DEV float turn_lane(float v) { return __uint_as_float(turn_lane<N>(__float_as_uint(v))); }
+template <int N>
+FP8L_DEV double turn_lane(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint64_t lo = turn_lane<N>((uint32_t)u), hi = turn_lane<N>((uint32_t)(u >> 32));
+  return __longlong_as_double((long long)(lo | (hi << 32)));
+}
+// f(N tag) for N = 1 .. 15
+template <int N = 1, class F>
+FP8L_DEV void other_lanes(F&& f) {
+  if constexpr (N < 16) {
+    f(std::integral_constant<int, N>{});
+    other_lanes<N + 1>(f);
+  }
+}
+
+// c of the experts in groups that are not kept becomes -inf, for rows of 16
+// lanes and groups of 2^j lanes (RouteArgs::lanes): every lane ranks its group
+// among those of the other lanes.  g: what groups are scored by.  Whether the
+// group stays, and its score, for the caller's proof.
+template <int V, class S>
+FP8L_DEV bool keep_groups_lanes(const RouteArgs& a, S (&c)[V], const S (&g)[V], int sl, S& mark) {
+  S hi = -(S)INFINITY, lo = -(S)INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lo = max(lo, min(hi, g[v]));
+    hi = max(hi, g[v]);
+  }
+  lane_steps<16>([&](auto s) {
+    constexpr int STEP = decltype(s)::value;
+    if (STEP < a.lanes) {
+      const S oh = lane_step<STEP>(hi), ol = lane_step<STEP>(lo);
+      lo = max(min(hi, oh), max(lo, ol));
+      hi = max(hi, oh);
+    }
+  });
+  mark = a.group_top == 2 && lo > -(S)INFINITY ? hi + lo : hi;
+  const int grp = sl / a.lanes;
+  int ahead = 0;  // lanes of better groups
+  other_lanes([&](auto n) {
+    constexpr int N = decltype(n)::value;
+    const S o = turn_lane<N>(mark);
+    const int og = turn_lane<N>(grp);
+    ahead += o > mark || (o == mark && og < grp) ? 1 : 0;
+  });
+  const bool in = ahead < a.kept * a.lanes;
+#pragma unroll
+  for (int v = 0; v < V; ++v) c[v] = in ? c[v] : -(S)INFINITY;
+  return in;
+}
+
 // The scores p of a row in S; m: its largest logit.
 template <int L, int V, class S>
 FP8L_DEV void row_scores(const RouteArgs& a, const float (&z)[V], float m, S (&p)[V]) {
@@ -203,7 +263,11 @@ FP8L_DEV int choose(const RouteArgs& a, const float (&z)[V], const float (&b)[V]
     else g[v] = (S)z[v];
     c[v] = a.bias ? g[v] : (S)z[v];
   }
-  if (a.groups > 1 && a.kept < a.groups) keep_groups<L>(a, c, g, sl, row);
+  if (a.groups > 1 && a.kept < a.groups) {
+    S mark;
+    if (L == 16 && a.lanes) keep_groups_lanes<V, S>(a, c, g, sl, mark);
+    else keep_groups<L>(a, c, g, sl, row);
+  }
   int mine = -1;
   for (int i = 0; i < a.k; ++i) {
     int at;
@@ -243,36 +307,241 @@ FP8L_DEV float slot_weight(const RouteArgs& a, const float (&z)[V], float m, boo
   return q;
 }
 
-// One row per L lanes, V experts per lane: E <= L V, k <= L.
+// ---------------------------------------------------------------- choice in 32 bits
+
+// The choice of scores held in 64 bits, from scores in 32 bits and a proof
+// (16384 rows of 256 experts entirely in 64 bits: 105 us).
+//
+//   keys     every expert gets an upper bound u of its c (a score in 32 bits
+//            is off by less than 2^-17 of itself: an exponential's argument of
+//            up to 88 rounded to 2^-24, a few units for exp, reciprocal and
+//            sums), as an ordered integer below 2^31 whose lowest bits give way
+//            to the expert's index, lower ones larger.  All keys differ, so a
+//            round of the top-k is a maximum over the lanes, and the largest
+//            key below the last one is last + max(key - last) in unsigned
+//            numbers, without striking anything out.
+//   proof    each chosen expert's c is taken in 64 bits, one per lane.  All
+//            others have c <= the bound of the (k + 1)-th key: if every chosen
+//            c exceeds that, the set is right.  The order is then checked on
+//            the same values, and sorted by them where it is not.
+//   groups   scored in 32 bits; right if the least kept and the best dropped
+//            group are further apart than the scores' errors.
+//   else     the wave does its rows again in 64 bits.
+//
+// Logits of 16 bits without a bias have keys without loss: nothing to prove.
+// One row per 16 lanes, V experts per lane.
+
+// Key bits of the index.
+template <int V>
+constexpr int key_low() { return V == 1 ? 4 : V == 4 ? 6 : V == 8 ? 7 : 8; }
+
+// Order-preserving integer of a float that is no NaN.
+FP8L_DEV uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+FP8L_DEV float unordered(uint32_t o) {
+  return __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
+}
+
+// Value of the next lane of 16 (the last one's: its own).
+FP8L_DEV uint32_t next_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x101, 0xF, 0xF, false);  // row_shl:1
+}
+FP8L_DEV double next_lane(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint64_t lo = next_lane((uint32_t)u), hi = next_lane((uint32_t)(u >> 32));
+  return __longlong_as_double((long long)(lo | (hi << 32)));
+}
+
+// The same in 32 bits; false where that cannot tell which groups stay.  err:
+// the largest error of a group's score (< 0: none).
+template <int V>
+FP8L_DEV bool keep_groups32(const RouteArgs& a, float (&c)[V], const float (&g)[V], int sl,
+                            float err) {
+  float mark;
+  const bool in = keep_groups_lanes<V, float>(a, c, g, sl, mark);
+  if (err < 0.0f) return true;
+  const float least = -lanes_max<16>(in ? -mark : -INFINITY);
+  const float best = lanes_max<16>(in ? -INFINITY : mark);
+  return best == -INFINITY || least - best > 2.0f * err + 0x1p-21f * (fabsf(least) + fabsf(best));
+}
+
+// The chosen expert of slot i in lane i (-1: none) and its logit; sure: false
+// where the row has to be done in 64 bits.  m: the row's largest logit.
+template <int IN, int V>
+FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[V], int64_t t,
+                      float m, int sl, bool& sure, float& zi) {
+  constexpr int LOW = key_low<V>();
+  const bool grouped = a.groups > 1 && a.kept < a.groups;
+  const bool by_score = a.bias || (grouped && a.group_top == 2);
+  float c[V], g[V], sum = 1.0f, top = 0.0f;
+  if (by_score) {
+    if (a.score == kSigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) g[v] = __builtin_amdgcn_rcpf(1.0f + __expf(-z[v]));
+    } else {
+      sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum += g[v] = __expf(z[v] - m);
+      sum = lanes_sum<16>(sum);
+      const float r = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v) g[v] *= r;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool off = z[v] == -INFINITY;
+      const float p = g[v];
+      top = fmaxf(top, off ? 0.0f : p);
+      g[v] = off ? -INFINITY : p + b[v];
+      // the bound: the score's error, the addition's, and what underflows
+      c[v] = a.bias ? g[v] + (0x1p-16f * p + 0x1p-22f * fabsf(g[v]) + 0x1p-120f) : z[v];
+      if (g[v] == -INFINITY) c[v] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = g[v] = z[v];
+  }
+  sure = !grouped ||
+         keep_groups32<V>(a, c, g, sl, by_score ? 0x1p-16f * lanes_max<16>(top) + 0x1p-120f : -1.0f);
+  uint32_t key[V], last = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t low = (uint32_t)((1 << LOW) - 1 - (sl * V + v));
+    key[v] = c[v] == -INFINITY ? 0u : ((ordered(c[v]) >> (LOW + 1)) << LOW) | low;
+    last = max(last, key[v]);
+  }
+  lane_steps<16>([&](auto s) { last = max(last, lane_step<decltype(s)::value>(last)); });
+  uint32_t slot = 0;  // this lane's slot's key
+  for (int i = 0; i < a.k; ++i) {
+    if (sl == i) slot = last;
+    uint32_t r = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) r = max(r, key[v] - last);
+    lane_steps<16>([&](auto s) { r = max(r, lane_step<decltype(s)::value>(r)); });
+    last = (int32_t)r < 0 ? r + last : 0u;  // no key below the last one: none is left
+  }
+  const bool live = slot != 0;
+  int e = live ? (1 << LOW) - 1 - (int)(slot & ((1 << LOW) - 1)) : -1;
+  zi = live ? load1<IN>(a.z, t * a.E + e) : 0.0f;
+  if (IN != kInF32 && !a.bias) return e;
+
+  double ci = -INFINITY, p = 0.0;
+  if (live) {
+    if (a.bias) {
+      p = a.score == kSigmoid ? 1.0 / (1.0 + exp(-(double)zi))
+                              : exp((double)zi - (double)m) / (double)sum;
+      ci = p + (double)a.bias[e];
+    } else {
+      ci = zi;
+    }
+  }
+  const bool loose = a.bias && a.score == kSoftmax;  // p carries the 32-bit sum's error
+  const double slack = loose ? 0x1p-16 : 0.0;
+  // (last: the (k + 1)-th key)
+  const double bound =
+      last == 0 ? -INFINITY
+                : (double)unordered((((last >> LOW) + 1) << (LOW + 1)) - 1);
+  bool ok = !live || ci - slack * p > bound;
+  const double cn = next_lane(ci), pn = next_lane(p);
+  const int en = (int)next_lane((uint32_t)e);
+  const bool both = sl + 1 < a.k && live && en >= 0;
+  const bool wrong = both && (ci < cn || (ci == cn && e > en));
+  if (loose) ok = ok && !wrong && !(both && p != pn && fabs(ci - cn) <= slack * fabs(p - pn));
+  sure = sure && !lanes_any<16>(!ok);
+  if (!loose && __any(wrong)) {
+    // slots without an expert keep their places behind the others
+    const int id = live ? e : 1024 + sl;
+    int rank = 0;
+    other_lanes([&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const double o = turn_lane<N>(ci);
+      const int oid = turn_lane<N>(id);
+      rank += o > ci || (o == ci && oid < id) ? 1 : 0;
+    });
+    const int to = ((threadIdx.x & 48) + rank) * 4;
+    e = __builtin_amdgcn_ds_permute(to, e);
+    zi = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(zi)));
+  }
+  return e;
+}
+
+// V consecutive logits (or biases) from element i on.
+template <int IN, int V>
+FP8L_DEV void load_v(const void* p, int64_t i, float (&v)[V]) {
+  if constexpr (V >= 8) {
+#pragma unroll
+    for (int j = 0; j < V; j += 8) load8<IN>(p, i + j, v + j);
+  } else if constexpr (V == 4 && IN == kInF32) {
+    const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = load1<IN>(p, i + j);
+  }
+}
+
+// One row of L lanes, V experts per lane (E <= L V, k <= L): the slot of lane
+// sl: its expert, and its weight in w.
 template <int IN, int L, int V>
-__global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kRThreads / L * route_row_lds<L, V>()];
-  const int sl = threadIdx.x % L;
-  uint8_t* const row_lds = lds + threadIdx.x / L * route_row_lds<L, V>();
-  const int64_t t0 = (int64_t)blockIdx.x * (kRThreads / L) + threadIdx.x / L;
-  const bool there = t0 < a.T;
-  const int64_t t = there ? t0 : a.T - 1;
+FP8L_DEV int route_row(const RouteArgs& a, int64_t t, int sl, uint8_t* row_lds, float& w) {
   float z[V], b[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) z[v] = -INFINITY, b[v] = 0.0f;
+  if (a.vec) {
+    if (sl * V < a.E) {
+      load_v<IN>(a.z, t * a.E + sl * V, z);
+      if (a.bias) load_v<kInF32>(a.bias, sl * V, b);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = sl * V + v;
+      if (e < a.E) {
+        z[v] = load1<IN>(a.z, t * a.E + e);
+        if (a.bias) b[v] = a.bias[e];
+      }
+    }
+  }
   bool bad = false;
   float m = -INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = sl * V + v;
-    z[v] = e < a.E ? load1<IN>(a.z, t * a.E + e) : -INFINITY;
-    b[v] = a.bias && e < a.E ? a.bias[e] : 0.0f;
     bad = bad || z[v] != z[v] || b[v] != b[v] || (a.score == kSoftmax && z[v] == INFINITY);
     m = fmaxf(m, z[v]);
   }
   m = lanes_max<L>(m);
   bad = lanes_any<L>(bad);
-  int mine = choose<L, V, double>(a, z, b, m, sl, row_lds);
-  if (bad) mine = sl;
-  const bool live = sl < a.k && mine >= 0;
-  const float zi = live ? load1<IN>(a.z, t * a.E + mine) : 0.0f;
-  float w = a.scale * slot_weight<L>(a, z, m, live, zi);
+  int mine;
+  float zi = 0.0f;
+  bool sure = false;
+  if constexpr (L == 16) {
+    if (a.lanes) mine = choose32<IN, V>(a, z, b, t, m, sl, sure, zi);
+  }
+  if (__any(!sure && !bad)) {
+    const int again = choose<L, V, double>(a, z, b, m, sl, row_lds);
+    if (!sure) {
+      mine = again;
+      zi = sl < a.k && mine >= 0 ? load1<IN>(a.z, t * a.E + mine) : 0.0f;
+    }
+  }
+  const bool live = sl < a.k && !bad && mine >= 0;
+  w = a.scale * slot_weight<L>(a, z, m, live, zi);
   if (bad) w = __uint_as_float(0x7fc00000u);
-  if (there && sl < a.k) {
-    a.idx[t * a.k + sl] = mine;
+  return bad ? sl : mine;
+}
+
+template <int IN, int L, int V>
+__global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRThreads / L * route_row_lds<L, V>()];
+  const int sl = threadIdx.x % L;
+  const int64_t t = (int64_t)blockIdx.x * (kRThreads / L) + threadIdx.x / L;
+  float w;
+  const int e = route_row<IN, L, V>(a, t < a.T ? t : a.T - 1, sl,
+                                    lds + threadIdx.x / L * route_row_lds<L, V>(), w);
+  if (t < a.T && sl < a.k) {
+    a.idx[t * a.k + sl] = e;
     a.w[t * a.k + sl] = w;
   }
 }
@@ -360,7 +629,6 @@ struct PlanArgs {
 };
 
 FP8L_DEV int slot_expert(const PlanArgs& a, int j) {
-  if (j >= a.n) return a.E;
   const int e = a.idx[j];
   return e >= 0 && e < a.E ? e : a.E;
 }
@@ -373,7 +641,7 @@ __global__ __launch_bounds__(kRThreads) void plan_count_kernel(PlanArgs a) {
   for (int j = j0 + threadIdx.x; j < min(j0 + a.chunk, a.n); j += kRThreads)
     atomicAdd(&h[slot_expert(a, j)], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kRThreads) a.counts[blockIdx.x * a.E + e] = h[e];
+  for (int e = threadIdx.x; e < a.E; e += kRThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = h[e];
 }
 
 // Lanes of the wave with the same key (< 2^bits).
@@ -386,77 +654,106 @@ FP8L_DEV uint64_t same_key(int key, int bits) {
   return peers;
 }
 
-__global__ __launch_bounds__(kRThreads) void plan_place_kernel(PlanArgs a) {
-  constexpr int NW = kRThreads / 64, PER = kRouteMaxE / kRThreads;
-  __shared__ int32_t next[NW][kRouteMaxE + 1];  // each wave's next place of an expert
-  __shared__ int32_t wave_total[NW];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  for (int e = tid; e < NW * (kRouteMaxE + 1); e += kRThreads) (&next[0][0])[e] = 0;
+// Places the slots of one chunk, NT threads; expert(j): slot j's expert, a.E
+// for none.  lds: NW (E + 1) integers, then 3 NT more.
+template <int NT>
+constexpr int place_lds(int E) { return 4 * (NT / 64 * (E + 1) + 3 * NT); }
+
+template <int NT, class F>
+FP8L_DEV void place_chunk(const PlanArgs& a, int block, int32_t* lds, F&& expert) {
+  constexpr int NW = NT / 64, COLS = NT < 256 ? NT : 256, SPLIT = NT / COLS;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, W = a.E + 1;
+  int32_t* const next = lds;  // [wave][expert]: the wave's slots, then its next place
+  int32_t* const before_part = lds + NW * W;  // [SPLIT][COLS]
+  int32_t* const total_part = before_part + NT;
+  int32_t* const wave_total = total_part + NT;
+  for (int i = tid; i < NW * W; i += NT) next[i] = 0;
   __syncthreads();
-  // wave w's slots: the w-th quarter of the chunk
+  // wave w's slots: the w-th part of the chunk
   const int per = a.chunk / NW;
-  const int j0 = blockIdx.x * a.chunk + wave * per;
-  for (int j = j0 + lane; j < j0 + per; j += 64) atomicAdd(&next[wave][slot_expert(a, j)], 1);
+  const int j0 = block * a.chunk + wave * per, j1 = min(j0 + per, a.n);
+  int32_t* const mine = next + wave * W;
+  for (int j = j0 + lane; j < j1; j += 64) atomicAdd(&mine[expert(j)], 1);
   __syncthreads();
-  // thread's experts: PER consecutive ones
-  int before[PER], total[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid * PER + i;
-    before[i] = total[i] = 0;
+  // first places of 256 experts at a time; SPLIT threads add up an expert's chunks
+  int carry = 0;
+  for (int e0 = 0; e0 < a.E; e0 += COLS) {
+    const int col = tid % COLS, part = tid / COLS, e = e0 + col;
+    int before = 0, total = 0;
     if (e < a.E) {
       if (a.chunks == 1) {
-        for (int w = 0; w < NW; ++w) total[i] += next[w][e];
+        for (int w = part; w < NW; w += SPLIT) total += next[w * W + e];
       } else {
-        for (int c = 0; c < a.chunks; ++c) {
-          const int n = a.counts[c * a.E + e];
-          if (c < (int)blockIdx.x) before[i] += n;
-          total[i] += n;
+        constexpr int U = 16;  // loads in flight
+        for (int c0 = part; c0 < a.chunks; c0 += U * SPLIT) {
+          int n[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * SPLIT;
+            n[u] = a.counts[min(c, a.chunks - 1) * a.E + e];
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * SPLIT;
+            if (c < a.chunks) total += n[u];
+            if (c < block) before += n[u];
+          }
         }
       }
     }
-    sum += total[i];
-  }
-  // exclusive prefix over the threads
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 63) wave_total[wave] = incl;
-  __syncthreads();
-  int first = incl - sum;
-  for (int w = 0; w < wave; ++w) first += wave_total[w];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid * PER + i;
-    if (e < a.E) {
-      if (blockIdx.x == 0) {
-        a.offsets[e] = first;
-        if (e == a.E - 1) a.offsets[a.E] = first + total[i];
+    before_part[tid] = before;
+    total_part[tid] = total;
+    __syncthreads();
+    before = total = 0;
+    if (tid < COLS)
+      for (int s = 0; s < SPLIT; ++s) {
+        before += before_part[s * COLS + tid];
+        total += total_part[s * COLS + tid];
       }
-      int at = first + before[i];
+    int incl = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    int first = carry + incl - total;
+    for (int w = 0; w < COLS / 64; ++w) {
+      if (w < wave) first += wave_total[w];
+      carry += wave_total[w];
+    }
+    if (tid < COLS && e < a.E) {
+      if (block == 0) {
+        a.offsets[e] = first;
+        if (e == a.E - 1) a.offsets[a.E] = first + total;
+      }
+      int at = first + before;
       for (int w = 0; w < NW; ++w) {
-        const int n = next[w][e];
-        next[w][e] = at;
+        const int n = next[w * W + e];
+        next[w * W + e] = at;
         at += n;
       }
     }
-    first += total[i];
+    __syncthreads();
   }
-  __syncthreads();
   const int bits = 32 - __builtin_clz(a.E);
-  for (int j = j0 + lane; j - lane < j0 + per; j += 64) {
-    const int e = slot_expert(a, j);
+  for (int j = j0 + lane; j - lane < j1; j += 64) {
+    const int e = j < j1 ? expert(j) : a.E;
     const uint64_t peers = same_key(e, bits);
     const int rank = __popcll(peers & ((1ull << lane) - 1));
-    const int at = next[wave][e] + rank;
+    const int at = mine[e] + rank;
     wave_fence();
-    if (rank == 0) next[wave][e] += __popcll(peers);
+    if (rank == 0) mine[e] += __popcll(peers);
     wave_fence();
-    if (j < a.n) a.pos[j] = e < a.E ? at : -1;
+    if (j < j1) a.pos[j] = e < a.E ? at : -1;
   }
+}
+
+constexpr int kPlaceThreads = 512;
+__global__ __launch_bounds__(kPlaceThreads) void plan_place_kernel(PlanArgs a) {
+  extern __shared__ __attribute__((aligned(16))) int32_t place_mem[];
+  place_chunk<kPlaceThreads>(a, blockIdx.x, place_mem, [&](int j) { return slot_expert(a, j); });
 }
 
 // ---------------------------------------------------------------- rows
