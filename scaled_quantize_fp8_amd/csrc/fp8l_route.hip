@@ -125,6 +125,7 @@ int fp8_route_fwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t d
   if ((offsets || pos) && (st = check_plan(T, k, E, offsets, pos, ws))) return st;
   RouteArgs a = {logits, bias, idx, weights, (int32_t)T, E, k, score == FP8_ROUTE_SIGMOID,
                  groups, groups_kept, group_top, renorm != 0, scale, 0, 0};
+  bool placed = false;
   if (T > 0)
     by_type(dtype, [&](auto in) {
       by_row(E, k, [&](auto l, auto v) {
@@ -135,11 +136,23 @@ int fp8_route_fwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t d
         // whole groups in 2^j lanes, or no limit by groups
         if (L == 16 && (groups == 1 || groups_kept == groups)) a.lanes = 16;
         else if (L == 16 && n % V == 0 && (n / V & (n / V - 1)) == 0) a.lanes = n / V;
+        if constexpr (L == 16) {
+          if (offsets && T <= kRoutePlaceRows) {
+            const PlanArgs p = {idx, offsets, pos, nullptr, (int32_t)(T * k), E, kPlaceThreads, 1};
+            static std::atomic<bool> lds_set[64];
+            set_lds_limit((const void*)route_place_kernel<IN, V>, route_place_lds<V>(256, true),
+                          lds_set);
+            hipLaunchKernelGGL((route_place_kernel<IN, V>), dim3(1), dim3(kPlaceThreads),
+                               route_place_lds<V>(E, !a.lanes), stream, a, p);
+            placed = true;
+            return;
+          }
+        }
         hipLaunchKernelGGL((route_kernel<IN, L, V>), dim3((unsigned)((T + per - 1) / per)),
                            dim3(kRThreads), 0, stream, a);
       });
     });
-  if (offsets) enqueue_plan(idx, T, k, E, offsets, pos, ws, stream);
+  if (offsets && !placed) enqueue_plan(idx, T, k, E, offsets, pos, ws, stream);
   return hip_status();
 }
 

@@ -657,7 +657,9 @@ FP8L_DEV uint64_t same_key(int key, int bits) {
 // Places the slots of one chunk, NT threads; expert(j): slot j's expert, a.E
 // for none.  lds: NW (E + 1) integers, then 3 NT more.
 template <int NT>
-constexpr int place_lds(int E) { return 4 * (NT / 64 * (E + 1) + 3 * NT); }
+__host__ __device__ constexpr int place_lds(int E) {
+  return (4 * (NT / 64 * (E + 1) + 3 * NT) + 15) & ~15;
+}
 
 template <int NT, class F>
 FP8L_DEV void place_chunk(const PlanArgs& a, int block, int32_t* lds, F&& expert) {
@@ -754,6 +756,33 @@ constexpr int kPlaceThreads = 512;
 __global__ __launch_bounds__(kPlaceThreads) void plan_place_kernel(PlanArgs a) {
   extern __shared__ __attribute__((aligned(16))) int32_t place_mem[];
   place_chunk<kPlaceThreads>(a, blockIdx.x, place_mem, [&](int j) { return slot_expert(a, j); });
+}
+
+// Few tokens: choice and places by one block, in one launch.
+template <int IN, int V>
+__global__ __launch_bounds__(kPlaceThreads) void route_place_kernel(RouteArgs a, PlanArgs p) {
+  extern __shared__ __attribute__((aligned(16))) int32_t place_mem[];
+  int32_t* const slots = place_mem;  // [T][k]
+  int32_t* const place = slots + kPlaceThreads;
+  uint8_t* const rows = reinterpret_cast<uint8_t*>(place) + place_lds<kPlaceThreads>(p.E);
+  const int sl = threadIdx.x % 16, t = threadIdx.x / 16;
+  float w;
+  // (lds of the rows only where groups need it)
+  const int e = route_row<IN, 16, V>(a, min(t, a.T - 1), sl,
+                                     rows + (a.lanes ? 0 : t * route_row_lds<16, V>()), w);
+  if (t < a.T && sl < a.k) {
+    a.idx[t * a.k + sl] = e;
+    a.w[t * a.k + sl] = w;
+    slots[t * a.k + sl] = e < 0 ? p.E : e;
+  }
+  __syncthreads();
+  place_chunk<kPlaceThreads>(p, 0, place, [&](int j) { return slots[j]; });
+}
+constexpr int kRoutePlaceRows = kPlaceThreads / 16;
+template <int V>
+constexpr int route_place_lds(int E, bool rows) {
+  return 4 * kPlaceThreads + place_lds<kPlaceThreads>(E) +
+         (rows ? kRoutePlaceRows * route_row_lds<16, V>() : 0);
 }
 
 // ---------------------------------------------------------------- rows
