@@ -110,11 +110,23 @@ void launch_tile(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st
   }
 }
 
+// Waves that split K in a skinny launch of `waves` tile columns, doubled
+// while a wave has over 8 pieces (16 experts of 4096 -> 11008, one row each:
+// 64.9 us unsplit, 60.7 by two, 65.6 by four), or the chip has room for more
+// waves and each keeps its kU pieces in flight (one row, 11008 -> 4096: 50.8 us
+// unsplit, 10.5 by four, 8.2 by eight).
+int mx_split(int64_t waves, int64_t steps, int kU) {
+  const int64_t pieces = (steps + 1) / 2;
+  int kw = 1;
+  while (kw < 8 && (pieces > 8 * kw || (waves * kw < 8192 && pieces >= 2 * kU * kw))) kw *= 2;
+  return kw;
+}
+
 template <int MT>
 void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st) {
   const int64_t units = gr ? most_units(gr->T, gr->E, 16 * MT) : (g.M + 16 * MT - 1) / (16 * MT);
   const int64_t cols = (g.N + 15) / 16;
-  const int kw = skinny_kw(units * cols, g.ld);
+  const int kw = mx_split(units * cols, g.steps, MxSkinny<MT>::kU);
   const int lds = kw > 1 ? MxSkinny<MT>::kLds : 0;
   g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
   if (gr)
@@ -124,6 +136,36 @@ void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t 
   else
     hipLaunchKernelGGL((mx4_skinny_kernel<MT>), dim3((unsigned)(units * g.tiles_n)), dim3(512), lds,
                        st, g, kw);
+}
+
+// Whether a call's blocks quantize its X themselves (MxFused).  Every 16
+// columns' block does all of it again, about 1 us for 8192 values, where the
+// launch that it saves takes 2 to 3 (bf16, us fused / in two launches: one row
+// of 4096 -> 11008 8.2 / 10.2, of 11008 -> 4096 9.5 / 11.6; four rows of 1536 ->
+// 6912 5.7 / 8.1, of 4096 -> 11008 10.9 / 10.7, of 11008 -> 4096 13.9 / 11.6).
+// Groups: two rows per expert on average (any unit may have 16, whose codes
+// must leave room for two blocks per CU; 24 rows, 64 experts of 1536 -> 6912
+// 21.5 / 26.8; 16 rows, 16 of 4096 -> 11008 60.1 / 64.9).  groups 0: dense.
+bool fuse_x(const void* x, int32_t dt, int64_t rows, int64_t groups, int64_t K) {
+  if (!is_hp(dt) || K == 0 || K % 8 != 0 || !aligned16(x) || forced_tile() != kTileAuto) return false;
+  if (groups == 0) return rows == 1 ? K <= 16384 : rows <= 16 && rows * K <= 12288;
+  return rows <= 2 * groups && K <= 4096;
+}
+
+template <int IN>
+void launch_fused(MxArgs& g, const MxFusedX& fx, const Groups* gr, const MxStrides& s,
+                  hipStream_t st) {
+  const int64_t units = gr ? most_units(gr->T, gr->E, 16) : 1, cols = (g.N + 15) / 16;
+  const int kw = mx_split(units * cols, g.steps, MxSkinny<1>::kU);
+  const int lds = MxFused<IN>::lds(gr ? 16 : (int)g.M, g.ld, g.steps);
+  g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
+  if (gr)
+    hipLaunchKernelGGL((mx4_fused_groups_kernel<IN>),
+                       dim3((unsigned)((units * g.tiles_n + 7) & ~7LL)), dim3(512), lds, st, g, fx,
+                       *gr, s, kw);
+  else
+    hipLaunchKernelGGL((mx4_fused_kernel<IN>), dim3((unsigned)g.tiles_n), dim3(512), lds, st, g, fx,
+                       kw);
 }
 
 // The kernel for `rows` rows per group on average.
@@ -203,9 +245,16 @@ int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x
   if (!mul_ok(M, N) || !grid_fits(((M + 63) / 64) * ((N + 15) / 16), 512)) return FP8_ERR_SHAPE;
   if ((st = check_linear(M, N, K, x, x_dtype, x_scales, w, w_scales, out_dtype, y, x4_out, sx_out)))
     return st;
+  MxArgs g = mx_args(M, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
+  if (M > 0 && N > 0 && fuse_x(x, x_dtype, M, 0, K)) {
+    by_type(x_dtype, [&](auto in) {
+      launch_fused<decltype(in)::value>(g, MxFusedX{x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)}, nullptr, MxStrides{},
+                                        stream);
+    });
+    return hip_status();
+  }
   if (is_hp(x_dtype)) enqueue_mx_quantize(x, x_dtype, 1, M, K, x4_out, sx_out, nullptr, stream);
   if (M == 0 || N == 0) return hip_status();
-  MxArgs g = mx_args(M, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
   launch_product(g, M, nullptr, MxStrides{}, stream);
   return hip_status();
 }
@@ -221,12 +270,18 @@ int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const
   if (!offsets) return FP8_ERR_NULL;
   if ((st = check_linear(T, N, K, x, x_dtype, x_scales, w, w_scales, out_dtype, y, x4_out, sx_out)))
     return st;
-  if (is_hp(x_dtype))
-    enqueue_mx_quantize(x, x_dtype, 1, T, K, x4_out, sx_out, offsets + E, stream);
-  if (T == 0 || N == 0) return hip_status();
   MxArgs g = mx_args(T, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
   const MxStrides s = {N * g.ld, N * g.steps, N};
   const Groups gr = {offsets, E, (int32_t)T};
+  if (T > 0 && N > 0 && fuse_x(x, x_dtype, T, E, K)) {
+    by_type(x_dtype, [&](auto in) {
+      launch_fused<decltype(in)::value>(g, MxFusedX{x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)}, &gr, s, stream);
+    });
+    return hip_status();
+  }
+  if (is_hp(x_dtype))
+    enqueue_mx_quantize(x, x_dtype, 1, T, K, x4_out, sx_out, offsets + E, stream);
+  if (T == 0 || N == 0) return hip_status();
   launch_product(g, (T + E - 1) / E, &gr, s, stream);
   return hip_status();
 }

@@ -59,8 +59,27 @@ FP8L_DEV uint32_t mx_codes8(const float v[8], float inv) {
   return w;
 }
 
-// 16 lanes hold a step of 128 values, 8 each: four lanes a block, whose amax
-// they share by two DPP steps, then the four blocks' exponents meet in a word.
+// 16 lanes hold a step of 128 values, lane sl of them values 8 sl and on: four
+// lanes a block, whose amax they share by two DPP steps; then the four blocks'
+// exponents meet in a word.  inside: the lane's block is one of the row's.
+struct MxEight {
+  uint32_t codes, word;
+};
+FP8L_DEV MxEight mx_eight(const float v[8], bool inside, int sl) {
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = max(mx, absbits(v[i]));
+  mx = max(mx, (uint32_t)__builtin_amdgcn_mov_dpp((int)mx, 0xB1, 0xF, 0xF, false));
+  mx = max(mx, (uint32_t)__builtin_amdgcn_mov_dpp((int)mx, 0x4E, 0xF, 0xF, false));
+  const uint32_t e = inside ? mx_scale(mx) : 0u;
+  MxEight r;
+  r.word = e << (8 * (sl >> 2));
+  r.word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)r.word, 0x141, 0xF, 0xF, false);
+  r.word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)r.word, 0x140, 0xF, 0xF, false);
+  r.codes = e == 255u ? 0u : mx_codes8(v, mx_inverse(e));
+  return r;
+}
+
 // A block of 256 threads walks its tile of rows along K.
 template <int IN>
 __global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a) {
@@ -88,21 +107,13 @@ __global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a)
             if (k + i < a.K) v[i] = load1<IN>(a.x, at + i);
         }
       }
-      uint32_t mx = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mx = max(mx, absbits(v[i]));
-      mx = max(mx, (uint32_t)__builtin_amdgcn_mov_dpp((int)mx, 0xB1, 0xF, 0xF, false));
-      mx = max(mx, (uint32_t)__builtin_amdgcn_mov_dpp((int)mx, 0x4E, 0xF, 0xF, false));
       const bool inside = 4 * s + (sl >> 2) < a.blocks;
-      const uint32_t e = inside ? mx_scale(mx) : 0u;
-      uint32_t word = e << (8 * (sl >> 2));
-      word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)word, 0x141, 0xF, 0xF, false);
-      word |= (uint32_t)__builtin_amdgcn_mov_dpp((int)word, 0x140, 0xF, 0xF, false);
+      const MxEight e = mx_eight(v, inside, sl);
       if (r < rows) {
         if (inside)
           *reinterpret_cast<uint32_t*>(a.codes + (mat * a.rows + r) * row_bytes + s * 64 + 4 * sl) =
-              e == 255u ? 0u : mx_codes8(v, mx_inverse(e));
-        if (sl == 0) a.scales[(mat * a.steps + s) * a.rows + r] = word;
+              e.codes;
+        if (sl == 0) a.scales[(mat * a.steps + s) * a.rows + r] = e.word;
       }
     }
   }
@@ -207,7 +218,10 @@ FP8L_DEV uint2 mx_pack4(const MxArgs& g, const float v[4]) {
 template <int MT>
 struct MxSkinny {
   static constexpr int kBM = 16 * MT, kWaveN = 16, kThreads = 512, kLds = 8 * MT * 1024;
-  static constexpr int kU = MT == 1 ? 4 : (MT == 2 ? 3 : 2);  // pieces in flight
+  // Pieces in flight per wave.  More of them cost the registers of more waves:
+  // one row of 4096 -> 11008 with 1 / 2 / 4 pieces: 7.9 / 7.8 / 8.1 us; 33 rows
+  // 13.0 / 13.6 / 15.8; 64 rows of 11008 -> 4096 16.4 / 17.6 / 20.7.
+  static constexpr int kU = MT == 1 ? 2 : 1;
 
   FP8L_DEV static v8i load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
     const v4i a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
@@ -235,50 +249,11 @@ struct MxSkinny {
     }
   }
 
-  // g: moved to the tile's rows (at most kBM) and the block's first column.
-  FP8L_DEV static void run(const MxArgs& g, int KW, uint8_t* smem) {
+  // The sums of all K: of the KW waves of a column in wave order.
+  FP8L_DEV static void finish(const MxArgs& g, const v4f (&acc)[MT], int KW, uint8_t* smem) {
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
-    const int j0 = jw * kWaveN;
-    const int cols = (int)min<int64_t>(g.N, JW * kWaveN);  // rows of W in reach
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.M * g.ld));
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(g.b, (uint32_t)(cols * g.ld));
-    // scale words of rows past the end are those of other rows (or zeros past
-    // the last step): they meet zero codes or rows that are not stored
-    const __amdgpu_buffer_rsrc_t rsa =
-        make_rsrc(g.sa, (uint32_t)(((int64_t)(g.steps - 1) * g.sa_step + g.M) * 4));
-    const __amdgpu_buffer_rsrc_t rsb =
-        make_rsrc(g.sb, (uint32_t)(((int64_t)(g.steps - 1) * g.sb_step + cols) * 4));
-    const uint32_t ld = (uint32_t)g.ld;
-    v4f acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t pieces = ((uint32_t)g.steps + 1) / 2;
-    for (uint32_t p = kw; p < pieces; p += KW * kU) {
-      v8i fb[2 * kU], fa[2 * kU][MT];
-      uint32_t eb[2 * kU], ea[2 * kU][MT];
-#pragma unroll
-      for (int u = 0; u < 2 * kU; ++u) {
-        const uint32_t s = 2 * (p + (u >> 1) * KW) + (u & 1);
-        const uint32_t k = s * 64 + 16 * q;
-        const bool in = k < ld;  // blocks and steps past the last: zeros
-        fb[u] = load16(rb, in ? (uint32_t)(j0 + r) * ld + k : 0x80000000u);
-        eb[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-            rsb, in ? (s * (uint32_t)g.sb_step + j0 + r) * 4 : 0x80000000u, 0, 0);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          fa[u][m] = load16(ra, in ? (uint32_t)(16 * m + r) * ld + k : 0x80000000u);
-          ea[u][m] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-              rsa, in ? (s * (uint32_t)g.sa_step + 16 * m + r) * 4 : 0x80000000u, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2 * kU; ++u)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          acc[m] = mma(fb[u], fa[u][m], acc[m], eb[u] >> (8 * q), ea[u][m] >> (8 * q));
-    }
+    const int j0 = wave / KW * kWaveN, JW = 8 / KW;
     if (KW == 1) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) store(g, 16 * m + r, j0 + 4 * q, acc[m]);
@@ -300,6 +275,155 @@ struct MxSkinny {
       }
       store(g, 16 * fm + r, fj * kWaveN + 4 * q, s);
     }
+  }
+
+  // A piece of W for the wave's 16 columns: two steps' codes and scale words.
+  struct Piece {
+    v8i b[2];
+    uint32_t e[2];
+  };
+  struct W {
+    __amdgpu_buffer_rsrc_t codes, scales;
+    uint32_t row, word;  // this lane's row: bytes of codes, words of scales
+    FP8L_DEV W(const MxArgs& g, int j0, int JW) {
+      const int cols = (int)min<int64_t>(g.N, JW * kWaveN);  // rows of W in reach
+      const int r = threadIdx.x & 15;
+      codes = make_rsrc(g.b, (uint32_t)(cols * g.ld));
+      // words of rows past the end are those of other rows, or zeros past the
+      // last step: they meet zero codes or columns that are not stored
+      scales = make_rsrc(g.sb, (uint32_t)(((int64_t)(g.steps - 1) * g.sb_step + cols) * 4));
+      row = (uint32_t)((j0 + r) * g.ld);
+      word = (uint32_t)(j0 + r);
+    }
+    // pieces p, p + KW, ..
+    FP8L_DEV void load(const MxArgs& g, uint32_t p, int KW, Piece (&out)[kU]) const {
+      const uint32_t q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u) {
+        const uint32_t s = 2 * (p + (u >> 1) * KW) + (u & 1), k = s * 64 + 16 * q;
+        const bool in = k < (uint32_t)g.ld;  // blocks and steps past the last: zeros
+        out[u >> 1].b[u & 1] = load16(codes, in ? row + k : 0x80000000u);
+        out[u >> 1].e[u & 1] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+            scales, in ? (s * (uint32_t)g.sb_step + word) * 4 : 0x80000000u, 0, 0);
+      }
+    }
+  };
+
+  // g: moved to the tile's rows (at most kBM) and the block's first column.
+  FP8L_DEV static void run(const MxArgs& g, int KW, uint8_t* smem) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
+    const W w(g, jw * kWaveN, JW);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.M * g.ld));
+    const __amdgpu_buffer_rsrc_t rsa =
+        make_rsrc(g.sa, (uint32_t)(((int64_t)(g.steps - 1) * g.sa_step + g.M) * 4));
+    const uint32_t ld = (uint32_t)g.ld;
+    v4f acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t pieces = ((uint32_t)g.steps + 1) / 2;
+    for (uint32_t p = kw; p < pieces; p += KW * kU) {
+      Piece piece[kU];
+      w.load(g, p, KW, piece);
+      v8i fa[2 * kU][MT];
+      uint32_t ea[2 * kU][MT];
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u) {
+        const uint32_t s = 2 * (p + (u >> 1) * KW) + (u & 1), k = s * 64 + 16 * q;
+        const bool in = k < ld;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          fa[u][m] = load16(ra, in ? (uint32_t)(16 * m + r) * ld + k : 0x80000000u);
+          ea[u][m] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+              rsa, in ? (s * (uint32_t)g.sa_step + 16 * m + r) * 4 : 0x80000000u, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m] = mma(piece[u >> 1].b[u & 1], fa[u][m], acc[m], piece[u >> 1].e[u & 1] >> (8 * q),
+                       ea[u][m] >> (8 * q));
+    }
+    finish(g, acc, KW, smem);
+  }
+};
+
+// The skinny kernel for a high-precision X of so few rows that every block
+// quantizes them itself, into LDS, while its first pieces of W are on the way:
+// one launch instead of two.  The block of the first tile column writes codes
+// and scales out.  (Quantizing in the registers of the wave that multiplies
+// needs no LDS, but does 16 rows' work for one row: 16.8 us against 13.0 of two
+// launches for one token, 4096 -> 11008.)
+struct MxFusedX {
+  const void* x;     // [M][K]
+  int64_t K;
+  uint8_t* codes;    // [M][ld]
+  uint32_t* scales;  // words [steps][sa_step]
+};
+
+template <int IN>
+struct MxFused {
+  using S = MxSkinny<1>;
+  static constexpr int kU = S::kU, kSize = IN == kInF32 ? 4 : 2;
+  // LDS: partial sums, scale words [steps][rows], codes [rows][ld]
+  static int lds(int rows, int64_t ld, int64_t steps) {
+    return S::kLds + (int)(((steps * rows * 4 + 15) & ~15LL) + rows * ld);
+  }
+
+  // g, fx: moved to the tile's rows (at most 16) and the block's first column.
+  FP8L_DEV static void run(const MxArgs& g, const MxFusedX& fx, bool write, int KW, uint8_t* smem) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
+    const int j0 = jw * S::kWaveN, rows = (int)g.M;
+    const typename S::W w(g, j0, JW);
+    typename S::Piece piece[kU];
+    w.load(g, kw, KW, piece);
+    uint32_t* const xe = reinterpret_cast<uint32_t*>(smem + S::kLds);
+    uint8_t* const xc = smem + S::kLds + ((g.steps * rows * 4 + 15) & ~15);
+    const uint32_t ld = (uint32_t)g.ld, K = (uint32_t)fx.K;
+    // 16 lanes a step of 128 values, as in the quantize kernel
+    const int sl = threadIdx.x & 15;
+    for (int i = threadIdx.x >> 4; i < rows * g.steps; i += 32) {
+      const int row = i / g.steps, s = i - row * g.steps;
+      const uint32_t k = 128 * s + 8 * sl;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      if (k < K) load8<IN>(fx.x, (int64_t)row * K + k, v);
+      const MxEight e = mx_eight(v, k < 2 * ld, sl);
+      if (k < 2 * ld) {
+        *reinterpret_cast<uint32_t*>(xc + row * ld + 64 * s + 4 * sl) = e.codes;
+        if (write) *reinterpret_cast<uint32_t*>(fx.codes + (int64_t)row * ld + 64 * s + 4 * sl) = e.codes;
+      }
+      if (sl == 0) {
+        xe[s * rows + row] = e.word;
+        if (write) fx.scales[(int64_t)s * g.sa_step + row] = e.word;
+      }
+    }
+    lds_barrier();
+    // rows past the last one take its values: their sums are not stored
+    const int rr = min(r, rows - 1);
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t pieces = ((uint32_t)g.steps + 1) / 2;
+    for (uint32_t p = kw; p < pieces; p += KW * kU) {
+      if (p != (uint32_t)kw) w.load(g, p, KW, piece);
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u) {
+        const int s = 2 * (p + (u >> 1) * KW) + (u & 1);
+        if (s >= g.steps) continue;
+        const uint32_t k = 64 * s + 16 * q;
+        const v4i a = *reinterpret_cast<const v4i*>(xc + rr * ld + (k < ld ? k : 0));
+        const uint32_t ea = xe[s * rows + rr];
+        const v8i fa = {a.x, a.y, a.z, a.w, 0, 0, 0, 0};
+        acc = S::mma(piece[u >> 1].b[u & 1], fa, acc, piece[u >> 1].e[u & 1] >> (8 * q),
+                     ea >> (8 * q));
+      }
+    }
+    const v4f sums[1] = {acc};
+    S::finish(g, sums, KW, smem);
   }
 };
 
@@ -333,6 +457,29 @@ __global__ __launch_bounds__(512) void mx4_skinny_groups_kernel(MxArgs g, Groups
   mx_group(g, st, sp, tm, S::kBM);
   mx_move(g, 0, g.M, (int64_t)tn * (8 / kw) * S::kWaveN);
   S::run(g, kw, smem_mx);
+}
+
+template <int IN>
+__global__ __launch_bounds__(512, 4) void mx4_fused_kernel(MxArgs g, MxFusedX fx, int kw) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_mx[];
+  mx_move(g, 0, g.M, (int64_t)blockIdx.x * (8 / kw) * 16);
+  MxFused<IN>::run(g, fx, blockIdx.x == 0, kw, smem_mx);
+}
+
+template <int IN>
+__global__ __launch_bounds__(512, 4) void mx4_fused_groups_kernel(MxArgs g, MxFusedX fx, Groups gr,
+                                                               MxStrides st, int kw) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_mx[];
+  int tm, tn;
+  const GroupSpan sp = rows_work(gr, 16, g.tiles_n, tm, tn);
+  if (sp.e < 0) return;
+  mx_group(g, st, sp, tm, 16);
+  const int64_t row = sp.start + 16 * (int64_t)tm;
+  fx.x = reinterpret_cast<const uint8_t*>(fx.x) + row * fx.K * MxFused<IN>::kSize;
+  fx.codes += row * g.ld;
+  fx.scales += row;
+  mx_move(g, 0, g.M, (int64_t)tn * (8 / kw) * 16);
+  MxFused<IN>::run(g, fx, tn == 0, kw, smem_mx);
 }
 
 }  // namespace fp8l

@@ -233,8 +233,15 @@ int fp8_route_combine(int64_t T, int32_t k, int64_t D, int64_t R, const void* y,
   by_type(dtype, [&](auto in) {
     constexpr int IN = decltype(in)::value;
     const dim3 grid = row_grid(T, vec ? D / 8 : D, a.grid);
-    if (vec) hipLaunchKernelGGL((combine_kernel<IN, 8>), grid, dim3(kRThreads), 0, stream, a);
-    else hipLaunchKernelGGL((combine_kernel<IN, 1>), grid, dim3(kRThreads), 0, stream, a);
+    const bool uni = a.grid.width_log >= 6;  // a wave's pieces are one token's
+    auto go = [&](auto n, auto u) {
+      hipLaunchKernelGGL((combine_kernel<IN, decltype(n)::value, decltype(u)::value>), grid,
+                         dim3(kRThreads), 0, stream, a);
+    };
+    if (vec && uni) go(Int<8>{}, std::true_type{});
+    else if (vec) go(Int<8>{}, std::false_type{});
+    else if (uni) go(Int<1>{}, std::true_type{});
+    else go(Int<1>{}, std::false_type{});
   });
   return hip_status();
 }

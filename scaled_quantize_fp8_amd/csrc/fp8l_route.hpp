@@ -850,28 +850,93 @@ FP8L_DEV void store_n(void* p, int64_t i, const float (&v)[N]) {
   else store1<IN>(p, i, v[0]);
 }
 
-// out[t] = sum_i w[t, i] y[pos[t, i]], in slot order in 32 bits, rounded once.
+// N values as loaded, and in 32 bits.
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
 template <int IN, int N>
+struct Raw {
+  static constexpr int kWords = N == 1 ? 1 : (IN == kInF32 ? 8 : 4);
+  uint32_t w[kWords];
+  FP8L_DEV void load(const void* p, int64_t i) {
+    if constexpr (N == 1) {
+      w[0] = __float_as_uint(load1<IN>(p, i));
+    } else {
+      const uint4* const q = reinterpret_cast<const uint4*>(
+          reinterpret_cast<const uint8_t*>(p) + i * (IN == kInF32 ? 4 : 2));
+#pragma unroll
+      for (int j = 0; j < kWords / 4; ++j) {
+        const v4u x = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(q + j));  // read once
+        w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+      }
+    }
+  }
+  FP8L_DEV void zero() {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = 0;
+  }
+  FP8L_DEV float get(int j) const {
+    if constexpr (N == 1 || IN == kInF32) return __uint_as_float(w[j]);
+    else if constexpr (IN == kInBF16)
+      return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    else return f16_to_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
+  }
+};
+
+constexpr int kSlotBatch = 8;  // slots whose rows are loaded together
+
+// Places and weights of slots i0 .. i0 + 7 of a token (-1, 0 past the last).
+// UNI: the token is the wave's, so its slots come by scalar loads (nothing
+// writes them meanwhile) and every row's address is a scalar.
+template <bool UNI>
+FP8L_DEV void load_slots(const int32_t* pos, const float* w, int64_t t, int k, int i0, int R,
+                         int (&p)[kSlotBatch], float (&wt)[kSlotBatch]) {
+  typedef const __attribute__((address_space(4))) int32_t* SInt;
+  typedef const __attribute__((address_space(4))) float* SFloat;
+#pragma unroll
+  for (int s = 0; s < kSlotBatch; ++s) {
+    const int64_t at = t * k + min(i0 + s, k - 1);
+    if constexpr (UNI) {
+      p[s] = ((SInt)(uintptr_t)pos)[at];
+      wt[s] = w ? ((SFloat)(uintptr_t)w)[at] : 1.0f;
+    } else {
+      p[s] = pos[at];
+      wt[s] = w ? w[at] : 1.0f;
+    }
+    if (i0 + s >= k || p[s] >= R) p[s] = -1;
+  }
+}
+
+// out[t] = sum_i w[t, i] y[pos[t, i]], in slot order in 32 bits, rounded once.
+// Bound by reading y: a thread has its piece of eight rows in flight (4096
+// tokens, 8 slots of 4096 bf16 values, 302 MB: COMBINE_US us; one row after the
+// other 91).
+template <int IN, int N, bool UNI>
 __global__ __launch_bounds__(kRThreads) void combine_kernel(CombineArgs a) {
   const int piece = blockIdx.y * (1 << a.grid.width_log) + (threadIdx.x & ((1 << a.grid.width_log) - 1));
-  if (piece >= a.grid.pieces) return;
   const int per = kRThreads >> a.grid.width_log;
   const int64_t at = (int64_t)piece * N;
-  for (int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.grid.width_log); t < a.T;
-       t += (int64_t)gridDim.x * per) {
+  for (int64_t t0 = (int64_t)blockIdx.x * per + (threadIdx.x >> a.grid.width_log); t0 < a.T;
+       t0 += (int64_t)gridDim.x * per) {
+    const int t = UNI ? __builtin_amdgcn_readfirstlane((int)t0) : (int)t0;
     float acc[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-    for (int i = 0; i < a.k; ++i) {
-      const int p = a.pos[t * a.k + i];
-      if (p < 0 || p >= a.R) continue;
-      const float w = a.w ? a.w[t * a.k + i] : 1.0f;
-      float v[N];
-      load_n<IN>(a.y, p * a.D + at, v);
+    for (int i0 = 0; i0 < a.k; i0 += kSlotBatch) {
+      int p[kSlotBatch];
+      float w[kSlotBatch];
+      load_slots<UNI>(a.pos, a.w, t, a.k, i0, a.R, p, w);
+      Raw<IN, N> v[kSlotBatch];
 #pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = __builtin_fmaf(w, v[j], acc[j]);
+      for (int s = 0; s < kSlotBatch; ++s) {
+        v[s].zero();
+        if (p[s] >= 0 && piece < a.grid.pieces) v[s].load(a.y, p[s] * a.D + at);
+      }
+#pragma unroll
+      for (int s = 0; s < kSlotBatch; ++s)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          acc[j] = __builtin_fmaf(p[s] >= 0 ? w[s] : 0.0f, v[s].get(j), acc[j]);
     }
-    store_n<IN>(a.out, t * a.D + at, acc);
+    if (piece < a.grid.pieces) store_n<IN>(a.out, t * a.D + at, acc);
   }
 }
 
@@ -890,40 +955,42 @@ struct CombineBwdArgs {
 // wave per token, eight slots at a time.
 template <int IN, int N>
 __global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a) {
-  constexpr int S = 8;
+  constexpr int S = kSlotBatch;
   const int lane = threadIdx.x & 63;
   const int64_t pieces = a.D / N;
-  for (int64_t t = (int64_t)blockIdx.x * (kRThreads / 64) + (threadIdx.x >> 6); t < a.T;
-       t += (int64_t)gridDim.x * (kRThreads / 64)) {
+  for (int64_t t0 = (int64_t)blockIdx.x * (kRThreads / 64) + (threadIdx.x >> 6); t0 < a.T;
+       t0 += (int64_t)gridDim.x * (kRThreads / 64)) {
+    const int t = __builtin_amdgcn_readfirstlane((int)t0);
     for (int i0 = 0; i0 < a.k; i0 += S) {
       int p[S];
       float w[S], dot[S];
+      load_slots<true>(a.pos, a.w, t, a.k, i0, a.R, p, w);
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const bool in = i0 + s < a.k;
-        p[s] = in ? a.pos[t * a.k + i0 + s] : -1;
-        if (p[s] >= a.R) p[s] = -1;
-        w[s] = in ? a.w[t * a.k + i0 + s] : 0.0f;
-        dot[s] = 0.0f;
-      }
+      for (int s = 0; s < S; ++s) dot[s] = 0.0f;
       for (int64_t c = lane; c < pieces; c += 64) {
         float g[N];
         load_n<IN>(a.dout, t * a.D + c * N, g);
+        if (a.dw) {
+          Raw<IN, N> v[S];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          if (p[s] < 0) continue;
-          const int64_t at = p[s] * a.D + c * N;
-          if (a.dw) {
-            float v[N];
-            load_n<IN>(a.y, at, v);
-#pragma unroll
-            for (int j = 0; j < N; ++j) dot[s] = __builtin_fmaf(g[j], v[j], dot[s]);
+          for (int s = 0; s < S; ++s) {
+            if (p[s] >= 0) v[s].load(a.y, p[s] * a.D + c * N);
+            else v[s].zero();
           }
-          if (a.dy) {
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              if (p[s] >= 0) dot[s] = __builtin_fmaf(g[j], v[s].get(j), dot[s]);
+        }
+        if (a.dy) {
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            if (p[s] < 0) continue;
             float v[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) v[j] = w[s] * g[j];
-            store_n<IN>(a.dy, at, v);
+            store_n<IN>(a.dy, p[s] * a.D + c * N, v);
           }
         }
       }
@@ -931,7 +998,7 @@ __global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           const float d = lanes_sum<64>(dot[s]);
-          if (lane == 0 && i0 + s < a.k) a.dw[t * a.k + i0 + s] = d;
+          if (lane == 0 && i0 + s < a.k) a.dw[(int64_t)t * a.k + i0 + s] = d;
         }
       }
     }
