@@ -30,14 +30,14 @@ void by_type(int32_t dt, F&& f) {
   else f(std::integral_constant<int, kInBF16>{});
 }
 
-// Tiles of 16 rows (fewer where there are no more), walked along K by as many
-// blocks as give the chip about 16 per CU.
-dim3 quant_grid(int64_t mats, int64_t rows, int64_t steps, int32_t* rows_log) {
+// Tiles of 16 rows (fewer where there are no more); along K, `unroll` steps at
+// a time, as many blocks side by side as give the chip about 16 per CU.
+dim3 quant_grid(int64_t mats, int64_t rows, int64_t steps, int unroll, int32_t* rows_log) {
   int log = 0;
   while (log < 4 && (1 << log) < rows) ++log;
   *rows_log = log;
   const int64_t bx = (rows + (1 << log) - 1) >> log, cap = 1 << 20;
-  const int64_t across = 16 >> log, most = (steps + across - 1) / across;
+  const int64_t across = (16 >> log) * unroll, most = (steps + across - 1) / across;
   int64_t by = (16 * cu_count() + bx * mats - 1) / (bx * mats);
   by = by < most ? by : most;
   return dim3((unsigned)(bx < cap ? bx : cap), (unsigned)(by < 65535 ? by : 65535), (unsigned)mats);
@@ -47,11 +47,13 @@ void enqueue_mx_quantize(const void* x, int32_t dt, int64_t mats, int64_t rows, 
                          uint8_t* codes, uint8_t* scales, const int32_t* valid, hipStream_t st) {
   if (mats == 0 || rows == 0 || K == 0) return;
   MxQuantArgs a = {x, codes, reinterpret_cast<uint32_t*>(scales), rows, K, (int32_t)mx_steps(K),
-                   (int32_t)mx_blocks(K), 0, 0, valid};
-  a.vec = aligned16(x) && K % 8 == 0;
-  const dim3 grid = quant_grid(mats, rows, a.steps, &a.rows_log);
+                   (int32_t)mx_blocks(K), 0, valid};
+  const bool vec = aligned16(x) && K % 8 == 0;
+  const dim3 grid = quant_grid(mats, rows, a.steps, dt == FP8_DT_F32 ? 2 : 4, &a.rows_log);
   by_type(dt, [&](auto in) {
-    hipLaunchKernelGGL((mx4_quantize_kernel<decltype(in)::value>), grid, dim3(kMxThreads), 0, st, a);
+    constexpr int IN = decltype(in)::value;
+    if (vec) hipLaunchKernelGGL((mx4_quantize_kernel<IN, true>), grid, dim3(kMxThreads), 0, st, a);
+    else hipLaunchKernelGGL((mx4_quantize_kernel<IN, false>), grid, dim3(kMxThreads), 0, st, a);
   });
 }
 
@@ -228,7 +230,7 @@ int fp8_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t mats
   MxDequantArgs a = {codes, reinterpret_cast<const uint32_t*>(scales), out, rows, K,
                      (int32_t)mx_steps(K), (int32_t)mx_blocks(K), 0, 0};
   a.vec = aligned16(out) && K % 8 == 0;
-  const dim3 grid = quant_grid(mats, rows, a.steps, &a.rows_log);
+  const dim3 grid = quant_grid(mats, rows, a.steps, 1, &a.rows_log);
   by_type(out_dtype, [&](auto in) {
     hipLaunchKernelGGL((mx4_dequantize_kernel<decltype(in)::value>), grid, dim3(kMxThreads), 0,
                        stream, a);

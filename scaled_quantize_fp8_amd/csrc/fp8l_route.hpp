@@ -850,37 +850,6 @@ FP8L_DEV void store_n(void* p, int64_t i, const float (&v)[N]) {
   else store1<IN>(p, i, v[0]);
 }
 
-// N values as loaded, and in 32 bits.
-typedef unsigned v4u __attribute__((ext_vector_type(4)));
-template <int IN, int N>
-struct Raw {
-  static constexpr int kWords = N == 1 ? 1 : (IN == kInF32 ? 8 : 4);
-  uint32_t w[kWords];
-  FP8L_DEV void load(const void* p, int64_t i) {
-    if constexpr (N == 1) {
-      w[0] = __float_as_uint(load1<IN>(p, i));
-    } else {
-      const uint4* const q = reinterpret_cast<const uint4*>(
-          reinterpret_cast<const uint8_t*>(p) + i * (IN == kInF32 ? 4 : 2));
-#pragma unroll
-      for (int j = 0; j < kWords / 4; ++j) {
-        const v4u x = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(q + j));  // read once
-        w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
-      }
-    }
-  }
-  FP8L_DEV void zero() {
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = 0;
-  }
-  FP8L_DEV float get(int j) const {
-    if constexpr (N == 1 || IN == kInF32) return __uint_as_float(w[j]);
-    else if constexpr (IN == kInBF16)
-      return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-    else return f16_to_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
-  }
-};
-
 constexpr int kSlotBatch = 8;  // slots whose rows are loaded together
 
 // Places and weights of slots i0 .. i0 + 7 of a token (-1, 0 past the last).
@@ -928,7 +897,7 @@ __global__ __launch_bounds__(kRThreads) void combine_kernel(CombineArgs a) {
 #pragma unroll
       for (int s = 0; s < kSlotBatch; ++s) {
         v[s].zero();
-        if (p[s] >= 0 && piece < a.grid.pieces) v[s].load(a.y, p[s] * a.D + at);
+        if (p[s] >= 0 && piece < a.grid.pieces) v[s].template load<true>(a.y, p[s] * a.D + at);
       }
 #pragma unroll
       for (int s = 0; s < kSlotBatch; ++s)
@@ -974,7 +943,7 @@ __global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a
           Raw<IN, N> v[S];
 #pragma unroll
           for (int s = 0; s < S; ++s) {
-            if (p[s] >= 0) v[s].load(a.y, p[s] * a.D + c * N);
+            if (p[s] >= 0) v[s].template load<true>(a.y, p[s] * a.D + c * N);
             else v[s].zero();
           }
 #pragma unroll

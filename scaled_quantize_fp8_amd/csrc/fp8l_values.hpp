@@ -1,5 +1,5 @@
-// Stores of fp32 values in the high-precision types (kIn*), rounded to
-// nearest even: the counterparts of load1 and load8.
+// Values of the high-precision types (kIn*): stores of fp32 values, rounded to
+// nearest even (the counterparts of load1 and load8), and raw pieces.
 #pragma once
 
 #include "fp8l_gemm.hpp"
@@ -30,5 +30,58 @@ FP8L_DEV void store8(void* p, int64_t i, const float v[8]) {
     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
+
+// N values (1, or 8 aligned as for load8) as loaded, and in 32 bits: several
+// are in flight when all are loaded before the first is looked at.  ONCE: a
+// streaming load (values that are read once).
+template <int IN, int N>
+struct Raw {
+  static constexpr int kWords = N == 1 ? 1 : (IN == kInF32 ? 8 : 4);
+  typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+  uint32_t w[kWords];
+  // At any address that suits the type (N = 8): gfx950 takes such wide loads.
+  FP8L_DEV void load_any(const void* p, int64_t i) {
+    typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
+    const any4* const q = reinterpret_cast<const any4*>(reinterpret_cast<const uint8_t*>(p) +
+                                                        i * (IN == kInF32 ? 4 : 2));
+#pragma unroll
+    for (int j = 0; j < kWords / 4; ++j) {
+      const any4 x = q[j];
+      w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+    }
+  }
+  FP8L_DEV void put(int j, float f) {  // of a value that the type holds
+    if constexpr (N == 1 || IN == kInF32) w[j] = __float_as_uint(f);
+    else {
+      const uint32_t h = IN == kInBF16 ? __float_as_uint(f) >> 16 : f32_to_f16(f);
+      w[j / 2] = j & 1 ? (w[j / 2] & 0xffffu) | (h << 16) : (w[j / 2] & 0xffff0000u) | h;
+    }
+  }
+  template <bool ONCE = false>
+  FP8L_DEV void load(const void* p, int64_t i) {
+    if constexpr (N == 1) {
+      w[0] = __float_as_uint(load1<IN>(p, i));
+    } else {
+      const uint4* const q = reinterpret_cast<const uint4*>(
+          reinterpret_cast<const uint8_t*>(p) + i * (IN == kInF32 ? 4 : 2));
+#pragma unroll
+      for (int j = 0; j < kWords / 4; ++j) {
+        const words4* const at = reinterpret_cast<const words4*>(q + j);
+        const words4 x = ONCE ? __builtin_nontemporal_load(at) : *at;
+        w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+      }
+    }
+  }
+  FP8L_DEV void zero() {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = 0;
+  }
+  FP8L_DEV float get(int j) const {
+    if constexpr (N == 1 || IN == kInF32) return __uint_as_float(w[j]);
+    else if constexpr (IN == kInBF16)
+      return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    else return f16_to_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
+  }
+};
 
 }  // namespace fp8l
