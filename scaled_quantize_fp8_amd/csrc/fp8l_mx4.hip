@@ -230,7 +230,7 @@ int fp8_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t mats
   MxDequantArgs a = {codes, reinterpret_cast<const uint32_t*>(scales), out, rows, K,
                      (int32_t)mx_steps(K), (int32_t)mx_blocks(K), 0, 0};
   a.vec = aligned16(out) && K % 8 == 0;
-  const dim3 grid = quant_grid(mats, rows, a.steps, 1, &a.rows_log);
+  const dim3 grid = quant_grid(mats, rows, a.steps, 4, &a.rows_log);
   by_type(out_dtype, [&](auto in) {
     hipLaunchKernelGGL((mx4_dequantize_kernel<decltype(in)::value>), grid, dim3(kMxThreads), 0,
                        stream, a);

@@ -146,40 +146,51 @@ struct MxDequantArgs {
   int32_t steps, blocks, vec, rows_log;
 };
 
-// The values of the codes, rounded once to the output's type.
+// The values of the codes, rounded once to the output's type, kU steps in
+// flight.
 template <int IN>
 __global__ __launch_bounds__(kMxThreads) void mx4_dequantize_kernel(MxDequantArgs a) {
+  constexpr int kU = 4;
   const int sl = threadIdx.x & 15, grp = threadIdx.x >> 4;
   const int per = 1 << a.rows_log, across = 16 >> a.rows_log;
   const int64_t mat = blockIdx.z;
   const int64_t row_bytes = (int64_t)a.blocks * 16;
   for (int64_t r = (int64_t)blockIdx.x * per + (grp & (per - 1)); r < a.rows;
        r += (int64_t)gridDim.x * per) {
-    for (int64_t s = (int64_t)blockIdx.y * across + (grp >> a.rows_log); s < a.steps;
-         s += (int64_t)gridDim.y * across) {
-      const int64_t k = s * 128 + 8 * sl;
-      if (k >= a.K) continue;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(
-          a.codes + (mat * a.rows + r) * row_bytes + s * 64 + 4 * sl);
-      const uint32_t word = a.scales[(mat * a.steps + s) * a.rows + r];
-      const uint32_t e = (word >> (8 * (sl >> 2))) & 255u;
-      float v[8];
-      const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-      const f32x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-      const f32x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-      const f32x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-      v[0] = p0.x; v[1] = p0.y; v[2] = p1.x; v[3] = p1.y;
-      v[4] = p2.x; v[5] = p2.y; v[6] = p3.x; v[7] = p3.y;
+    const uint8_t* const codes = a.codes + (mat * a.rows + r) * row_bytes;
+    for (int64_t s0 = (int64_t)blockIdx.y * across * kU + (grp >> a.rows_log); s0 < a.steps;
+         s0 += (int64_t)gridDim.y * across * kU) {
+      uint32_t w[kU], word[kU];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = e == 255u ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(v[i], (int)e - 127);
-      const int64_t at = (mat * a.rows + r) * a.K + k;
-      if (a.vec) {
-        store8<IN>(a.out, at, v);
-      } else {
+      for (int u = 0; u < kU; ++u) {
+        // past the last value: the first piece again, not stored
+        const int64_t s = s0 + u * across, at = s * 128 + 8 * sl < a.K ? s : 0;
+        w[u] = *reinterpret_cast<const uint32_t*>(codes + at * 64 + (at == s ? 4 * sl : 0));
+        word[u] = a.scales[(mat * a.steps + at) * a.rows + r];
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t k = (s0 + u * across) * 128 + 8 * sl;
+        const uint32_t e = (word[u] >> (8 * (sl >> 2))) & 255u;
+        float v[8];
+        const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 0);
+        const f32x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 1);
+        const f32x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 2);
+        const f32x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 3);
+        v[0] = p0.x; v[1] = p0.y; v[2] = p1.x; v[3] = p1.y;
+        v[4] = p2.x; v[5] = p2.y; v[6] = p3.x; v[7] = p3.y;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (k + i < a.K) store1<IN>(a.out, at + i, v[i]);
+          v[i] = e == 255u ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(v[i], (int)e - 127);
+        if (k >= a.K) continue;
+        const int64_t at = (mat * a.rows + r) * a.K + k;
+        if (a.vec) {
+          store8<IN>(a.out, at, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (k + i < a.K) store1<IN>(a.out, at + i, v[i]);
+        }
       }
     }
   }
