@@ -124,6 +124,17 @@ int mx_split(int64_t waves, int64_t steps, int kU) {
   return kw;
 }
 
+// Whether a kernel's blocks for T rows in E groups fit a launch.
+bool mx_fits(int tile, int64_t T, int64_t E, int64_t N, int64_t K) {
+  const int64_t n256 = (N + 255) / 256;
+  if (tile == kTile128x256) return grid_fits(most_units(T, E, 128) * n256, 256);
+  if (tile == kTile256x256w8) return grid_fits(most_units(T, E, 256) * n256, 512);
+  const int mt = tile - kTileSkinny16 + 1;
+  const int64_t units = most_units(T, E, 16 * mt), cols = (N + 15) / 16;
+  const int jw = 8 / mx_split(units * cols, mx_steps(K), mt == 1 ? MxSkinny<1>::kU : MxSkinny<2>::kU);
+  return grid_fits(units * ((cols + jw - 1) / jw), 512);
+}
+
 template <int MT>
 void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st) {
   const int64_t units = gr ? most_units(gr->T, gr->E, 16 * MT) : (g.M + 16 * MT - 1) / (16 * MT);
@@ -148,8 +159,9 @@ void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t 
 // Groups: two rows per expert on average (any unit may have 16, whose codes
 // must leave room for two blocks per CU; 24 rows, 64 experts of 1536 -> 6912
 // 21.5 / 26.8; 16 rows, 16 of 4096 -> 11008 60.1 / 64.9).  groups 0: dense.
-bool fuse_x(const void* x, int32_t dt, int64_t rows, int64_t groups, int64_t K) {
+bool fuse_x(const void* x, int32_t dt, int64_t rows, int64_t groups, int64_t N, int64_t K) {
   if (!is_hp(dt) || K == 0 || K % 8 != 0 || !aligned16(x) || forced_tile() != kTileAuto) return false;
+  if (!mx_fits(kTileSkinny16, rows, groups ? groups : 1, N, K)) return false;
   if (groups == 0) return rows == 1 ? K <= 16384 : rows <= 16 && rows * K <= 12288;
   return rows <= 2 * groups && K <= 4096;
 }
@@ -170,17 +182,46 @@ void launch_fused(MxArgs& g, const MxFusedX& fx, const Groups* gr, const MxStrid
                        kw);
 }
 
-// The kernel for `rows` rows per group on average.
-int mx_tile(int64_t rows, int64_t E, int64_t N) {
+// Microseconds of the kernels, from fits to a sweep of 8 to 8192 rows over six
+// layer shapes, dense and in 8 and 64 groups; `steps` of 128 values of K.
+//   skinny, 16 / 32 / 48 / 64 rows a unit: 4 + units N K (1.05 / 1.86 / 2.42 /
+//     3.2) 1e-7: 17 rows of 4096 -> 11008 10.1 (12.4), 64 18.2 (18.4), of 11008
+//     -> 4096 16.6 (18.4); 32 rows in 64 groups of 4096 -> 11008 115 (122)
+//   128x256, one block per CU: 5.5 + 0.635 steps: K = 1536 / 4096 / 11008 13.6 /
+//     26.5 / 60 (13.1 / 25.8 / 60.1); two blocks per CU: a full round of 512
+//     tiles takes 1.4 steps, fewer tiles at least 0.8 of it: 688 tiles of
+//     K = 4096 67 (65), 1376 126 (125); not below the bytes of W at 5 TB/s
+//   256x256: a full round 1.2 steps, a part of one 0.7 + 0.5 its share (under
+//     the power limit busy CUs slow each other): 129 / 344 / 688 tiles of
+//     K = 4096 34 / 69 / 121 (35 / 71 / 115)
+// The fastest of those that fit a launch, 0: none does.
+int mx_tile(int64_t rows, int64_t E, int64_t N, int64_t K) {
   const int f = forced_tile();
-  if (f == kTile256x256w8 || f == kTile128x256 || (f >= kTileSkinny16 && f <= kTileSkinny64)) return f;
-  if (rows <= 64) return kTileSkinny16 + (int)((rows + 15) / 16) - 1;
-  const int64_t t256 = (rows + 255) / 256 * E * ((N + 255) / 256);
-  return t256 >= cu_count() / 2 ? kTile256x256w8 : kTile128x256;
+  if ((f == kTile256x256w8 || f == kTile128x256 || (f >= kTileSkinny16 && f <= kTileSkinny64)) &&
+      mx_fits(f, rows, E, N, K))
+    return f;
+  const double cus = cu_count(), steps = (double)mx_steps(K), nk = (double)N * (double)K;
+  const double per[4] = {1.05e-7, 1.86e-7, 2.42e-7, 3.2e-7};
+  int best = 0;
+  double us = 1e300;
+  auto offer = [&](int tile, double t) {
+    if (t < us && mx_fits(tile, rows, E, N, K)) us = t, best = tile;
+  };
+  for (int mt = 1; mt <= 4; ++mt)
+    offer(kTileSkinny16 + mt - 1, 4 + expected_units(rows, E, 16 * mt) * nk * per[mt - 1]);
+  const double n256 = (double)((N + 255) / 256), bytes = expected_units(rows, E, 1 << 30) * nk * 0.53;
+  const double t128 = expected_units(rows, E, 128) * n256;
+  double t = t128 <= cus ? 5.5 + 0.635 * steps
+                         : 5 + (t128 < 1.6 * cus ? 0.8 : t128 / (2 * cus)) * 1.4 * steps;
+  offer(kTile128x256, t < 4 + bytes / 5e6 ? 4 + bytes / 5e6 : t);
+  const double rounds = expected_units(rows, E, 256) * n256 / cus, full = floor(rounds);
+  t = 5 + (1.2 * full + (rounds > full ? 0.7 + 0.5 * (rounds - full) : 0)) * steps;
+  offer(kTile256x256w8, t < 4 + bytes / 5e6 ? 4 + bytes / 5e6 : t);
+  return best;
 }
 
-void launch_product(MxArgs& g, int64_t rows, const Groups* gr, const MxStrides& s, hipStream_t st) {
-  switch (mx_tile(rows, gr ? gr->E : 1, g.N)) {
+void launch_product(int tile, MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st) {
+  switch (tile) {
     case kTileSkinny16: return launch_skinny<1>(g, gr, s, st);
     case kTileSkinny32: return launch_skinny<2>(g, gr, s, st);
     case kTileSkinny48: return launch_skinny<3>(g, gr, s, st);
@@ -244,11 +285,13 @@ int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x
                        uint8_t* sx_out, hipStream_t stream) {
   int st = check_mx(M, K);
   if (st || (st = check_mx(N, K))) return st;
-  if (!mul_ok(M, N) || !grid_fits(((M + 63) / 64) * ((N + 15) / 16), 512)) return FP8_ERR_SHAPE;
+  if (!mul_ok(M, N)) return FP8_ERR_SHAPE;
+  const int tile = M > 0 && N > 0 ? mx_tile(M, 1, N, K) : 1;
+  if (tile == 0) return FP8_ERR_SHAPE;
   if ((st = check_linear(M, N, K, x, x_dtype, x_scales, w, w_scales, out_dtype, y, x4_out, sx_out)))
     return st;
   MxArgs g = mx_args(M, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
-  if (M > 0 && N > 0 && fuse_x(x, x_dtype, M, 0, K)) {
+  if (M > 0 && N > 0 && fuse_x(x, x_dtype, M, 0, N, K)) {
     by_type(x_dtype, [&](auto in) {
       launch_fused<decltype(in)::value>(g, MxFusedX{x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)}, nullptr, MxStrides{},
                                         stream);
@@ -257,7 +300,7 @@ int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x
   }
   if (is_hp(x_dtype)) enqueue_mx_quantize(x, x_dtype, 1, M, K, x4_out, sx_out, nullptr, stream);
   if (M == 0 || N == 0) return hip_status();
-  launch_product(g, M, nullptr, MxStrides{}, stream);
+  launch_product(tile, g, nullptr, MxStrides{}, stream);
   return hip_status();
 }
 
@@ -268,14 +311,15 @@ int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const
                                hipStream_t stream) {
   int st = check_grouped(T, E, N, K);
   if (st || (st = check_mx(T, K)) || (st = check_mx(N, K))) return st;
-  if (!grid_fits(most_units(T, E, 64) * ((N + 15) / 16), 512)) return FP8_ERR_SHAPE;
+  const int tile = T > 0 && N > 0 ? mx_tile(T, E, N, K) : 1;
+  if (tile == 0) return FP8_ERR_SHAPE;
   if (!offsets) return FP8_ERR_NULL;
   if ((st = check_linear(T, N, K, x, x_dtype, x_scales, w, w_scales, out_dtype, y, x4_out, sx_out)))
     return st;
   MxArgs g = mx_args(T, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
   const MxStrides s = {N * g.ld, N * g.steps, N};
   const Groups gr = {offsets, E, (int32_t)T};
-  if (T > 0 && N > 0 && fuse_x(x, x_dtype, T, E, K)) {
+  if (T > 0 && N > 0 && fuse_x(x, x_dtype, T, E, N, K)) {
     by_type(x_dtype, [&](auto in) {
       launch_fused<decltype(in)::value>(g, MxFusedX{x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)}, &gr, s, stream);
     });
@@ -284,7 +328,7 @@ int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const
   if (is_hp(x_dtype))
     enqueue_mx_quantize(x, x_dtype, 1, T, K, x4_out, sx_out, offsets + E, stream);
   if (T == 0 || N == 0) return hip_status();
-  launch_product(g, (T + E - 1) / E, &gr, s, stream);
+  launch_product(tile, g, &gr, s, stream);
   return hip_status();
 }
 

@@ -81,7 +81,7 @@ FP8L_DEV MxEight mx_eight(const float v[8], bool inside, int sl) {
 
 // A block of 256 threads walks its tile of rows along K, kU steps at a time
 // with their loads in flight together (11008 x 4096 bf16, 114 MB in and out:
-// QUANT_US us; one step at a time 34).
+// 22 us; one step at a time 34).
 // VEC: K a multiple of 8 and x aligned to 16 bytes.
 template <int IN, bool VEC>
 __global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a) {

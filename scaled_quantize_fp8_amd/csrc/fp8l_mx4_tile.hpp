@@ -4,13 +4,23 @@
 // The schedule is the 8-bit tiles' (fp8l_gemm4.hpp, fp8l_gemm6.hpp): operands
 // go by DMA into a ring of LDS stages of 64 bytes of K per row (128 values
 // here), fragments of the next step are read while the current one's MFMAs
-// run, A fragments single-buffered, B fragments double-buffered.  A 32x32x64
+// run, A fragments single-buffered, B fragments double-buffered, here in two
+// asm blocks a step instead of five (8192 x 8192 x 8192: 287 us against 289 to
+// 294).  A 32x32x64
 // MFMA takes 16 bytes of codes per lane, so a lane's 32 bytes of a step feed
 // two: its low half (block 2 h of the step, h = lane / 32) and its high half
 // (block 2 h + 1), each with that block's scale.  Which blocks meet in which
 // instruction does not matter as long as both operands agree.  Per step a wave
 // issues 16 MFMAs of 8 passes: the LDS traffic per matrix cycle is that of the
 // 8-bit tiles.
+//
+// What bounds it: 8192 x 8192 x 8192 runs at 3.8 P/s (the vendor library's
+// product 3.05), matrix cores busy 52% of the cycles at 1.7 GHz, the clock that
+// the power limit leaves for these operands; with zeros for operands the same
+// kernel takes 240 us at 2.4.  Tried, no faster with real operands: 16x16x128
+// MFMAs (alone 8.5 P/s where these reach 6.5), four waves of 128x128 with a
+// third less LDS traffic (305 us), the stages' loads dealt to other waves at
+// other times (313).
 //
 // Scales travel with the codes: a step's 4-byte words of the tile's rows and
 // columns (one DMA load of 64 words per wave, more for 128x256) lie behind the
@@ -37,69 +47,56 @@ struct MxSlot {
 #define FP8L_XH(i)                                                                        \
   "v_mfma_scale_f32_32x32x64_f8f6f4 %[c" #i "], %[d" #i "], %[y" #i "], %[c" #i "], %[t" #i \
   "], %[u" #i "] op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4\n\t"
-#define FP8L_XM1 FP8L_XL(0) FP8L_XH(0)
-#define FP8L_XM2 FP8L_XL(0) FP8L_XL(1) FP8L_XH(0) FP8L_XH(1)
+#define FP8L_XM4                                                                          \
+  FP8L_XL(0) FP8L_XL(1) FP8L_XL(2) FP8L_XL(3) FP8L_XH(0) FP8L_XH(1) FP8L_XH(2) FP8L_XH(3)
 #define FP8L_XI(i)                                                              \
   [b##i] "v"(lo4(*m[i].b)), [d##i] "v"(hi4(*m[i].b)), [x##i] "v"(lo4(*m[i].x)), \
       [y##i] "v"(hi4(*m[i].x)), [t##i] "v"(*m[i].sb), [u##i] "v"(*m[i].sx)
-#define FP8L_XI1 FP8L_XI(0)
-#define FP8L_XI2 FP8L_XI1, FP8L_XI(1)
+#define FP8L_XI4 FP8L_XI(0), FP8L_XI(1), FP8L_XI(2), FP8L_XI(3)
 
-#define FP8L_MX_BY_COUNT(S)      \
-  do {                           \
-    if constexpr (NM == 1) S(1); \
-    else S(2);                   \
-  } while (0)
-
-template <int NM>
-FP8L_DEV void mx_mfma_only(const MxSlot (&m)[2]) {
+FP8L_DEV void mx_mfma_only(const MxSlot (&m)[4]) {
   // s_nop 1: operands may have just been written by VALU
-#define FP8L_XONLY(n) asm volatile("s_nop 1\n\t" FP8L_XM##n "" : FP8L_CO##n : FP8L_XI##n)
-  FP8L_MX_BY_COUNT(FP8L_XONLY);
-#undef FP8L_XONLY
+  asm volatile("s_nop 1\n\t" FP8L_XM4 "" : FP8L_CO4 : FP8L_XI4);
 }
 
-// Fragment at offset OFF from the lane addresses a0, a1 and its scales at
-// offset SOFF from sa, read while NM fragments' products run.
-template <int NM, int OFF, int SOFF>
-FP8L_DEV void mx_read1(uint32_t a0, uint32_t a1, uint32_t sa, v8i& n0, uint32_t& s0,
-                       const MxSlot (&m)[2]) {
-  v4i r0, r1;
-  uint32_t e0;
-#define FP8L_XR1(n)                                                                            \
-  asm volatile(FP8L_RKC(r0, a0, o0) FP8L_RKC(r1, a1, o0)                                       \
-               "ds_read_u16 %[e0], %[sa] offset:%[so]\n\t" FP8L_XM##n "s_waitcnt lgkmcnt(0)"   \
-               : [r0] "=&v"(r0), [r1] "=&v"(r1), [e0] "=&v"(e0), FP8L_CO##n                    \
-               : [a0] "v"(a0), [a1] "v"(a1), [sa] "v"(sa), [o0] "n"(OFF), [so] "n"(SOFF),      \
-                 FP8L_XI##n                                                                    \
-               : "memory")
-  FP8L_MX_BY_COUNT(FP8L_XR1);
-#undef FP8L_XR1
-  n0 = v8i{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-  s0 = e0;
-}
-
-// Two fragments 32 rows apart and their scales.
-template <int NM>
-FP8L_DEV void mx_read2(uint32_t a0, uint32_t a1, uint32_t sa, v8i& n0, v8i& n1, uint32_t& s0,
-                       uint32_t& s1, const MxSlot (&m)[2]) {
+// A fragments f and f + 1 of the next step at offset OFF (their scales at SOFF)
+// and, WITH_B, its B fragments, read while the four fragment products m run.
+FP8L_DEV v8i join8(v4i a, v4i b) { return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}; }
+template <int OFF, int SOFF>
+FP8L_DEV void mx_read_a(const uint32_t (&a)[2], uint32_t sa, v8i* n, uint32_t* e,
+                        const MxSlot (&m)[4]) {
   v4i r0, r1, r2, r3;
   uint32_t e0, e1;
-#define FP8L_XR2(n)                                                                            \
-  asm volatile(FP8L_RKC(r0, a0, o0) FP8L_RKC(r1, a1, o0) FP8L_RKC(r2, a0, o1)                  \
-                   FP8L_RKC(r3, a1, o1) "ds_read_u16 %[e0], %[sa]\n\t"                         \
-                   "ds_read_u16 %[e1], %[sa] offset:128\n\t" FP8L_XM##n "s_waitcnt lgkmcnt(0)" \
-               : [r0] "=&v"(r0), [r1] "=&v"(r1), [r2] "=&v"(r2), [r3] "=&v"(r3),               \
-                 [e0] "=&v"(e0), [e1] "=&v"(e1), FP8L_CO##n                                    \
-               : [a0] "v"(a0), [a1] "v"(a1), [sa] "v"(sa), [o0] "n"(0), [o1] "n"(2048),        \
-                 FP8L_XI##n                                                                    \
-               : "memory")
-  FP8L_MX_BY_COUNT(FP8L_XR2);
-#undef FP8L_XR2
-  n0 = v8i{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-  n1 = v8i{r2.x, r2.y, r2.z, r2.w, r3.x, r3.y, r3.z, r3.w};
-  s0 = e0;
-  s1 = e1;
+  asm volatile(FP8L_RKC(r0, a0, o0) FP8L_RKC(r1, a1, o0) FP8L_RKC(r2, a0, o1) FP8L_RKC(r3, a1, o1)
+               "ds_read_u16 %[e0], %[sa] offset:%[s0]\n\t"
+               "ds_read_u16 %[e1], %[sa] offset:%[s1]\n\t" FP8L_XM4 "s_waitcnt lgkmcnt(0)"
+               : [r0] "=&v"(r0), [r1] "=&v"(r1), [r2] "=&v"(r2), [r3] "=&v"(r3), [e0] "=&v"(e0),
+                 [e1] "=&v"(e1), FP8L_CO4
+               : [a0] "v"(a[0]), [a1] "v"(a[1]), [sa] "v"(sa), [o0] "n"(OFF), [o1] "n"(OFF + 2048),
+                 [s0] "n"(SOFF), [s1] "n"(SOFF + 128), FP8L_XI4
+               : "memory");
+  n[0] = join8(r0, r1), n[1] = join8(r2, r3), e[0] = e0, e[1] = e1;
+}
+FP8L_DEV void mx_read_ab(const uint32_t (&a)[2], uint32_t sa, const uint32_t (&b)[2], uint32_t sb,
+                         v8i* na, uint32_t* ea, v8i* nb, uint32_t* eb, const MxSlot (&m)[4]) {
+  v4i r0, r1, r2, r3, r4, r5, r6, r7;
+  uint32_t e0, e1, e2, e3;
+  asm volatile(
+      "ds_read_b128 %[r0], %[a0]\n\tds_read_b128 %[r1], %[a1]\n\t"
+      "ds_read_b128 %[r4], %[p0]\n\tds_read_b128 %[r5], %[p1]\n\t"
+      "ds_read_b128 %[r2], %[a0] offset:2048\n\tds_read_b128 %[r3], %[a1] offset:2048\n\t"
+      "ds_read_b128 %[r6], %[p0] offset:2048\n\tds_read_b128 %[r7], %[p1] offset:2048\n\t"
+      "ds_read_u16 %[e0], %[sa]\n\tds_read_u16 %[e1], %[sa] offset:128\n\t"
+      "ds_read_u16 %[e2], %[sb]\n\tds_read_u16 %[e3], %[sb] offset:128\n\t" FP8L_XM4
+      "s_waitcnt lgkmcnt(0)"
+      : [r0] "=&v"(r0), [r1] "=&v"(r1), [r2] "=&v"(r2), [r3] "=&v"(r3), [r4] "=&v"(r4),
+        [r5] "=&v"(r5), [r6] "=&v"(r6), [r7] "=&v"(r7), [e0] "=&v"(e0), [e1] "=&v"(e1),
+        [e2] "=&v"(e2), [e3] "=&v"(e3), FP8L_CO4
+      : [a0] "v"(a[0]), [a1] "v"(a[1]), [p0] "v"(b[0]), [p1] "v"(b[1]), [sa] "v"(sa), [sb] "v"(sb),
+        FP8L_XI4
+      : "memory");
+  na[0] = join8(r0, r1), na[1] = join8(r2, r3), ea[0] = e0, ea[1] = e1;
+  nb[0] = join8(r4, r5), nb[1] = join8(r6, r7), eb[0] = e2, eb[1] = e3;
 }
 
 template <int WGM>
@@ -202,12 +199,12 @@ struct MxTile {
           : "=&v"(ea[0]), "=&v"(ea[1]), "=&v"(ea[2]), "=&v"(ea[3]), "=&v"(eb[0][0]), "=&v"(eb[0][1])
           : "v"(sra), "v"(srb)
           : "memory");
-      const MxSlot m[2] = {slot(0, 0, 0), slot(0, 1, 0)};
-      mx_mfma_only<2>(m);
+      const MxSlot m[4] = {slot(0, 0, 0), slot(0, 1, 0), slot(1, 0, 0), slot(1, 1, 0)};
+      mx_mfma_only(m);
     }
 
-    // Step kt: on entry the products (a0, *) of step kt are issued; fa, ea
-    // hold step kt's A fragments, fb[CUR], eb[CUR] its B fragments.
+    // Step kt: on entry the products of A fragments 0 and 1 of step kt are issued;
+    // fa, ea hold step kt's A fragments, fb[CUR], eb[CUR] its B fragments.
     const __amdgpu_buffer_rsrc_t ra_all = make_rsrc(g.a, a_bytes);
     const __amdgpu_buffer_rsrc_t rb_all = make_rsrc(g.b, b_bytes);
     auto kstep_body = [&](int kt, auto cur_tag, auto fast_tag) {
@@ -228,8 +225,7 @@ struct MxTile {
       uint8_t* const sf = step_buf(kf);
       auto load = [&](auto j_tag) {
         constexpr int j = decltype(j_tag)::value;
-        if constexpr (j >= kDma) return;
-        else if constexpr (j >= OA::kPerWave + OB::kPerWave) {
+        if constexpr (j >= OA::kPerWave + OB::kPerWave) {
           if (refill) scale_load(kf, std::integral_constant<int, j - OA::kPerWave - OB::kPerWave>{});
         } else if constexpr (FAST) {
           if constexpr (j < OA::kPerWave)
@@ -246,41 +242,21 @@ struct MxTile {
             ob.template issue_step<j - OA::kPerWave>(rb_k, sf + OA::kBytes, kf, wv);
         }
       };
-      auto loads = [&](auto b_tag) {  // this block's share of the refill
-        load(std::integral_constant<int, 2 * decltype(b_tag)::value>{});
-        load(std::integral_constant<int, 2 * decltype(b_tag)::value + 1>{});
-      };
       const uint32_t d = (uint32_t)(((kt + 1) % kStages) * kStep);
-      using I0 = std::integral_constant<int, 0>;
-      using I1 = std::integral_constant<int, 1>;
-      using I2 = std::integral_constant<int, 2>;
-      using I3 = std::integral_constant<int, 3>;
-      {  // fa[0] <- step kt+1; products (a1, *)
-        const MxSlot m[2] = {slot(1, 0, CUR), slot(1, 1, CUR)};
-        mx_read1<2, 0, 0>(fra.a[0] + d, fra.a[1] + d, sra + d, fa[0], ea[0], m);
+      const uint32_t a0[2] = {fra.a[0] + d, fra.a[1] + d}, b0[2] = {frb.a[0] + d, frb.a[1] + d};
+      constexpr int kHalf = (kDma + 1) / 2;
+      {  // A 0 and 1, B <- step kt+1; products of A 2 and 3
+        const MxSlot m[4] = {slot(2, 0, CUR), slot(2, 1, CUR), slot(3, 0, CUR), slot(3, 1, CUR)};
+        mx_read_ab(a0, sra + d, b0, srb + d, &fa[0], &ea[0], fb[NXT], eb[NXT], m);
       }
-      loads(I0{});
-      {  // fa[1] <- step kt+1; products (a2, *)
-        const MxSlot m[2] = {slot(2, 0, CUR), slot(2, 1, CUR)};
-        mx_read1<2, 2048, 128>(fra.a[0] + d, fra.a[1] + d, sra + d, fa[1], ea[1], m);
+      static_for<kHalf>(load);
+      {  // A 2 and 3 <- step kt+1; products of A 0 and 1 of step kt+1
+        const MxSlot m[4] = {slot(0, 0, NXT), slot(0, 1, NXT), slot(1, 0, NXT), slot(1, 1, NXT)};
+        mx_read_a<4096, 256>(a0, sra + d, &fa[2], &ea[2], m);
       }
-      loads(I1{});
-      {  // fa[2] <- step kt+1; product (a3, b0)
-        const MxSlot m[2] = {slot(3, 0, CUR), slot(3, 0, CUR)};
-        mx_read1<1, 4096, 256>(fra.a[0] + d, fra.a[1] + d, sra + d, fa[2], ea[2], m);
-      }
-      loads(I2{});
-      {  // fb[NXT] <- step kt+1; product (a3, b1)
-        const MxSlot m[2] = {slot(3, 1, CUR), slot(3, 1, CUR)};
-        mx_read2<1>(frb.a[0] + d, frb.a[1] + d, srb + d, fb[NXT][0], fb[NXT][1], eb[NXT][0],
-                    eb[NXT][1], m);
-      }
-      loads(I3{});
-      static_assert(kDma <= 8, "loads over four blocks");
-      {  // fa[3] <- step kt+1; products (a0, *) of step kt+1
-        const MxSlot m[2] = {slot(0, 0, NXT), slot(0, 1, NXT)};
-        mx_read1<2, 6144, 384>(fra.a[0] + d, fra.a[1] + d, sra + d, fa[3], ea[3], m);
-      }
+      static_for<kDma - kHalf>([&](auto j) {
+        load(std::integral_constant<int, kHalf + decltype(j)::value>{});
+      });
     };
     // steps whose refill (step kt + kStages) ends at or before K; an even count
     const int nf = (int)(g.ld / kBK3);
