@@ -580,7 +580,7 @@ int fp8_i8_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const 
 typedef enum { FP8_ROUTE_SOFTMAX = 0, FP8_ROUTE_SIGMOID = 1 } fp8_route_score_t;
 
 /* Bytes of the workspace of fp8_route_plan, and of fp8_route_fwd with places;
- * 0 where none is needed (at most 2048 slots) or the sizes are refused. */
+ * 0 where none is needed (at most 32768 slots) or the sizes are refused. */
 size_t fp8_route_workspace_bytes(int64_t T, int32_t E, int32_t k);
 
 /*

@@ -312,23 +312,28 @@ FP8L_DEV float slot_weight(const RouteArgs& a, const float (&z)[V], float m, boo
 // The choice of scores held in 64 bits, from scores in 32 bits and a proof
 // (16384 rows of 256 experts entirely in 64 bits: 105 us).
 //
-//   keys     every expert gets an upper bound u of its c (a score in 32 bits
-//            is off by less than 2^-17 of itself: an exponential's argument of
-//            up to 88 rounded to 2^-24, a few units for exp, reciprocal and
-//            sums), as an ordered integer below 2^31 whose lowest bits give way
-//            to the expert's index, lower ones larger.  All keys differ, so a
-//            round of the top-k is a maximum over the lanes, and the largest
-//            key below the last one is last + max(key - last) in unsigned
-//            numbers, without striking anything out.
-//   proof    each chosen expert's c is taken in 64 bits, one per lane.  All
-//            others have c <= the bound of the (k + 1)-th key: if every chosen
-//            c exceeds that, the set is right.  The order is then checked on
-//            the same values, and sorted by them where it is not.
+//   keys     every expert gets an upper bound of its c as an integer below
+//            2^31 whose lowest bits give way to the expert's index, lower ones
+//            larger: a fixed-point number over the range of the row's c (24 bits
+//            less one, so as fine as the scores), or the float's ordered bits
+//            where logits of 16 bits are compared as they are, without loss.
+//            All keys differ, so a round of the top-k is a maximum over the
+//            lanes, and the largest key below the last one is
+//            last + max(key - last) in unsigned numbers, without striking
+//            anything out.
+//   proof    the chosen experts' c, one per lane, in 32 bits with its bound:
+//            all others have c <= what the (k + 1)-th key stands for, so the
+//            set is right if every chosen c is larger, and the order if they
+//            are further apart than their errors.  If not, the same in 64 bits,
+//            where the order is also mended.
+//   errors   a score in 32 bits is off by less than (|x| + 24) 2^-23 of itself,
+//            x its exponential's argument (rounded to 2^-24, and by the factor
+//            log2 e; the rest for exp, reciprocal and the softmax's sum: 20
+//            additions, and its terms' |x|, whose mean is at most log E).
 //   groups   scored in 32 bits; right if the least kept and the best dropped
 //            group are further apart than the scores' errors.
 //   else     the wave does its rows again in 64 bits.
 //
-// Logits of 16 bits without a bias have keys without loss: nothing to prove.
 // One row per 16 lanes, V experts per lane.
 
 // Key bits of the index.
@@ -340,10 +345,6 @@ FP8L_DEV uint32_t ordered(float f) {
   const uint32_t u = __float_as_uint(f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-FP8L_DEV float unordered(uint32_t o) {
-  return __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
-}
-
 // Value of the next lane of 16 (the last one's: its own).
 FP8L_DEV uint32_t next_lane(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x101, 0xF, 0xF, false);  // row_shl:1
@@ -367,49 +368,81 @@ FP8L_DEV bool keep_groups32(const RouteArgs& a, float (&c)[V], const float (&g)[
   return best == -INFINITY || least - best > 2.0f * err + 0x1p-21f * (fabsf(least) + fabsf(best));
 }
 
+// A score in 32 bits; x: what its error grows with.  m, r: the row's largest
+// logit and the reciprocal of the softmax's sum.
+FP8L_DEV float score32(const RouteArgs& a, float z, float m, float r, float& x) {
+  if (a.score == kSigmoid) {
+    x = fabsf(z);
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+  }
+  x = m - z;
+  return __expf(z - m) * r;
+}
+// c's error: the score's, the addition's, and what underflows.
+FP8L_DEV float c_error(float p, float x, float c) {
+  return p * ((fminf(x, 128.0f) + 24.0f) * 0x1p-23f) + 0x1p-23f * fabsf(c) + 0x1p-120f;
+}
+
 // The chosen expert of slot i in lane i (-1: none) and its logit; sure: false
 // where the row has to be done in 64 bits.  m: the row's largest logit.
 template <int IN, int V>
 FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[V], int64_t t,
                       float m, int sl, bool& sure, float& zi) {
   constexpr int LOW = key_low<V>();
+  constexpr uint32_t MASK = (1u << LOW) - 1;
   const bool grouped = a.groups > 1 && a.kept < a.groups;
   const bool by_score = a.bias || (grouped && a.group_top == 2);
-  float c[V], g[V], sum = 1.0f, top = 0.0f;
+  float c[V], g[V], sum = 1.0f, rs = 1.0f, err = 0.0f;
   if (by_score) {
-    if (a.score == kSigmoid) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) g[v] = __builtin_amdgcn_rcpf(1.0f + __expf(-z[v]));
-    } else {
+    if (a.score == kSoftmax) {
       sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) sum += g[v] = __expf(z[v] - m);
       sum = lanes_sum<16>(sum);
-      const float r = __builtin_amdgcn_rcpf(sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v) g[v] *= r;
+      rs = __builtin_amdgcn_rcpf(sum);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const bool off = z[v] == -INFINITY;
-      const float p = g[v];
-      top = fmaxf(top, off ? 0.0f : p);
+      float x, p = score32(a, z[v], m, rs, x);
       g[v] = off ? -INFINITY : p + b[v];
-      // the bound: the score's error, the addition's, and what underflows
-      c[v] = a.bias ? g[v] + (0x1p-16f * p + 0x1p-22f * fabsf(g[v]) + 0x1p-120f) : z[v];
+      const float d = g[v] == -INFINITY ? 0.0f : c_error(p, x, g[v]);
+      err = fmaxf(err, d);
+      c[v] = a.bias ? g[v] + 2.0f * d : z[v];  // twice: the addition of the bound
       if (g[v] == -INFINITY) c[v] = -INFINITY;
     }
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = g[v] = z[v];
   }
-  sure = !grouped ||
-         keep_groups32<V>(a, c, g, sl, by_score ? 0x1p-16f * lanes_max<16>(top) + 0x1p-120f : -1.0f);
+  sure = !grouped || keep_groups32<V>(a, c, g, sl, by_score ? 2.0f * lanes_max<16>(err) : -1.0f);
+  // keys
+  const bool exact = IN != kInF32 && !a.bias;
   uint32_t key[V], last = 0;
+  float low = 0.0f, scale = 1.0f;
+  if (exact) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      key[v] = ((ordered(c[v]) >> (LOW + 1)) << LOW) | (MASK - (uint32_t)(sl * V + v));
+  } else {
+    float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      hi = fmaxf(hi, c[v]);
+      lo = fminf(lo, c[v] == -INFINITY ? INFINITY : c[v]);
+    }
+    hi = lanes_max<16>(hi);
+    // masks of very small logits do not count: what lies below is one key apart
+    low = fmaxf(-lanes_max<16>(-lo), hi - 64.0f);
+    scale = 8388600.0f / fmaxf(hi - low, 0x1p-60f);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      key[v] = ((1u + (uint32_t)fmaxf((c[v] - low) * scale, 0.0f)) << LOW) |
+               (MASK - (uint32_t)(sl * V + v));
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const uint32_t low = (uint32_t)((1 << LOW) - 1 - (sl * V + v));
-    key[v] = c[v] == -INFINITY ? 0u : ((ordered(c[v]) >> (LOW + 1)) << LOW) | low;
+    if (c[v] == -INFINITY) key[v] = 0;
     last = max(last, key[v]);
   }
   lane_steps<16>([&](auto s) { last = max(last, lane_step<decltype(s)::value>(last)); });
@@ -423,27 +456,46 @@ FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[
     last = (int32_t)r < 0 ? r + last : 0u;  // no key below the last one: none is left
   }
   const bool live = slot != 0;
-  int e = live ? (1 << LOW) - 1 - (int)(slot & ((1 << LOW) - 1)) : -1;
+  int e = live ? (int)(MASK - (slot & MASK)) : -1;
   zi = live ? load1<IN>(a.z, t * a.E + e) : 0.0f;
-  if (IN != kInF32 && !a.bias) return e;
+  if (exact) return e;
 
+  // (last: the (k + 1)-th key, of a c at most `units` units above low: 1.5 for
+  // the roundings of its three steps)
+  const float units = (float)(last >> LOW) + 2.0f;
+  const float bi = live && a.bias ? a.bias[e] : 0.0f;
+  {
+    float x, p = 0.0f, ci = live ? zi : -INFINITY, d = 0.0f;
+    if (a.bias && live) {
+      p = score32(a, zi, m, rs, x);
+      ci = p + bi;
+      d = c_error(p, x, ci);
+    }
+    const float above = units / scale;
+    const float bound =
+        last == 0 ? -INFINITY : low + above + 0x1p-22f * (fabsf(low) + above);
+    const float cn = __uint_as_float(next_lane(__float_as_uint(ci)));
+    const float dn = __uint_as_float(next_lane(__float_as_uint(d)));
+    const int en = (int)next_lane((uint32_t)e);
+    const bool both = sl + 1 < a.k && live && en >= 0;
+    const bool ok = !live || (ci - 2.0f * d > bound && (!both || ci - cn > 2.0f * (d + dn) ||
+                                                        (!a.bias && ci == cn && e < en)));
+    if (!__any(!ok)) return e;
+  }
   double ci = -INFINITY, p = 0.0;
   if (live) {
     if (a.bias) {
       p = a.score == kSigmoid ? 1.0 / (1.0 + exp(-(double)zi))
                               : exp((double)zi - (double)m) / (double)sum;
-      ci = p + (double)a.bias[e];
+      ci = p + (double)bi;
     } else {
       ci = zi;
     }
   }
   const bool loose = a.bias && a.score == kSoftmax;  // p carries the 32-bit sum's error
   const double slack = loose ? 0x1p-16 : 0.0;
-  // (last: the (k + 1)-th key)
-  const double bound =
-      last == 0 ? -INFINITY
-                : (double)unordered((((last >> LOW) + 1) << (LOW + 1)) - 1);
-  bool ok = !live || ci - slack * p > bound;
+  const double bound = last == 0 ? -INFINITY : ((double)low + (double)units / (double)scale);
+  bool ok = !live || ci - slack * p > bound + 0x1p-30 * fabs(bound);
   const double cn = next_lane(ci), pn = next_lane(p);
   const int en = (int)next_lane((uint32_t)e);
   const bool both = sl + 1 < a.k && live && en >= 0;
@@ -616,15 +668,16 @@ __global__ __launch_bounds__(kRThreads) void route_bwd_kernel(RouteBwdArgs a) {
 
 // Rows sorted by expert, in the order of the slots (a stable counting sort):
 // slot j = t k + i with expert e goes to offsets[e] + the number of earlier
-// slots of e.  Slots of no expert get -1.  The slots are cut into chunks; a
-// first launch counts each chunk's experts, the second adds up what lies
-// before its chunk and places the chunk's slots.  One chunk needs one launch.
-// Nothing is counted by atomics across blocks: places do not depend on timing.
+// slots of e.  Slots of no expert get -1.  The slots are cut into chunks, one
+// per block.  With few of them every block counts all slots itself; with many,
+// a first launch counts each chunk's, and a block adds up what lies before its
+// own.  Nothing is counted by atomics across blocks: places do not depend on
+// timing.
 struct PlanArgs {
   const int32_t* idx;
   int32_t* offsets;  // [E + 1]
   int32_t* pos;      // [n]
-  int32_t* counts;   // [chunks][E]
+  int32_t* counts;   // [chunks][E], null: each block counts all slots
   int32_t n, E, chunk, chunks;
 };
 
@@ -658,7 +711,7 @@ FP8L_DEV uint64_t same_key(int key, int bits) {
 // for none.  lds: NW (E + 1) integers, then 3 NT more.
 template <int NT>
 __host__ __device__ constexpr int place_lds(int E) {
-  return (4 * (NT / 64 * (E + 1) + 3 * NT) + 15) & ~15;
+  return (4 * ((NT / 64 + 2) * (E + 1) + 3 * NT) + 15) & ~15;
 }
 
 template <int NT, class F>
@@ -669,8 +722,23 @@ FP8L_DEV void place_chunk(const PlanArgs& a, int block, int32_t* lds, F&& expert
   int32_t* const before_part = lds + NW * W;  // [SPLIT][COLS]
   int32_t* const total_part = before_part + NT;
   int32_t* const wave_total = total_part + NT;
+  int32_t* const all = wave_total + NT;  // without counts: [before this chunk, from it on][expert]
+  const bool count_all = a.chunks > 1 && !a.counts;
   for (int i = tid; i < NW * W; i += NT) next[i] = 0;
+  if (count_all)
+    for (int i = tid; i < 2 * W; i += NT) all[i] = 0;
   __syncthreads();
+  if (count_all) {
+    constexpr int U = 8;  // loads in flight
+    for (int j0 = tid; j0 < a.n; j0 += U * NT) {
+      int e[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) e[u] = expert(min(j0 + u * NT, a.n - 1));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + u * NT < a.n) atomicAdd(&all[(j0 + u * NT < block * a.chunk ? 0 : W) + e[u]], 1);
+    }
+  }
   // wave w's slots: the w-th part of the chunk
   const int per = a.chunk / NW;
   const int j0 = block * a.chunk + wave * per, j1 = min(j0 + per, a.n);
@@ -685,6 +753,8 @@ FP8L_DEV void place_chunk(const PlanArgs& a, int block, int32_t* lds, F&& expert
     if (e < a.E) {
       if (a.chunks == 1) {
         for (int w = part; w < NW; w += SPLIT) total += next[w * W + e];
+      } else if (count_all) {
+        if (part == 0) before = all[e], total = all[e] + all[W + e];
       } else {
         constexpr int U = 16;  // loads in flight
         for (int c0 = part; c0 < a.chunks; c0 += U * SPLIT) {

@@ -46,19 +46,19 @@ def test_route_refusals(lib):
     for kw in (dict(dt=E4), dict(dt=9), dict(score=2), dict(score=-1)):
         assert _fwd(lib, **kw) == F.FP8_ERR_DTYPE, kw
         assert _bwd(lib, **kw) == F.FP8_ERR_DTYPE, kw
-    for kw in (dict(z=Z), dict(idx=Z), dict(w=Z), dict(off=Z), dict(pos=Z), dict(T=4000, ws=Z)):
+    for kw in (dict(z=Z), dict(idx=Z), dict(w=Z), dict(off=Z), dict(pos=Z), dict(T=20000, ws=Z)):
         assert _fwd(lib, **kw) == F.FP8_ERR_NULL, kw
     for kw in (dict(z=Z), dict(idx=Z), dict(dw=Z), dict(dz=Z)):
         assert _bwd(lib, **kw) == F.FP8_ERR_NULL, kw
     assert _bwd(lib, k=9) == F.FP8_ERR_SHAPE
-    for kw in (dict(idx=Z), dict(off=Z), dict(pos=Z), dict(T=4000, ws=Z)):
+    for kw in (dict(idx=Z), dict(off=Z), dict(pos=Z), dict(T=20000, ws=Z)):
         assert _plan(lib, **kw) == F.FP8_ERR_NULL, kw
-    assert _plan(lib, T=4000, ws=ctypes.c_void_p(0x100002)) == F.FP8_ERR_SHAPE
+    assert _plan(lib, T=20000, ws=ctypes.c_void_p(0x100002)) == F.FP8_ERR_SHAPE
 
 
 def test_workspace():
     w = F.fp8_route_workspace_bytes
-    assert w(0, 8, 2) == 0 and w(1024, 8, 2) == 0 and w(1025, 8, 2) == 2 * 8 * 4
+    assert w(0, 8, 2) == 0 and w(16384, 8, 2) == 0 and w(16385, 8, 2) == 17 * 8 * 4
     assert w(-1, 8, 2) == 0 and w(10000, 2000, 2) == 0
     for T in (1 << 10, 1 << 17, 1 << 20, 1 << 24):  # at most 512 chunks
         assert w(T, 256, 8) <= 512 * 256 * 4
