@@ -6,13 +6,18 @@ convergence-sanity workload, not a language model.
 
 The qkv, out, up and down projections are the interchangeable linears; the
 embedding, norms, attention and the vocabulary head stay in bf16 PyTorch.
-Attention runs only on the fused flash / memory-efficient backends."""
+Attention runs only on the fused flash / memory-efficient backends.  With
+experts, the up and down projections are those of a Mixture, and ``served``
+gives the model with its projections in 4-bit floating point or 8-bit
+integers."""
 
 from __future__ import annotations
 
 import torch
 
 from .autograd import Fp8Linear
+from .mixture import Mixture
+from .mx4 import Mx4GroupedLinear, Mx4Linear
 
 
 def attention_backends():
@@ -35,13 +40,16 @@ def fp8_linear(i, o, device):
 
 
 class Block(torch.nn.Module):
-    def __init__(self, d, heads, ffn, lin, device):
+    def __init__(self, d, heads, ffn, lin, device, experts=0, k=2):
         super().__init__()
         self.h = heads
         self.n1 = torch.nn.RMSNorm(d, dtype=torch.bfloat16, device=device)
         self.n2 = torch.nn.RMSNorm(d, dtype=torch.bfloat16, device=device)
         self.qkv, self.out = lin(d, 3 * d, device), lin(d, d, device)
-        self.up, self.down = lin(d, ffn, device), lin(ffn, d, device)
+        if experts:
+            self.mix = Mixture(d, ffn, experts, k, device=device)
+        else:
+            self.mix, self.up, self.down = None, lin(d, ffn, device), lin(ffn, d, device)
 
     def forward(self, x):
         B, T, d = x.shape
@@ -49,25 +57,43 @@ class Block(torch.nn.Module):
         a = torch.nn.functional.scaled_dot_product_attention(
             q.contiguous(), k.contiguous(), v.contiguous(), is_causal=True)
         x = x + self.out(a.transpose(1, 2).reshape(B, T, d))
+        if self.mix is not None:
+            return x + self.mix(self.n2(x))
         return x + self.down(torch.nn.functional.gelu(self.up(self.n2(x))))
 
 
 class Transformer(torch.nn.Module):
     def __init__(self, lin, layers=12, d=1024, heads=16, ffn=4096, vocab=32000, device="cuda",
-                 seed=0):
+                 seed=0, experts=0, k=2):
         super().__init__()
         torch.manual_seed(seed)
         self.emb = torch.nn.Embedding(vocab, d, dtype=torch.bfloat16, device=device)
-        self.blocks = torch.nn.ModuleList(Block(d, heads, ffn, lin, device) for _ in range(layers))
+        self.blocks = torch.nn.ModuleList(Block(d, heads, ffn, lin, device, experts, k)
+                                          for _ in range(layers))
         self.norm = torch.nn.RMSNorm(d, dtype=torch.bfloat16, device=device)
         self.head = torch.nn.Linear(d, vocab, bias=False, dtype=torch.bfloat16, device=device)
 
-    def loss(self, tok, tgt):
+    def logits(self, tok):
         x = self.emb(tok)
         for blk in self.blocks:
             x = blk(x)
-        logits = self.head(self.norm(x)).float()
+        return self.head(self.norm(x)).float()
+
+    def loss(self, tok, tgt):
+        logits = self.logits(tok)
         return torch.nn.functional.cross_entropy(logits.view(-1, logits.shape[-1]), tgt.view(-1))
+
+
+def served(model, linear=Mx4Linear, grouped=Mx4GroupedLinear):
+    """A trained Transformer, in place, with its projections quantized for
+    serving: linear and grouped are Mx4Linear and Mx4GroupedLinear, or
+    Int8Linear and Int8GroupedLinear.  It has no gradients any more."""
+    for blk in model.blocks:
+        for name in ("qkv", "out") + (("up", "down") if blk.mix is None else ()):
+            setattr(blk, name, linear.from_linear(getattr(blk, name)))
+        if blk.mix is not None:
+            blk.mix = blk.mix.served(grouped)
+    return model.requires_grad_(False)
 
 
 def synthetic_batch(batch, seq, vocab, device, seed=0):
