@@ -690,6 +690,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# the current device without torch.cuda's check that it is initialized: the
+# arguments are tensors there
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _arg_stream(stream, dev):
     if stream is None:
         return _raw_stream(dev.index)
@@ -705,7 +710,7 @@ def _run(name, args, dev):
     fn = _entry.get(name)
     if fn is None:
         fn = _entry[name] = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         st = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -983,25 +988,25 @@ def bind_fp8_mx4_dequantize(q, out, stream=None):
     return _bind_run("fp8_mx4_dequantize", *_mx4_dequantize_args(q, out, stream))
 
 
-def _mx4_args(x, w, bias, y, x4_out, sx_out, lead, bshape, dev):
+def _mx4_args(x, w, bias, y, x4_out, sx_out, lead, M, N, dev):
     """C arguments shared by the dense and the grouped call: x, its type and
     scales, w and its scales, bias, out dtype, y, x4_out, sx_out."""
-    N, k = w.codes.shape[-2], w.cols
+    k = w.cols
+    cb, sb = 16 * (-(-k // 32)), -(-k // 128)  # of a row, as _mx4_shapes has them
     if isinstance(x, QuantizedMx4):
-        M = _shape_of(x.codes, 2, "x.codes")[0]
         if x.cols != k:
             raise ValueError(f"x: rows of {x.cols} values, w has {k}")
         xp, xs = _mx4_pointers(x.codes, x.scale, "x", (), M, k, dev)
         dt, qp, sp = FP8_DT_MX4, None, None
     else:
-        M = _shape_of(x, 2, "x")[0]
         xp, xs, dt = _arg(x, "x", _HP, (M, k), dev), None, _TORCH_DT[x.dtype]
-        sc, ss = _mx4_shapes((), M, k)
-        qp, sp = _arg(x4_out, "x4_out", _U8, sc, dev), _arg(sx_out, "sx_out", _U8, ss, dev)
-    wp, wsp = _mx4_pointers(w.codes, w.scale, "w", lead, N, k, dev)
-    return (xp, dt, xs, wp, wsp, _arg(bias, "bias", _OUT16 if y is None else (y.dtype,), bshape, dev,
-                                      True),
-            _TORCH_DT.get(getattr(y, "dtype", None), -1), _arg(y, "y", _OUT16, (M, N), dev), qp, sp)
+        qp = _arg(x4_out, "x4_out", _U8, (M, cb), dev)
+        sp = _arg(sx_out, "sx_out", _U8, (sb, M, 4), dev)
+    yp = _arg(y, "y", _OUT16, (M, N), dev)
+    return (xp, dt, xs, _arg(w.codes, "w.codes", _U8, (*lead, N, cb), dev),
+            _arg(w.scale, "w.scale", _U8, (*lead, sb, N, 4), dev),
+            None if bias is None else _arg(bias, "bias", (y.dtype,), (*lead, N), dev),
+            _TORCH_DT[y.dtype], yp, qp, sp)
 
 
 def _mx4_linear_args(x, w, bias, y, x4_out, sx_out, stream):
@@ -1009,9 +1014,9 @@ def _mx4_linear_args(x, w, bias, y, x4_out, sx_out, stream):
         raise TypeError("w: expected a QuantizedMx4 operand")
     N = _shape_of(w.codes, 2, "w.codes")[0]
     xc = x.codes if isinstance(x, QuantizedMx4) else x
-    dev = _gpu_of(xc, "x")
     M = _shape_of(xc, 2, "x")[0]
-    return (M, N, w.cols, *_mx4_args(x, w, bias, y, x4_out, sx_out, (), (N,), dev),
+    dev = xc.device
+    return (M, N, w.cols, *_mx4_args(x, w, bias, y, x4_out, sx_out, (), M, N, dev),
             _arg_stream(stream, dev)), dev
 
 
@@ -1032,10 +1037,10 @@ def _mx4_grouped_args(x, w, bias, offsets, y, x4_out, sx_out, stream):
         raise TypeError("w: expected a QuantizedMx4 operand")
     E, N, _ = _shape_of(w.codes, 3, "w.codes")
     xc = x.codes if isinstance(x, QuantizedMx4) else x
-    dev = _gpu_of(xc, "x")
     T = _shape_of(xc, 2, "x")[0]
+    dev = xc.device
     return (T, E, N, w.cols, _arg(offsets, "offsets", _I32, (E + 1,), dev),
-            *_mx4_args(x, w, bias, y, x4_out, sx_out, (E,), (E, N), dev),
+            *_mx4_args(x, w, bias, y, x4_out, sx_out, (E,), T, N, dev),
             _arg_stream(stream, dev)), dev
 
 
@@ -1058,6 +1063,8 @@ def _arg_places(T, k, E, offsets, pos, ws, dev):
     """Pointers of a call that places rows: offsets, pos, workspace."""
     op = _arg(offsets, "offsets", _I32, (E + 1,), dev)
     pp = _arg(pos, "pos", _I32, (T, k), dev)
+    if ws is None:  # the library refuses it where it needs one
+        return op, pp, None
     need = fp8_route_workspace_bytes(T, E, k)
     if need == 0:
         return op, pp, None
