@@ -690,9 +690,16 @@ __global__ __launch_bounds__(kRThreads) void plan_count_kernel(PlanArgs a) {
   __shared__ int32_t h[kRouteMaxE + 1];
   for (int e = threadIdx.x; e <= a.E; e += kRThreads) h[e] = 0;
   __syncthreads();
-  const int j0 = blockIdx.x * a.chunk;
-  for (int j = j0 + threadIdx.x; j < min(j0 + a.chunk, a.n); j += kRThreads)
-    atomicAdd(&h[slot_expert(a, j)], 1);
+  const int j1 = min((int)(blockIdx.x + 1) * a.chunk, a.n);
+  constexpr int U = 8;  // loads in flight
+  for (int j = blockIdx.x * a.chunk + threadIdx.x; j < j1; j += U * kRThreads) {
+    int e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) e[u] = slot_expert(a, min(j + u * kRThreads, a.n - 1));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j + u * kRThreads < j1) atomicAdd(&h[e[u]], 1);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kRThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = h[e];
 }
@@ -728,22 +735,50 @@ FP8L_DEV void place_chunk(const PlanArgs& a, int block, int32_t* lds, F&& expert
   if (count_all)
     for (int i = tid; i < 2 * W; i += NT) all[i] = 0;
   __syncthreads();
-  if (count_all) {
-    constexpr int U = 8;  // loads in flight
-    for (int j0 = tid; j0 < a.n; j0 += U * NT) {
-      int e[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) e[u] = expert(min(j0 + u * NT, a.n - 1));
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j0 + u * NT < a.n) atomicAdd(&all[(j0 + u * NT < block * a.chunk ? 0 : W) + e[u]], 1);
-    }
-  }
-  // wave w's slots: the w-th part of the chunk
+  // wave w's slots: the w-th part of the chunk, steps of 64, U of them in flight
+  constexpr int U = 4;
   const int per = a.chunk / NW;
   const int j0 = block * a.chunk + wave * per, j1 = min(j0 + per, a.n);
   int32_t* const mine = next + wave * W;
-  for (int j = j0 + lane; j < j1; j += 64) atomicAdd(&mine[expert(j)], 1);
+  int slot[U];
+  auto load_slots = [&](int j) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = j + 64 * u + lane;
+      slot[u] = i < j1 ? expert(i) : a.E;
+    }
+  };
+  const int last = per > 0 ? (per - 1) / (64 * U) * (64 * U) : 0;
+  load_slots(j0 + last);
+  if (count_all) {
+    constexpr int Q = 8;  // loads of four slots in flight
+    typedef int32_t four __attribute__((ext_vector_type(4), aligned(4)));
+    const int before = block * a.chunk, quads = a.n / 4;  // (a chunk is a multiple of 4)
+    auto count = [&](int j, int e) {
+      atomicAdd(&all[(j < before ? 0 : W) + (e >= 0 && e < a.E ? e : a.E)], 1);
+    };
+    for (int q0 = tid; q0 < quads; q0 += Q * NT) {
+      four v[Q];
+#pragma unroll
+      for (int u = 0; u < Q; ++u)
+        v[u] = reinterpret_cast<const four*>(a.idx)[min(q0 + u * NT, quads - 1)];
+#pragma unroll
+      for (int u = 0; u < Q; ++u) {
+        const int q = q0 + u * NT;
+        if (q < quads)
+          for (int i = 0; i < 4; ++i) count(4 * q, v[u][i]);
+      }
+    }
+    if (tid < a.n % 4) count(4 * quads + tid, a.idx[4 * quads + tid]);
+  }
+  // from the last steps to the first, which stay for the places below
+  for (int j = j0 + last;; j -= 64 * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j + 64 * u + lane < j1) atomicAdd(&mine[slot[u]], 1);
+    if (j <= j0) break;
+    load_slots(j - 64 * U);
+  }
   __syncthreads();
   // first places of 256 experts at a time; SPLIT threads add up an expert's chunks
   int carry = 0;
@@ -810,15 +845,20 @@ FP8L_DEV void place_chunk(const PlanArgs& a, int block, int32_t* lds, F&& expert
     __syncthreads();
   }
   const int bits = 32 - __builtin_clz(a.E);
-  for (int j = j0 + lane; j - lane < j1; j += 64) {
-    const int e = j < j1 ? expert(j) : a.E;
-    const uint64_t peers = same_key(e, bits);
-    const int rank = __popcll(peers & ((1ull << lane) - 1));
-    const int at = mine[e] + rank;
-    wave_fence();
-    if (rank == 0) mine[e] += __popcll(peers);
-    wave_fence();
-    if (j < j1) a.pos[j] = e < a.E ? at : -1;
+  for (int jb = j0; jb < j1; jb += 64 * U) {
+    if (jb > j0) load_slots(jb);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (jb + 64 * u >= j1) break;
+      const int j = jb + 64 * u + lane, e = slot[u];
+      const uint64_t peers = same_key(e, bits);
+      const int rank = __popcll(peers & ((1ull << lane) - 1));
+      const int at = mine[e] + rank;
+      wave_fence();
+      if (rank == 0) mine[e] += __popcll(peers);
+      wave_fence();
+      if (j < j1) a.pos[j] = e < a.E ? at : -1;
+    }
   }
 }
 
