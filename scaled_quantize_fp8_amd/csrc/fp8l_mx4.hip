@@ -112,15 +112,17 @@ void launch_tile(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st
   }
 }
 
-// Waves that split K in a skinny launch of `waves` tile columns, doubled
-// while a wave has over 8 pieces (16 experts of 4096 -> 11008, one row each:
-// 64.9 us unsplit, 60.7 by two, 65.6 by four), or the chip has room for more
-// waves and each keeps its kU pieces in flight (one row, 11008 -> 4096: 50.8 us
-// unsplit, 10.5 by four, 8.2 by eight).
-int mx_split(int64_t waves, int64_t steps, int kU) {
+// Waves that split K in a skinny launch of `waves` tile columns: doubled while
+// the chip has room for more of them and each keeps two pieces (one row of
+// 11008 -> 4096 22.6 us unsplit, 8.6 by four, 7.6 by eight; 32 rows of 4096 ->
+// 32000, with 2000 tile columns, 13.6 unsplit, 14.8 by two); two of more than 8
+// pieces where columns wait in line (16 experts of 4096 -> 11008, one row
+// each: 53.2 unsplit, 49.5 by two, 50.9 by four).
+int mx_split(int64_t waves, int64_t steps) {
   const int64_t pieces = (steps + 1) / 2;
+  if (waves > 2048) return pieces > 8 ? 2 : 1;
   int kw = 1;
-  while (kw < 8 && (pieces > 8 * kw || (waves * kw < 8192 && pieces >= 2 * kU * kw))) kw *= 2;
+  while (kw < 8 && waves * kw <= 1536 && pieces >= 2 * kw) kw *= 2;
   return kw;
 }
 
@@ -131,7 +133,7 @@ bool mx_fits(int tile, int64_t T, int64_t E, int64_t N, int64_t K) {
   if (tile == kTile256x256w8) return grid_fits(most_units(T, E, 256) * n256, 512);
   const int mt = tile - kTileSkinny16 + 1;
   const int64_t units = most_units(T, E, 16 * mt), cols = (N + 15) / 16;
-  const int jw = 8 / mx_split(units * cols, mx_steps(K), mt == 1 ? MxSkinny<1>::kU : MxSkinny<2>::kU);
+  const int jw = 8 / mx_split(units * cols, mx_steps(K));
   return grid_fits(units * ((cols + jw - 1) / jw), 512);
 }
 
@@ -139,8 +141,11 @@ template <int MT>
 void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t st) {
   const int64_t units = gr ? most_units(gr->T, gr->E, 16 * MT) : (g.M + 16 * MT - 1) / (16 * MT);
   const int64_t cols = (g.N + 15) / 16;
-  const int kw = mx_split(units * cols, g.steps, MxSkinny<MT>::kU);
-  const int lds = kw > 1 ? MxSkinny<MT>::kLds : 0;
+  const int kw = mx_split(units * cols, g.steps);
+  const int lds = MxSkinny<MT>::kLds;
+  static std::atomic<bool> set_groups[64], set_dense[64];  // skinny_lds
+  set_lds_limit((const void*)mx4_skinny_groups_kernel<MT>, lds, set_groups);
+  set_lds_limit((const void*)mx4_skinny_kernel<MT>, lds, set_dense);
   g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
   if (gr)
     hipLaunchKernelGGL((mx4_skinny_groups_kernel<MT>),
@@ -151,18 +156,18 @@ void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t 
                        st, g, kw);
 }
 
-// Whether a call's blocks quantize its X themselves (MxFused).  Every 16
-// columns' block does all of it again, about 1 us for 8192 values, where the
-// launch that it saves takes 2 to 3 (bf16, us fused / in two launches: one row
-// of 4096 -> 11008 8.2 / 10.2, of 11008 -> 4096 9.5 / 11.6; four rows of 1536 ->
-// 6912 5.7 / 8.1, of 4096 -> 11008 10.9 / 10.7, of 11008 -> 4096 13.9 / 11.6).
-// Groups: two rows per expert on average (any unit may have 16, whose codes
-// must leave room for two blocks per CU; 24 rows, 64 experts of 1536 -> 6912
-// 21.5 / 26.8; 16 rows, 16 of 4096 -> 11008 60.1 / 64.9).  groups 0: dense.
+// Whether a call's blocks quantize its X themselves (MxFused).  Every block of
+// 16 columns or more does all of it again, where the launch that it saves takes
+// 2 to 3 us (bf16, us fused / in two launches: one row of 4096 -> 11008 6.6 /
+// 10.1, of 11008 -> 4096 8.0 / 10.0; four rows of 1536 -> 6912 4.5 / 7.1, of 4096
+// -> 11008 8.4 / 10.0, of 6912 -> 1536 7.5 / 8.0; eight of 4096 -> 11008 10.9 /
+// 10.1).  Groups: two rows per expert on average (any unit may have 16, whose
+// codes must leave room for two blocks per CU; 24 rows, 64 experts of 1536 ->
+// 6912 19.3 / 22.6; 16 rows, 16 of 4096 -> 11008 52.2 / 55.1).  groups 0: dense.
 bool fuse_x(const void* x, int32_t dt, int64_t rows, int64_t groups, int64_t N, int64_t K) {
   if (!is_hp(dt) || K == 0 || K % 8 != 0 || !aligned16(x) || forced_tile() != kTileAuto) return false;
   if (!mx_fits(kTileSkinny16, rows, groups ? groups : 1, N, K)) return false;
-  if (groups == 0) return rows == 1 ? K <= 16384 : rows <= 16 && rows * K <= 12288;
+  if (groups == 0) return rows <= 16 && rows * K <= 28672;
   return rows <= 2 * groups && K <= 4096;
 }
 
@@ -170,7 +175,7 @@ template <int IN>
 void launch_fused(MxArgs& g, const MxFusedX& fx, const Groups* gr, const MxStrides& s,
                   hipStream_t st) {
   const int64_t units = gr ? most_units(gr->T, gr->E, 16) : 1, cols = (g.N + 15) / 16;
-  const int kw = mx_split(units * cols, g.steps, MxSkinny<1>::kU);
+  const int kw = mx_split(units * cols, g.steps);
   const int lds = MxFused<IN>::lds(gr ? 16 : (int)g.M, g.ld, g.steps);
   g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
   if (gr)
@@ -184,9 +189,10 @@ void launch_fused(MxArgs& g, const MxFusedX& fx, const Groups* gr, const MxStrid
 
 // Microseconds of the kernels, from fits to a sweep of 8 to 8192 rows over six
 // layer shapes, dense and in 8 and 64 groups; `steps` of 128 values of K.
-//   skinny, 16 / 32 / 48 / 64 rows a unit: 4 + units N K (1.05 / 1.86 / 2.42 /
-//     3.2) 1e-7: 17 rows of 4096 -> 11008 10.1 (12.4), 64 18.2 (18.4), of 11008
-//     -> 4096 16.6 (18.4); 32 rows in 64 groups of 4096 -> 11008 115 (122)
+//   skinny, 16 / 32 / 48 / 64 rows a unit: 4 + units N K (0.72 / 0.85 / 1.15 /
+//     1.45) 1e-7: 32 rows of 4096 -> 11008 8.8 (7.8), 64 12.1 (10.5), 128 19.7
+//     (17.1), 192 26.2 (23.6); 64 of 11008 -> 4096 10.3 (10.5); 64 rows in 64
+//     groups of 1536 -> 6912 30.3 (34.7)
 //   128x256, one block per CU: 5.5 + 0.635 steps: K = 1536 / 4096 / 11008 13.6 /
 //     26.5 / 60 (13.1 / 25.8 / 60.1); two blocks per CU: a full round of 512
 //     tiles takes 1.4 steps, fewer tiles at least 0.8 of it: 688 tiles of
@@ -201,7 +207,7 @@ int mx_tile(int64_t rows, int64_t E, int64_t N, int64_t K) {
       mx_fits(f, rows, E, N, K))
     return f;
   const double cus = cu_count(), steps = (double)mx_steps(K), nk = (double)N * (double)K;
-  const double per[4] = {1.05e-7, 1.86e-7, 2.42e-7, 3.2e-7};
+  const double per[4] = {0.72e-7, 0.85e-7, 1.15e-7, 1.45e-7};
   int best = 0;
   double us = 1e300;
   auto offer = [&](int tile, double t) {

@@ -229,6 +229,17 @@ FP8L_DEV void mx_move(MxArgs& g, int64_t row, int64_t rows, int64_t col) {
   if (g.bias) g.bias += col;
 }
 
+// A descriptor of values that all lanes hold alike, in scalar registers from the
+// start: what a division left in vector registers the compiler would otherwise
+// bring over again in a loop around every load.
+FP8L_DEV __amdgpu_buffer_rsrc_t mx_rsrc(const void* p, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return make_rsrc(reinterpret_cast<const void*>((uint64_t)hi << 32 | lo),
+                   __builtin_amdgcn_readfirstlane((uint32_t)bytes));
+}
+
 FP8L_DEV float mx_half(const MxArgs& g, uint32_t h) {
   return g.out_f16 ? f16_to_f32(h) : bf16_to_f32(h);
 }
@@ -239,24 +250,119 @@ FP8L_DEV uint2 mx_pack4(const MxArgs& g, const float v[4]) {
   return make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
 }
 
-// Few rows (decoding): as the other formats' skinny kernels, a wave reads 16
-// rows of W straight into MFMA operands, no LDS and no barrier in the loop;
-// KW waves of a block share a tile column and split K, their partial sums
-// meet in LDS in wave order.  The 16x16x128 MFMA takes a block of 32 values
-// and its scale per lane (lane q 16 + r: row r, block q of the step).  A piece
-// is two steps: 128 bytes, a whole line, of every row.
-template <int MT>
-struct MxSkinny {
-  static constexpr int kBM = 16 * MT, kWaveN = 16, kThreads = 512, kLds = 8 * MT * 1024;
-  // Pieces in flight per wave.  More of them cost the registers of more waves:
-  // one row of 4096 -> 11008 with 1 / 2 / 4 pieces: 7.9 / 7.8 / 8.1 us; 33 rows
-  // 13.0 / 13.6 / 15.8; 64 rows of 11008 -> 4096 16.4 / 17.6 / 20.7.
-  static constexpr int kU = MT == 1 ? 2 : 1;
+// A wave's way of reading MFMA operands: 16 rows of W and 16 NX of X, a piece
+// (two steps: 128 bytes, a whole line, of every row) at a time.  The 16x16x128
+// MFMA takes a block of 32 values and its scale per lane (lane 16 q + r: row r,
+// block q of the step), so lanes side by side want different rows: loaded that
+// way, a load of 64 x 16 bytes keeps the address unit busy for 64 clocks.  Here
+// eight lanes load a row's line (16 clocks), and the wave turns it round in its
+// own part of LDS, without a barrier: 33 rows of 11008 -> 4096 9.4 us against
+// 11.8, 16 rows 7.4 against 9.6, 512 rows in 16 experts of 1536 -> 6912 21.9
+// against 45.2.
+template <int NX>
+struct MxPieces {
+  static constexpr int kOperands = 1 + NX;   // 0: W, 1 + m: X's rows from 16 m on
+  static constexpr int kPiece = 2048 + 128;  // bytes of codes [16][128], scale words [2][16]
+  // LDS holds W and two of X at a time: all five of 64 rows would leave room for
+  // one block per CU (64 rows of 4096 -> 11008 15.3 us, so 12.0).
+  static constexpr int kPlaces = kOperands < 3 ? kOperands : 3, kWave = kPlaces * kPiece;
+  struct Regs {
+    v4i c[kOperands][2];
+    uint32_t e[1 + (NX + 1) / 2];
+  };
+  __amdgpu_buffer_rsrc_t rb, rsb, ra, rsa;
+  uint32_t ld, sb_step, sa_step, steps, j0;
+  uint8_t* mine;
 
-  FP8L_DEV static v8i load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    const v4i a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+  // j0: the wave's first column from g's on, of cols in reach.
+  FP8L_DEV MxPieces(const MxArgs& g, uint32_t j0, int64_t cols, uint8_t* mine)
+      : rb(mx_rsrc(g.b, cols * g.ld)),
+        // words of rows past the end are those of other rows, or zeros past the
+        // last step: they meet zero codes or columns that are not stored
+        rsb(mx_rsrc(g.sb, ((int64_t)(g.steps - 1) * g.sb_step + cols) * 4)),
+        ra(mx_rsrc(g.a, NX ? g.M * g.ld : 0)),
+        rsa(mx_rsrc(g.sa, NX ? ((int64_t)(g.steps - 1) * g.sa_step + g.M) * 4 : 0)),
+        ld((uint32_t)g.ld), sb_step((uint32_t)g.sb_step), sa_step((uint32_t)g.sa_step),
+        steps((uint32_t)g.steps), j0(j0), mine(mine) {}
+
+  // Piece p, zeros past the last block.
+  FP8L_DEV void load(Regs& t, uint32_t p) const {
+    constexpr uint32_t kNowhere = 0x80000000u;
+    const uint32_t lane = threadIdx.x & 63, row = lane >> 3, k = 128 * p + 16 * (lane & 7);
+#pragma unroll
+    for (int o = 0; o < kOperands; ++o)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = (o ? 16 * (o - 1) : j0) + 8 * j + row;
+        t.c[o][j] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(o ? ra : rb, k < ld ? at * ld + k : kNowhere,
+                                                       0, 0));
+      }
+    const uint32_t s = 2 * p + (lane >> 4 & 1), r = lane & 15, half = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < 1 + (NX + 1) / 2; ++i) {
+      const uint32_t m = 2 * (i - 1) + half;  // of X
+      const bool in = s < steps && (i ? m < NX : half == 0);
+      const uint32_t at = i ? s * sa_step + 16 * m + r : s * sb_step + j0 + r;
+      t.e[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(i ? rsa : rsb, in ? 4 * at : kNowhere,
+                                                              0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // 16-byte chunk of a row's line: rows that are read together spread over the banks.
+  FP8L_DEV static uint32_t chunk(uint32_t row, uint32_t c) {
+    return 128 * row + 16 * (c ^ (row & 7));
+  }
+
+  // W to place 0; rows 16 m to 16 m + 32 of X to places 1 and 2 (m even).
+  FP8L_DEV void put_w(const Regs& t) const {
+    const uint32_t lane = threadIdx.x & 63;
+    put_codes(t, 0, 0);
+    if (lane < 32) *reinterpret_cast<uint32_t*>(mine + 2048 + 4 * lane) = t.e[0];
+    asm volatile("" ::: "memory");  // other lanes' bytes are read next
+  }
+  FP8L_DEV void put_x(const Regs& t, int m) const {
+    const uint32_t lane = threadIdx.x & 63, half = lane >> 5;
+    asm volatile("" ::: "memory");  // what lay there has been read
+    put_codes(t, 1 + m, 1);
+    if (m + 1 < NX) put_codes(t, 2 + m, 2);
+    if (m + 1 < NX || half == 0)
+      *reinterpret_cast<uint32_t*>(mine + (1 + half) * kPiece + 2048 + 4 * (lane & 31)) =
+          t.e[1 + m / 2];
+    asm volatile("" ::: "memory");
+  }
+  FP8L_DEV void put_codes(const Regs& t, int o, int place) const {
+    const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<v4i*>(mine + place * kPiece + chunk(8 * j + (lane >> 3), lane & 7)) =
+          t.c[o][j];
+  }
+
+  // The operand at a place, of step 2 p + u; a block past the last has zeros for
+  // a scale too.
+  FP8L_DEV v8i codes(int place, int u) const {
+    const uint32_t r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+    const v4i a = *reinterpret_cast<const v4i*>(mine + place * kPiece + chunk(r, 4 * u + q));
     return v8i{a.x, a.y, a.z, a.w, 0, 0, 0, 0};
   }
+  FP8L_DEV uint32_t scale(int place, int u, uint32_t p) const {
+    const uint32_t r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+    const uint32_t e = mine[place * kPiece + 2048 + 4 * (16 * u + r) + q];
+    return 128 * p + 64 * u + 16 * q < ld ? e : 0;
+  }
+};
+
+// Few rows (decoding): a wave multiplies 16 columns by all rows; KW waves of a
+// block share a tile column and split K, their partial sums meet in LDS in wave
+// order.
+template <int MT>
+struct MxSkinny {
+  using P = MxPieces<MT>;
+  static constexpr int kBM = 16 * MT, kWaveN = 16, kThreads = 512, kLds = 8 * P::kWave;
+  static_assert(kLds >= 8 * MT * 1024, "partial sums");
+
   FP8L_DEV static v4f mma(v8i b, v8i a, v4f c, uint32_t sb, uint32_t sa) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 4, 4, 0, (int)sb, 0, (int)sa);
   }
@@ -307,75 +413,38 @@ struct MxSkinny {
     }
   }
 
-  // A piece of W for the wave's 16 columns: two steps' codes and scale words.
-  struct Piece {
-    v8i b[2];
-    uint32_t e[2];
-  };
-  struct W {
-    __amdgpu_buffer_rsrc_t codes, scales;
-    uint32_t row, word;  // this lane's row: bytes of codes, words of scales
-    FP8L_DEV W(const MxArgs& g, int j0, int JW) {
-      const int cols = (int)min<int64_t>(g.N, JW * kWaveN);  // rows of W in reach
-      const int r = threadIdx.x & 15;
-      codes = make_rsrc(g.b, (uint32_t)(cols * g.ld));
-      // words of rows past the end are those of other rows, or zeros past the
-      // last step: they meet zero codes or columns that are not stored
-      scales = make_rsrc(g.sb, (uint32_t)(((int64_t)(g.steps - 1) * g.sb_step + cols) * 4));
-      row = (uint32_t)((j0 + r) * g.ld);
-      word = (uint32_t)(j0 + r);
-    }
-    // pieces p, p + KW, ..
-    FP8L_DEV void load(const MxArgs& g, uint32_t p, int KW, Piece (&out)[kU]) const {
-      const uint32_t q = (threadIdx.x & 63) >> 4;
-#pragma unroll
-      for (int u = 0; u < 2 * kU; ++u) {
-        const uint32_t s = 2 * (p + (u >> 1) * KW) + (u & 1), k = s * 64 + 16 * q;
-        const bool in = k < (uint32_t)g.ld;  // blocks and steps past the last: zeros
-        out[u >> 1].b[u & 1] = load16(codes, in ? row + k : 0x80000000u);
-        out[u >> 1].e[u & 1] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-            scales, in ? (s * (uint32_t)g.sb_step + word) * 4 : 0x80000000u, 0, 0);
-      }
-    }
-  };
-
   // g: moved to the tile's rows (at most kBM) and the block's first column.
   FP8L_DEV static void run(const MxArgs& g, int KW, uint8_t* smem) {
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
-    const W w(g, jw * kWaveN, JW);
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.M * g.ld));
-    const __amdgpu_buffer_rsrc_t rsa =
-        make_rsrc(g.sa, (uint32_t)(((int64_t)(g.steps - 1) * g.sa_step + g.M) * 4));
-    const uint32_t ld = (uint32_t)g.ld;
+    const P w(g, jw * kWaveN, min<int64_t>(g.N, JW * kWaveN), smem + wave * P::kWave);
     v4f acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const uint32_t pieces = ((uint32_t)g.steps + 1) / 2;
-    for (uint32_t p = kw; p < pieces; p += KW * kU) {
-      Piece piece[kU];
-      w.load(g, p, KW, piece);
-      v8i fa[2 * kU][MT];
-      uint32_t ea[2 * kU][MT];
+    // one piece on its way while the last is multiplied (two or three cost the
+    // registers of other waves: 16 rows of 11008 -> 4096 6.9 us, 7.9, 7.9)
+    typename P::Regs t;
+    w.load(t, kw);
+    for (uint32_t p = kw; p < pieces; p += KW) {
+      w.put_w(t);
+      v8i b[2];
+      uint32_t eb[2];
 #pragma unroll
-      for (int u = 0; u < 2 * kU; ++u) {
-        const uint32_t s = 2 * (p + (u >> 1) * KW) + (u & 1), k = s * 64 + 16 * q;
-        const bool in = k < ld;
+      for (int m = 0; m < MT; m += 2) {
+        w.put_x(t, m);
+        if (m + 2 >= MT) w.load(t, p + KW);  // past the last: zeros
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          fa[u][m] = load16(ra, in ? (uint32_t)(16 * m + r) * ld + k : 0x80000000u);
-          ea[u][m] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-              rsa, in ? (s * (uint32_t)g.sa_step + 16 * m + r) * 4 : 0x80000000u, 0, 0);
+        for (int u = 0; u < 2; ++u) {
+          if (m == 0) b[u] = w.codes(0, u), eb[u] = w.scale(0, u, p);
+#pragma unroll
+          for (int i = 0; i < 2 && m + i < MT; ++i)
+            acc[m + i] = mma(b[u], w.codes(1 + i, u), acc[m + i], eb[u], w.scale(1 + i, u, p));
         }
       }
-#pragma unroll
-      for (int u = 0; u < 2 * kU; ++u)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          acc[m] = mma(piece[u >> 1].b[u & 1], fa[u][m], acc[m], piece[u >> 1].e[u & 1] >> (8 * q),
-                       ea[u][m] >> (8 * q));
+      asm volatile("" ::: "memory");  // before the next piece is put there
     }
+    if (KW > 1) __syncthreads();  // the partial sums take the pieces' place
     finish(g, acc, KW, smem);
   }
 };
@@ -396,10 +465,12 @@ struct MxFusedX {
 template <int IN>
 struct MxFused {
   using S = MxSkinny<1>;
-  static constexpr int kU = S::kU, kSize = IN == kInF32 ? 4 : 2;
-  // LDS: partial sums, scale words [steps][rows], codes [rows][ld]
+  using P = MxPieces<0>;
+  static constexpr int kSize = IN == kInF32 ? 4 : 2, kOwn = 8 * P::kWave;
+  static_assert(kOwn >= 8 * 1024, "partial sums");
+  // LDS: pieces, then partial sums; scale words [steps][rows]; codes [rows][ld]
   static int lds(int rows, int64_t ld, int64_t steps) {
-    return S::kLds + (int)(((steps * rows * 4 + 15) & ~15LL) + rows * ld);
+    return kOwn + (int)(((steps * rows * 4 + 15) & ~15LL) + rows * ld);
   }
 
   // g, fx: moved to the tile's rows (at most 16) and the block's first column.
@@ -408,11 +479,11 @@ struct MxFused {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int jw = wave / KW, kw = wave % KW, JW = 8 / KW;
     const int j0 = jw * S::kWaveN, rows = (int)g.M;
-    const typename S::W w(g, j0, JW);
-    typename S::Piece piece[kU];
-    w.load(g, kw, KW, piece);
-    uint32_t* const xe = reinterpret_cast<uint32_t*>(smem + S::kLds);
-    uint8_t* const xc = smem + S::kLds + ((g.steps * rows * 4 + 15) & ~15);
+    const P w(g, j0, min<int64_t>(g.N, JW * S::kWaveN), smem + wave * P::kWave);
+    typename P::Regs t;
+    w.load(t, kw);
+    uint32_t* const xe = reinterpret_cast<uint32_t*>(smem + kOwn);
+    uint8_t* const xc = smem + kOwn + ((g.steps * rows * 4 + 15) & ~15);
     const uint32_t ld = (uint32_t)g.ld, K = (uint32_t)fx.K;
     // 16 lanes a step of 128 values, as in the quantize kernel
     const int sl = threadIdx.x & 15;
@@ -438,20 +509,21 @@ struct MxFused {
     const int rr = min(r, rows - 1);
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
     const uint32_t pieces = ((uint32_t)g.steps + 1) / 2;
-    for (uint32_t p = kw; p < pieces; p += KW * kU) {
-      if (p != (uint32_t)kw) w.load(g, p, KW, piece);
+    for (uint32_t p = kw; p < pieces; p += KW) {
+      w.put_w(t);
+      w.load(t, p + KW);
 #pragma unroll
-      for (int u = 0; u < 2 * kU; ++u) {
-        const int s = 2 * (p + (u >> 1) * KW) + (u & 1);
+      for (int u = 0; u < 2; ++u) {
+        const int s = 2 * p + u;
         if (s >= g.steps) continue;
         const uint32_t k = 64 * s + 16 * q;
         const v4i a = *reinterpret_cast<const v4i*>(xc + rr * ld + (k < ld ? k : 0));
-        const uint32_t ea = xe[s * rows + rr];
         const v8i fa = {a.x, a.y, a.z, a.w, 0, 0, 0, 0};
-        acc = S::mma(piece[u >> 1].b[u & 1], fa, acc, piece[u >> 1].e[u & 1] >> (8 * q),
-                     ea >> (8 * q));
+        acc = S::mma(w.codes(0, u), fa, acc, w.scale(0, u, p), xe[s * rows + rr] >> (8 * q));
       }
+      asm volatile("" ::: "memory");
     }
+    if (KW > 1) __syncthreads();
     const v4f sums[1] = {acc};
     S::finish(g, sums, KW, smem);
   }

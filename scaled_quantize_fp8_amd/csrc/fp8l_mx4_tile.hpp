@@ -158,7 +158,7 @@ struct MxTile {
       const uint32_t bytes =
           kt < g.steps && c < (kBM + kBN) / 64 ? (uint32_t)(4 * n) : 0u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          make_rsrc(p, __builtin_amdgcn_readfirstlane(bytes)),
+          mx_rsrc(p, bytes),
           (__attribute__((address_space(3))) void*)(step_buf(kt) + kCodes + 256 * c), 4,
           4u * (first + lane), 0, 0, 0);
     };
@@ -185,7 +185,7 @@ struct MxTile {
     const bool staged = g.bias && ((uintptr_t)g.bias & 3) == 0 && (cols & 1) == 0;
     if (staged && wv < 2)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          make_rsrc(g.bias, (uint32_t)(2 * cols)),
+          mx_rsrc(g.bias, 2 * cols),
           (__attribute__((address_space(3))) void*)(smem + kBiasOff + 256 * wv), 4,
           256u * wv + 4u * lane, 0, 0, 0);
     for (int s = 0; s < kStages && s <= nk; ++s) issue_step(s);
@@ -215,8 +215,8 @@ struct MxTile {
 
     // Step kt: on entry the products of A fragments 0 and 1 of step kt are issued;
     // fa, ea hold step kt's A fragments, fb[CUR], eb[CUR] its B fragments.
-    const __amdgpu_buffer_rsrc_t ra_all = make_rsrc(g.a, a_bytes);
-    const __amdgpu_buffer_rsrc_t rb_all = make_rsrc(g.b, b_bytes);
+    const __amdgpu_buffer_rsrc_t ra_all = mx_rsrc(g.a, a_bytes);
+    const __amdgpu_buffer_rsrc_t rb_all = mx_rsrc(g.b, b_bytes);
     auto kstep_body = [&](int kt, auto cur_tag, auto fast_tag) {
       constexpr int CUR = decltype(cur_tag)::value, NXT = CUR ^ 1;
       constexpr bool FAST = decltype(fast_tag)::value;
