@@ -151,10 +151,10 @@ int fp8_route_fwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t d
           if (offsets && T <= kRoutePlaceRows) {
             const PlanArgs p = {idx, offsets, pos, nullptr, (int32_t)(T * k), E, kPlaceThreads, 1};
             static std::atomic<bool> lds_set[64];
-            set_lds_limit((const void*)route_place_kernel<IN, V>, route_place_lds<V>(256, true),
+            set_lds_limit((const void*)route_place_kernel<IN, V>, route_place_lds<V>(256),
                           lds_set);
             hipLaunchKernelGGL((route_place_kernel<IN, V>), dim3(1), dim3(kPlaceThreads),
-                               route_place_lds<V>(E, !a.lanes), stream, a, p);
+                               route_place_lds<V>(E), stream, a, p);
             placed = true;
             return;
           }

@@ -42,7 +42,7 @@ struct RouteArgs {
   int32_t T, E, k, score, groups, kept, group_top, renorm;
   float scale;
   int32_t vec;    // a lane's experts by wide loads
-  int32_t lanes;  // lanes of a group for the choice in 32 bits, 0: not that way
+  int32_t lanes;  // lanes of a group where 16 hold a row, 0: groups end inside a lane
 };
 
 // ---------------------------------------------------------------- lanes
@@ -127,48 +127,103 @@ FP8L_DEV void strike(S (&c)[V], int sl, int at) {
 }
 
 // LDS of one row: its scores, then the marks of the kept groups.
-template <int L, int V>
-constexpr int route_row_lds() { return L * V * 9; }
+template <int L, int V, class S>
+constexpr int group_lds() { return L * V * ((int)sizeof(S) + 1); }
 
 // c of the experts in groups that are not kept becomes -inf.  g: the values
-// that the groups are scored by.
+// that the groups are scored by.  Any groups: a lane reads a group's values
+// from LDS.  The smallest score of a kept group and the largest of the others.
 template <int L, int V, class S>
-FP8L_DEV void keep_groups(const RouteArgs& a, S (&c)[V], const S (&g)[V], int sl, uint8_t* row) {
+FP8L_DEV void keep_groups(const RouteArgs& a, S (&c)[V], const S (&g)[V], int sl, uint8_t* row,
+                          S& least, S& best) {
   S* const sc = reinterpret_cast<S*>(row);
-  uint8_t* const mark = row + L * V * 8;
+  uint8_t* const mark = row + L * V * sizeof(S);
   const int n = a.E / a.groups;
 #pragma unroll
   for (int v = 0; v < V; ++v) sc[sl * V + v] = g[v];
   wave_fence();
-  S gs[V];
+  S gs[V], left[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {  // neighbouring lanes take neighbouring groups
+    if (v * L >= a.groups) break;
+    const int q = v * L + sl;
+    if (q >= a.groups) continue;
+    S hi = -(S)INFINITY, lo = -(S)INFINITY;
+#pragma unroll 4
+    for (int i = q * n; i < q * n + n; ++i) {
+      const S x = sc[i];
+      lo = max(lo, min(hi, x));
+      hi = max(hi, x);
+    }
+    gs[v] = a.group_top == 2 && lo > -(S)INFINITY ? hi + lo : hi;
+  }
+  wave_fence();
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (v * L + sl < a.groups) sc[v * L + sl] = gs[v];
+  wave_fence();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int q = sl * V + v;
-    gs[v] = -(S)INFINITY;
-    if (q < a.groups) {
-      S hi = -(S)INFINITY, lo = -(S)INFINITY;
-      for (int i = q * n; i < q * n + n; ++i) {
-        const S x = sc[i];
-        if (x > hi) lo = hi, hi = x;
-        else if (x > lo) lo = x;
-      }
-      gs[v] = a.group_top == 2 && lo > -(S)INFINITY ? hi + lo : hi;
-    }
+    left[v] = gs[v] = q < a.groups ? sc[q] : -(S)INFINITY;
     mark[q] = 0;
   }
   wave_fence();
   for (int i = 0; i < a.kept; ++i) {
     int at;
-    if (row_best<L>(gs, sl, at) > -(S)INFINITY && at / V == sl) mark[at] = 1;
-    strike(gs, sl, at);
+    if (row_best<L>(left, sl, at) > -(S)INFINITY && at / V == sl) mark[at] = 1;
+    strike(left, sl, at);
   }
   wave_fence();
+  least = (S)INFINITY, best = -(S)INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = sl * V + v;
+    const int q = sl * V + v, e = q;
+    if (q < a.groups) {
+      if (mark[q]) least = min(least, gs[v]);
+      else best = max(best, gs[v]);
+    }
     if (e < a.E && !mark[e / n]) c[v] = -(S)INFINITY;
   }
   wave_fence();
+}
+
+// Score of this lane's group of `lanes` (2^j) lanes, whose experts they hold.
+template <int L, int V, class S>
+FP8L_DEV S lane_group(const RouteArgs& a, const S (&g)[V], int lanes) {
+  S hi = -(S)INFINITY, lo = -(S)INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lo = max(lo, min(hi, g[v]));
+    hi = max(hi, g[v]);
+  }
+  lane_steps<L>([&](auto s) {
+    constexpr int STEP = decltype(s)::value;
+    if (STEP < lanes) {
+      const S oh = lane_step<STEP>(hi), ol = lane_step<STEP>(lo);
+      lo = max(min(hi, oh), max(lo, ol));
+      hi = max(hi, oh);
+    }
+  });
+  return a.group_top == 2 && lo > -(S)INFINITY ? hi + lo : hi;
+}
+
+// The same where 64 lanes hold a row and `lanes` (2^j) of them a group.
+template <int V>
+FP8L_DEV void keep_groups_wide(const RouteArgs& a, double (&c)[V], const double (&g)[V], int lane,
+                               int lanes) {
+  const double mark = lane_group<64>(a, g, lanes);
+  const uint64_t u = (uint64_t)__double_as_longlong(mark);
+  const int grp = lane / lanes;
+  int ahead = 0;  // better groups
+  for (int q = 0; q < a.groups; ++q) {
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, q * lanes);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), q * lanes);
+    const double o = __longlong_as_double((long long)(lo | hi << 32));
+    ahead += o > mark || (o == mark && q < grp) ? 1 : 0;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) c[v] = ahead < a.kept ? c[v] : -(double)INFINITY;
 }
 
 template <int N>
@@ -198,57 +253,42 @@ FP8L_DEV void other_lanes(F&& f) {
 // lanes and groups of 2^j lanes (RouteArgs::lanes): every lane ranks its group
 // among those of the other lanes.  g: what groups are scored by.  Whether the
 // group stays, and its score, for the caller's proof.
-template <int V, class S>
-FP8L_DEV bool keep_groups_lanes(const RouteArgs& a, S (&c)[V], const S (&g)[V], int sl, S& mark) {
-  S hi = -(S)INFINITY, lo = -(S)INFINITY;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    lo = max(lo, min(hi, g[v]));
-    hi = max(hi, g[v]);
-  }
-  lane_steps<16>([&](auto s) {
-    constexpr int STEP = decltype(s)::value;
-    if (STEP < a.lanes) {
-      const S oh = lane_step<STEP>(hi), ol = lane_step<STEP>(lo);
-      lo = max(min(hi, oh), max(lo, ol));
-      hi = max(hi, oh);
-    }
-  });
-  mark = a.group_top == 2 && lo > -(S)INFINITY ? hi + lo : hi;
+template <int V>
+FP8L_DEV bool keep_groups_lanes(const RouteArgs& a, float (&c)[V], const float (&g)[V], int sl,
+                                float& mark) {
+  mark = lane_group<16>(a, g, a.lanes);
   const int grp = sl / a.lanes;
   int ahead = 0;  // lanes of better groups
   other_lanes([&](auto n) {
     constexpr int N = decltype(n)::value;
-    const S o = turn_lane<N>(mark);
+    const float o = turn_lane<N>(mark);
     const int og = turn_lane<N>(grp);
     ahead += o > mark || (o == mark && og < grp) ? 1 : 0;
   });
   const bool in = ahead < a.kept * a.lanes;
 #pragma unroll
-  for (int v = 0; v < V; ++v) c[v] = in ? c[v] : -(S)INFINITY;
+  for (int v = 0; v < V; ++v) c[v] = in ? c[v] : -INFINITY;
   return in;
 }
 
-// The scores p of a row in S; m: its largest logit.
+// The scores p of a row in S; m: its largest logit.  (Both kinds share the
+// exponential's and the division's code, whose fetch is much of what a rare row
+// costs.)
 template <int L, int V, class S>
 FP8L_DEV void row_scores(const RouteArgs& a, const float (&z)[V], float m, S (&p)[V]) {
-  if (a.score == kSigmoid) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p[v] = (S)1 / ((S)1 + exp(-(S)z[v]));
-    return;
-  }
+  const bool sig = a.score == kSigmoid;
   S sum = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    p[v] = exp((S)z[v] - (S)m);
+    p[v] = exp(sig ? -(S)z[v] : (S)z[v] - (S)m);
     sum += p[v];
   }
   sum = lanes_sum<L>(sum);
 #pragma unroll
-  for (int v = 0; v < V; ++v) p[v] = p[v] / sum;
+  for (int v = 0; v < V; ++v) p[v] = (sig ? (S)1 : p[v]) / (sig ? (S)1 + p[v] : sum);
 }
 
-// The chosen experts of a row: slot i's in lane i (-1: none).
+// The chosen experts of a row, of scores in S: slot i's in lane i (-1: none).
 template <int L, int V, class S>
 FP8L_DEV int choose(const RouteArgs& a, const float (&z)[V], const float (&b)[V], float m, int sl,
                     uint8_t* row) {
@@ -264,9 +304,9 @@ FP8L_DEV int choose(const RouteArgs& a, const float (&z)[V], const float (&b)[V]
     c[v] = a.bias ? g[v] : (S)z[v];
   }
   if (a.groups > 1 && a.kept < a.groups) {
-    S mark;
-    if (L == 16 && a.lanes) keep_groups_lanes<V, S>(a, c, g, sl, mark);
-    else keep_groups<L>(a, c, g, sl, row);
+    S least, best;
+    if (a.lanes) keep_groups_wide(a, c, g, sl, V > 1 ? 4 * a.lanes : a.E / a.groups);
+    else keep_groups<L>(a, c, g, sl, row, least, best);
   }
   int mine = -1;
   for (int i = 0; i < a.k; ++i) {
@@ -326,13 +366,15 @@ FP8L_DEV float slot_weight(const RouteArgs& a, const float (&z)[V], float m, boo
 //            set is right if every chosen c is larger, and the order if they
 //            are further apart than their errors.  If not, the same in 64 bits,
 //            where the order is also mended.
-//   errors   a score in 32 bits is off by less than (|x| + 24) 2^-23 of itself,
+//   errors   a score in 32 bits is off by less than (|x| + n) 2^-23 of itself,
 //            x its exponential's argument (rounded to 2^-24, and by the factor
-//            log2 e; the rest for exp, reciprocal and the softmax's sum: 20
-//            additions, and its terms' |x|, whose mean is at most log E).
-//   groups   scored in 32 bits; right if the least kept and the best dropped
-//            group are further apart than the scores' errors.
-//   else     the wave does its rows again in 64 bits.
+//            log2 e); n = 4 for exp (1), 1 + exp (1/2) and reciprocal (1) of a
+//            sigmoid, 24 with a softmax's sum: 20 additions, and its terms' |x|,
+//            whose mean is at most log E.
+//   groups   scored in 32 bits, in lanes or, where groups end inside a lane, from
+//            LDS; right if the least kept and the best dropped group are further
+//            apart than the scores' errors.
+//   else     the wave does the row again in 64 bits, with all of its lanes.
 //
 // One row per 16 lanes, V experts per lane.
 
@@ -355,16 +397,23 @@ FP8L_DEV double next_lane(double v) {
   return __longlong_as_double((long long)(lo | (hi << 32)));
 }
 
-// The same in 32 bits; false where that cannot tell which groups stay.  err:
+// The groups in 32 bits; false where that cannot tell which ones stay.  err:
 // the largest error of a group's score (< 0: none).
 template <int V>
 FP8L_DEV bool keep_groups32(const RouteArgs& a, float (&c)[V], const float (&g)[V], int sl,
-                            float err) {
-  float mark;
-  const bool in = keep_groups_lanes<V, float>(a, c, g, sl, mark);
+                            uint8_t* row, float err) {
+  float least, best;
+  if (a.lanes) {
+    float mark;
+    const bool in = keep_groups_lanes<V>(a, c, g, sl, mark);
+    least = in ? mark : INFINITY;
+    best = in ? -INFINITY : mark;
+  } else {
+    keep_groups<16>(a, c, g, sl, row, least, best);
+  }
   if (err < 0.0f) return true;
-  const float least = -lanes_max<16>(in ? -mark : -INFINITY);
-  const float best = lanes_max<16>(in ? -INFINITY : mark);
+  least = -lanes_max<16>(-least);
+  best = lanes_max<16>(best);
   return best == -INFINITY || least - best > 2.0f * err + 0x1p-21f * (fabsf(least) + fabsf(best));
 }
 
@@ -379,15 +428,16 @@ FP8L_DEV float score32(const RouteArgs& a, float z, float m, float r, float& x) 
   return __expf(z - m) * r;
 }
 // c's error: the score's, the addition's, and what underflows.
-FP8L_DEV float c_error(float p, float x, float c) {
-  return p * ((fminf(x, 128.0f) + 24.0f) * 0x1p-23f) + 0x1p-23f * fabsf(c) + 0x1p-120f;
+FP8L_DEV float c_error(const RouteArgs& a, float p, float x, float c) {
+  const float n = a.score == kSigmoid ? 4.0f : 24.0f;
+  return p * ((fminf(x, 128.0f) + n) * 0x1p-23f) + 0x1p-23f * fabsf(c) + 0x1p-120f;
 }
 
 // The chosen expert of slot i in lane i (-1: none) and its logit; sure: false
 // where the row has to be done in 64 bits.  m: the row's largest logit.
 template <int IN, int V>
 FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[V], int64_t t,
-                      float m, int sl, bool& sure, float& zi) {
+                      float m, int sl, uint8_t* row, bool& sure, float& zi) {
   constexpr int LOW = key_low<V>();
   constexpr uint32_t MASK = (1u << LOW) - 1;
   const bool grouped = a.groups > 1 && a.kept < a.groups;
@@ -406,7 +456,7 @@ FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[
       const bool off = z[v] == -INFINITY;
       float x, p = score32(a, z[v], m, rs, x);
       g[v] = off ? -INFINITY : p + b[v];
-      const float d = g[v] == -INFINITY ? 0.0f : c_error(p, x, g[v]);
+      const float d = g[v] == -INFINITY ? 0.0f : c_error(a, p, x, g[v]);
       err = fmaxf(err, d);
       c[v] = a.bias ? g[v] + 2.0f * d : z[v];  // twice: the addition of the bound
       if (g[v] == -INFINITY) c[v] = -INFINITY;
@@ -415,7 +465,7 @@ FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = g[v] = z[v];
   }
-  sure = !grouped || keep_groups32<V>(a, c, g, sl, by_score ? 2.0f * lanes_max<16>(err) : -1.0f);
+  sure = !grouped || keep_groups32<V>(a, c, g, sl, row, by_score ? 2.0f * lanes_max<16>(err) : -1.0f);
   // keys
   const bool exact = IN != kInF32 && !a.bias;
   uint32_t key[V], last = 0;
@@ -469,7 +519,7 @@ FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[
     if (a.bias && live) {
       p = score32(a, zi, m, rs, x);
       ci = p + bi;
-      d = c_error(p, x, ci);
+      d = c_error(a, p, x, ci);
     }
     const float above = units / scale;
     const float bound =
@@ -485,8 +535,9 @@ FP8L_DEV int choose32(const RouteArgs& a, const float (&z)[V], const float (&b)[
   double ci = -INFINITY, p = 0.0;
   if (live) {
     if (a.bias) {
-      p = a.score == kSigmoid ? 1.0 / (1.0 + exp(-(double)zi))
-                              : exp((double)zi - (double)m) / (double)sum;
+      const bool sig = a.score == kSigmoid;
+      const double x = exp(sig ? -(double)zi : (double)zi - (double)m);
+      p = (sig ? 1.0 : x) / (sig ? 1.0 + x : (double)sum);
       ci = p + (double)bi;
     } else {
       ci = zi;
@@ -534,14 +585,13 @@ FP8L_DEV void load_v(const void* p, int64_t i, float (&v)[V]) {
   }
 }
 
-// One row of L lanes, V experts per lane (E <= L V, k <= L): the slot of lane
-// sl: its expert, and its weight in w.
-template <int IN, int L, int V>
-FP8L_DEV int route_row(const RouteArgs& a, int64_t t, int sl, uint8_t* row_lds, float& w) {
-  float z[V], b[V];
+// A lane's logits and biases of row t (-inf, 0 past the last expert).
+template <int IN, int V>
+FP8L_DEV void load_row(const RouteArgs& a, int64_t t, int sl, bool vec, float (&z)[V],
+                       float (&b)[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) z[v] = -INFINITY, b[v] = 0.0f;
-  if (a.vec) {
+  if (vec) {
     if (sl * V < a.E) {
       load_v<IN>(a.z, t * a.E + sl * V, z);
       if (a.bias) load_v<kInF32>(a.bias, sl * V, b);
@@ -556,6 +606,24 @@ FP8L_DEV int route_row(const RouteArgs& a, int64_t t, int sl, uint8_t* row_lds, 
       }
     }
   }
+}
+
+// Experts per lane where 64 lanes take a row of 16 V, and its LDS.
+template <int V>
+constexpr int wide_v() { return V < 4 ? 1 : V / 4; }
+template <int L, int V>
+constexpr int route_wave_lds() {
+  constexpr int rows = L == 64 ? 0 : 4 * group_lds<16, V, float>();
+  constexpr int wide = group_lds<64, L == 64 ? V : wide_v<V>(), double>();
+  return rows > wide ? rows : wide;
+}
+
+// One row of L lanes, V experts per lane (E <= L V, k <= L): the slot of lane
+// sl: its expert, and its weight in w.  lds: route_wave_lds of this wave.
+template <int IN, int L, int V>
+FP8L_DEV int route_row(const RouteArgs& a, int64_t t, int sl, uint8_t* lds, float& w) {
+  float z[V], b[V];
+  load_row<IN>(a, t, sl, a.vec, z, b);
   bool bad = false;
   float m = -INFINITY;
 #pragma unroll
@@ -565,17 +633,28 @@ FP8L_DEV int route_row(const RouteArgs& a, int64_t t, int sl, uint8_t* row_lds, 
   }
   m = lanes_max<L>(m);
   bad = lanes_any<L>(bad);
-  int mine;
+  int mine = -1;
   float zi = 0.0f;
-  bool sure = false;
-  if constexpr (L == 16) {
-    if (a.lanes) mine = choose32<IN, V>(a, z, b, t, m, sl, sure, zi);
-  }
-  if (__any(!sure && !bad)) {
-    const int again = choose<L, V, double>(a, z, b, m, sl, row_lds);
-    if (!sure) {
-      mine = again;
-      zi = sl < a.k && mine >= 0 ? load1<IN>(a.z, t * a.E + mine) : 0.0f;
+  if constexpr (L == 64) {
+    mine = choose<L, V, double>(a, z, b, m, sl, lds);
+    zi = sl < a.k && mine >= 0 ? load1<IN>(a.z, t * a.E + mine) : 0.0f;
+  } else {
+    bool sure;
+    const int lane = threadIdx.x & 63;
+    mine = choose32<IN, V>(a, z, b, t, m, sl, lds + (lane >> 4) * group_lds<16, V, float>(), sure,
+                           zi);
+    for (uint64_t todo = __ballot(!sure && !bad && sl == 0); todo; todo &= todo - 1) {
+      const int from = __builtin_ctzll(todo);
+      const int64_t row = __builtin_amdgcn_readlane((int)t, from);  // T < 2^31
+      constexpr int W = wide_v<V>();
+      float zw[W], bw[W];
+      load_row<IN>(a, row, lane, false, zw, bw);
+      const int all = choose<64, W, double>(a, zw, bw, __shfl(m, from), lane, lds);
+      const int again = __shfl(all, sl);
+      if (lane >> 4 == from >> 4) {
+        mine = again;
+        zi = sl < a.k && mine >= 0 ? load1<IN>(a.z, t * a.E + mine) : 0.0f;
+      }
     }
   }
   const bool live = sl < a.k && !bad && mine >= 0;
@@ -586,12 +665,12 @@ FP8L_DEV int route_row(const RouteArgs& a, int64_t t, int sl, uint8_t* row_lds, 
 
 template <int IN, int L, int V>
 __global__ __launch_bounds__(kRThreads) void route_kernel(RouteArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kRThreads / L * route_row_lds<L, V>()];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRThreads / 64 * route_wave_lds<L, V>()];
   const int sl = threadIdx.x % L;
   const int64_t t = (int64_t)blockIdx.x * (kRThreads / L) + threadIdx.x / L;
   float w;
   const int e = route_row<IN, L, V>(a, t < a.T ? t : a.T - 1, sl,
-                                    lds + threadIdx.x / L * route_row_lds<L, V>(), w);
+                                    lds + threadIdx.x / 64 * route_wave_lds<L, V>(), w);
   if (t < a.T && sl < a.k) {
     a.idx[t * a.k + sl] = e;
     a.w[t * a.k + sl] = w;
@@ -877,9 +956,8 @@ __global__ __launch_bounds__(kPlaceThreads) void route_place_kernel(RouteArgs a,
   uint8_t* const rows = reinterpret_cast<uint8_t*>(place) + place_lds<kPlaceThreads>(p.E);
   const int sl = threadIdx.x % 16, t = threadIdx.x / 16;
   float w;
-  // (lds of the rows only where groups need it)
   const int e = route_row<IN, 16, V>(a, min(t, a.T - 1), sl,
-                                     rows + (a.lanes ? 0 : t * route_row_lds<16, V>()), w);
+                                     rows + threadIdx.x / 64 * route_wave_lds<16, V>(), w);
   if (t < a.T && sl < a.k) {
     a.idx[t * a.k + sl] = e;
     a.w[t * a.k + sl] = w;
@@ -890,9 +968,9 @@ __global__ __launch_bounds__(kPlaceThreads) void route_place_kernel(RouteArgs a,
 }
 constexpr int kRoutePlaceRows = kPlaceThreads / 16;
 template <int V>
-constexpr int route_place_lds(int E, bool rows) {
+constexpr int route_place_lds(int E) {
   return 4 * kPlaceThreads + place_lds<kPlaceThreads>(E) +
-         (rows ? kRoutePlaceRows * route_row_lds<16, V>() : 0);
+         kPlaceThreads / 64 * route_wave_lds<16, V>();
 }
 
 // ---------------------------------------------------------------- rows
