@@ -340,17 +340,15 @@ struct MxPieces {
           t.c[o][j];
   }
 
-  // The operand at a place, of step 2 p + u; a block past the last has zeros for
-  // a scale too.
+  // The operand at a place, of the piece's step u.
   FP8L_DEV v8i codes(int place, int u) const {
     const uint32_t r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
     const v4i a = *reinterpret_cast<const v4i*>(mine + place * kPiece + chunk(r, 4 * u + q));
     return v8i{a.x, a.y, a.z, a.w, 0, 0, 0, 0};
   }
-  FP8L_DEV uint32_t scale(int place, int u, uint32_t p) const {
+  FP8L_DEV uint32_t scale(int place, int u) const {  // (bytes past the last block are zeros)
     const uint32_t r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
-    const uint32_t e = mine[place * kPiece + 2048 + 4 * (16 * u + r) + q];
-    return 128 * p + 64 * u + 16 * q < ld ? e : 0;
+    return mine[place * kPiece + 2048 + 4 * (16 * u + r) + q];
   }
 };
 
@@ -436,10 +434,10 @@ struct MxSkinny {
         if (m + 2 >= MT) w.load(t, p + KW);  // past the last: zeros
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (m == 0) b[u] = w.codes(0, u), eb[u] = w.scale(0, u, p);
+          if (m == 0) b[u] = w.codes(0, u), eb[u] = w.scale(0, u);
 #pragma unroll
           for (int i = 0; i < 2 && m + i < MT; ++i)
-            acc[m + i] = mma(b[u], w.codes(1 + i, u), acc[m + i], eb[u], w.scale(1 + i, u, p));
+            acc[m + i] = mma(b[u], w.codes(1 + i, u), acc[m + i], eb[u], w.scale(1 + i, u));
         }
       }
       asm volatile("" ::: "memory");  // before the next piece is put there
@@ -519,7 +517,7 @@ struct MxFused {
         const uint32_t k = 64 * s + 16 * q;
         const v4i a = *reinterpret_cast<const v4i*>(xc + rr * ld + (k < ld ? k : 0));
         const v8i fa = {a.x, a.y, a.z, a.w, 0, 0, 0, 0};
-        acc = S::mma(w.codes(0, u), fa, acc, w.scale(0, u, p), xe[s * rows + rr] >> (8 * q));
+        acc = S::mma(w.codes(0, u), fa, acc, w.scale(0, u), xe[s * rows + rr] >> (8 * q));
       }
       asm volatile("" ::: "memory");
     }

@@ -209,6 +209,25 @@ def test_linear_quantizes_its_input(M, N, K, dt):
     check(y2, r, m, "bf16")
 
 
+@pytest.mark.parametrize("tile", ["skinny16", "skinny32", "skinny48", "skinny64"])
+@pytest.mark.parametrize("N,K", [(33001, 2400), (26000, 300), (12000, 1100), (4100, 7000)])
+def test_few_rows_of_many_columns(monkeypatch, N, K, tile):
+    """Every way of splitting K over a block's waves (none to eight); rows of W
+    that repeat, so all their outputs do."""
+    _tile(monkeypatch, tile)
+    M = {"skinny16": 11, "skinny32": 27, "skinny48": 43, "skinny64": 59}[tile]
+    wc, we = matrix(300, K, 3)
+    rows = np.arange(N) % 300
+    x = matrix(M, K, 4)
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    F.fp8_mx4_linear_fwd(operand(*x, K), operand(wc[rows], we[rows], K), None, y)
+    r, m = X.linear(X.values(*x), X.values(wc, we))
+    check(y[:, :300], r, m, "bf16")
+    same = y[:, :N // 300 * 300].view(M, -1, 300)
+    assert torch.equal(same, y[:, None, :300].expand_as(same))
+    assert torch.equal(y[:, N // 300 * 300:], y[:, :N % 300])
+
+
 def test_empty_sizes():
     w = operand(*matrix(16, 64, 1), 64)
     y = torch.empty(0, 16, dtype=torch.bfloat16, device=DEV)

@@ -125,6 +125,26 @@ def test_scores_closer_than_32_bits(score, E):
 
 
 @pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("T", [1, 5, 33, 70])
+@pytest.mark.parametrize("E,groups", [(16, 4), (64, 8), (48, 4), (96, 12), (128, 4), (160, 8),
+                                      (256, 8), (255, 5), (600, 8)])
+def test_groups_closer_than_32_bits(E, groups, T, score):
+    """Every third row as above, others ordinary ones: groups, and experts of
+    them, that 32 bits do not tell apart; whole, in parts of a lane's experts
+    and over lanes."""
+    rng = np.random.default_rng(E + T)
+    base = np.float32(6.0) if score else np.float32(1.0)
+    z = np.float32(2 * rng.standard_normal((T, E)))
+    z[::3] = base + np.float32(rng.integers(0, 40, z[::3].shape)) * np.spacing(base)
+    z = torch.from_numpy(z)
+    for b in (None, np.full(E, np.float32(0.3))):
+        for top in (1, 2):
+            kw = dict(score=score, groups=groups, groups_kept=groups // 2, group_top=top)
+            idx, w, _, _ = _route(z, 4, b, **kw)
+            _check(z, b, 4, idx, w, **kw)
+
+
+@pytest.mark.parametrize("score", [0, 1])
 def test_saturated_and_underflowing_scores(score):
     rng = np.random.default_rng(2)
     z = np.concatenate([30 + rng.standard_normal((20, 48)), -150 + 20 * rng.standard_normal((20, 48)),
