@@ -650,11 +650,14 @@ def _gpu_of(t, what):
     return t.device
 
 
+_Tensor = torch.Tensor
+
+
 def _arg(t, what, dtypes, shape, dev, optional=False, numel=None):
     """Data pointer of a checked tensor argument (None when absent)."""
     if t is None and optional:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == dev and t.is_cuda
+    if (isinstance(t, _Tensor) and t.dtype in dtypes and t.device == dev and t.is_cuda
             and t.is_contiguous() and (shape is None or t.shape == shape)
             and (numel is None or t.numel() >= numel)):
         return t.data_ptr()
@@ -663,6 +666,8 @@ def _arg(t, what, dtypes, shape, dev, optional=False, numel=None):
 
 
 def _shape_of(t, dims, what):
+    if isinstance(t, _Tensor) and len(t.shape) == dims:
+        return t.shape
     d = t.codes if isinstance(t, (Quantized, QuantizedRows)) else t
     if not isinstance(d, torch.Tensor) or d.dim() != dims:
         raise ValueError(f"{what}: expected a {dims}-D tensor")
@@ -707,8 +712,9 @@ _entry = {}  # C functions by name
 
 
 def _run(name, args, dev):
-    fn = _entry.get(name)
-    if fn is None:
+    try:
+        fn = _entry[name]
+    except KeyError:
         fn = _entry[name] = getattr(lib(), name)
     if dev.index == _current_device():
         st = fn(*args)
@@ -1083,7 +1089,7 @@ def _route_fwd_args(logits, idx, weights, bias, score, groups, groups_kept, grou
                     scale, offsets, pos, ws, stream):
     T, E = _shape_of(logits, 2, "logits")
     k = _shape_of(idx, 2, "idx")[1]
-    dev = _gpu_of(logits, "logits")
+    dev = logits.device
     zp = _arg(logits, "logits", _HP, None, dev)
     places = (None, None, None)
     if offsets is not None or pos is not None:
@@ -1117,7 +1123,7 @@ def bind_fp8_route_fwd(logits, idx, weights, bias=None, score=FP8_ROUTE_SOFTMAX,
 def _route_bwd_args(logits, idx, dweights, dlogits, score, renorm, scale, stream):
     T, E = _shape_of(logits, 2, "logits")
     k = _shape_of(idx, 2, "idx")[1]
-    dev = _gpu_of(logits, "logits")
+    dev = logits.device
     return (T, E, k, _arg(logits, "logits", _HP, None, dev), _TORCH_DT[logits.dtype], score,
             int(bool(renorm)), scale, _arg(idx, "idx", _I32, (T, k), dev),
             _arg(dweights, "dweights", _F32, (T, k), dev),
@@ -1141,7 +1147,7 @@ def bind_fp8_route_bwd(logits, idx, dweights, dlogits, score=FP8_ROUTE_SOFTMAX, 
 def _route_plan_args(idx, offsets, pos, ws, stream):
     T, k = _shape_of(idx, 2, "idx")
     E = _shape_of(offsets, 1, "offsets")[0] - 1
-    dev = _gpu_of(idx, "idx")
+    dev = idx.device
     return (T, E, k, _arg(idx, "idx", _I32, None, dev),
             *_arg_places(T, k, E, offsets, pos, ws, dev), _arg_stream(stream, dev)), dev
 
@@ -1160,7 +1166,7 @@ def _route_gather_args(x, pos, out, stream):
     T, D = _shape_of(x, 2, "x")
     k = _shape_of(pos, 2, "pos")[1]
     R = _shape_of(out, 2, "out")[0]
-    dev = _gpu_of(x, "x")
+    dev = x.device
     return (T, k, D * x.element_size(), R, _arg(x, "x", (x.dtype,), None, dev),
             _arg(pos, "pos", _I32, (T, k), dev), _arg(out, "out", (x.dtype,), (R, D), dev),
             _arg_stream(stream, dev)), dev
@@ -1180,7 +1186,7 @@ def bind_fp8_route_gather(x, pos, out, stream=None):
 def _route_combine_args(y, pos, weights, out, stream):
     R, D = _shape_of(y, 2, "y")
     T, k = _shape_of(pos, 2, "pos")
-    dev = _gpu_of(y, "y")
+    dev = y.device
     yp = _arg(y, "y", _HP, None, dev)
     return (T, k, D, R, yp, _TORCH_DT[y.dtype], _arg(pos, "pos", _I32, None, dev),
             _arg(weights, "weights", _F32, (T, k), dev, True),
@@ -1201,7 +1207,7 @@ def bind_fp8_route_combine(y, pos, weights, out, stream=None):
 def _route_combine_bwd_args(dout, y, pos, weights, dy, dweights, stream):
     T, D = _shape_of(dout, 2, "dout")
     k = _shape_of(pos, 2, "pos")[1]
-    dev = _gpu_of(dout, "dout")
+    dev = dout.device
     gp = _arg(dout, "dout", _HP, None, dev)
     R = _shape_of(dy if y is None else y, 2, "y")[0]
     dt = (dout.dtype,)
