@@ -143,9 +143,6 @@ void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t 
   const int64_t cols = (g.N + 15) / 16;
   const int kw = mx_split(units * cols, g.steps);
   const int lds = MxSkinny<MT>::kLds;
-  static std::atomic<bool> set_groups[64], set_dense[64];  // skinny_lds
-  set_lds_limit((const void*)mx4_skinny_groups_kernel<MT>, lds, set_groups);
-  set_lds_limit((const void*)mx4_skinny_kernel<MT>, lds, set_dense);
   g.tiles_n = (int32_t)((cols + 8 / kw - 1) / (8 / kw));
   if (gr)
     hipLaunchKernelGGL((mx4_skinny_groups_kernel<MT>),
@@ -299,8 +296,8 @@ int fp8_mx4_linear_fwd(int64_t M, int64_t N, int64_t K, const void* x, int32_t x
   MxArgs g = mx_args(M, N, K, x, x_dtype, x_scales, w, w_scales, bias, out_dtype, y, x4_out, sx_out);
   if (M > 0 && N > 0 && fuse_x(x, x_dtype, M, 0, N, K)) {
     by_type(x_dtype, [&](auto in) {
-      launch_fused<decltype(in)::value>(g, MxFusedX{x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)}, nullptr, MxStrides{},
-                                        stream);
+      const MxFusedX fx = {x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)};
+      launch_fused<decltype(in)::value>(g, fx, nullptr, MxStrides{}, stream);
     });
     return hip_status();
   }
@@ -327,7 +324,8 @@ int fp8_mx4_grouped_linear_fwd(int64_t T, int32_t E, int64_t N, int64_t K, const
   const Groups gr = {offsets, E, (int32_t)T};
   if (T > 0 && N > 0 && fuse_x(x, x_dtype, T, E, N, K)) {
     by_type(x_dtype, [&](auto in) {
-      launch_fused<decltype(in)::value>(g, MxFusedX{x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)}, &gr, s, stream);
+      const MxFusedX fx = {x, K, x4_out, reinterpret_cast<uint32_t*>(sx_out)};
+      launch_fused<decltype(in)::value>(g, fx, &gr, s, stream);
     });
     return hip_status();
   }

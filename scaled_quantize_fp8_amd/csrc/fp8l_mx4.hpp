@@ -359,7 +359,7 @@ template <int MT>
 struct MxSkinny {
   using P = MxPieces<MT>;
   static constexpr int kBM = 16 * MT, kWaveN = 16, kThreads = 512, kLds = 8 * P::kWave;
-  static_assert(kLds >= 8 * MT * 1024, "partial sums");
+  static_assert(kLds >= 8 * MT * 1024 && kLds <= 65536, "partial sums fit, and need no larger limit");
 
   FP8L_DEV static v4f mma(v8i b, v8i a, v4f c, uint32_t sb, uint32_t sa) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 4, 4, 0, (int)sb, 0, (int)sa);

@@ -181,7 +181,7 @@ struct MxTile {
     };
     // the columns' bias, in words, behind the ring: older than every stage, so
     // the waits below cover it (kept out of the epilogue, where every tile would
-    // wait for it: 8200 rows through 16 experts of 1536 -> 6912 with bias 113 us)
+    // wait for it: 8200 rows through 16 experts of 1536 -> 6912 113 us, so 103)
     const bool staged = g.bias && ((uintptr_t)g.bias & 3) == 0 && (cols & 1) == 0;
     if (staged && wv < 2)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
