@@ -635,7 +635,7 @@ int fp8_route_plan(int64_t T, int32_t E, int32_t k, const int32_t* idx, int32_t*
  * Rows into expert order: out[pos[t, i]] = x[t] for every slot with a place in
  * [0, R).  Rows are row_bytes bytes (values of any type, codes, scales; fewer
  * than 2^24); x has T of them, out R.  Rows of out that no slot names are left as
- * they were.
+ * they were; a row that two tokens name is unspecified.
  */
 int fp8_route_gather(int64_t T, int32_t k, int64_t row_bytes, int64_t R, const void* x,
                      const int32_t* pos, void* out, hipStream_t stream);

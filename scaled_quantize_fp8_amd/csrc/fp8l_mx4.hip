@@ -48,7 +48,7 @@ void enqueue_mx_quantize(const void* x, int32_t dt, int64_t mats, int64_t rows, 
   if (mats == 0 || rows == 0 || K == 0) return;
   MxQuantArgs a = {x, codes, reinterpret_cast<uint32_t*>(scales), rows, K, (int32_t)mx_steps(K),
                    (int32_t)mx_blocks(K), 0, valid};
-  const bool vec = aligned16(x) && K % 8 == 0;
+  const bool vec = K % 8 == 0;
   const dim3 grid = quant_grid(mats, rows, a.steps, dt == FP8_DT_F32 ? 2 : 4, &a.rows_log);
   by_type(dt, [&](auto in) {
     constexpr int IN = decltype(in)::value;
@@ -273,7 +273,7 @@ int fp8_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t mats
   if (!aligned16(codes) || !aligned4(scales)) return FP8_ERR_SHAPE;
   MxDequantArgs a = {codes, reinterpret_cast<const uint32_t*>(scales), out, rows, K,
                      (int32_t)mx_steps(K), (int32_t)mx_blocks(K), 0, 0};
-  a.vec = aligned16(out) && K % 8 == 0;
+  a.vec = K % 8 == 0;
   const dim3 grid = quant_grid(mats, rows, a.steps, 4, &a.rows_log);
   by_type(out_dtype, [&](auto in) {
     hipLaunchKernelGGL((mx4_dequantize_kernel<decltype(in)::value>), grid, dim3(kMxThreads), 0,

@@ -82,7 +82,7 @@ FP8L_DEV MxEight mx_eight(const float v[8], bool inside, int sl) {
 // A block of 256 threads walks its tile of rows along K, kU steps at a time
 // with their loads in flight together (11008 x 4096 bf16, 114 MB in and out:
 // 22 us; one step at a time 34).
-// VEC: K a multiple of 8 and x aligned to 16 bytes.
+// VEC: K a multiple of 8.
 template <int IN, bool VEC>
 __global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a) {
   constexpr int kU = IN == kInF32 ? 2 : 4;
@@ -102,10 +102,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a)
       for (int u = 0; u < kU; ++u) {
         const int64_t k = (s0 + u * across) * 128 + 8 * sl;
         raw[u].zero();
-        if (r < rows && k + 8 <= a.K) {
-          if constexpr (VEC) raw[u].load(a.x, at + k);
-          else raw[u].load_any(a.x, at + k);
-        }
+        if (r < rows && k + 8 <= a.K) raw[u].load(a.x, at + k);
       }
       if constexpr (!VEC) {
         // the row's last piece, where it is not whole

@@ -218,16 +218,12 @@ int fp8_route_gather(int64_t T, int32_t k, int64_t row_bytes, int64_t R, const v
   if (!x || !pos || !out) return FP8_ERR_NULL;
   GatherArgs a = {reinterpret_cast<const uint8_t*>(x), reinterpret_cast<uint8_t*>(out), pos,
                   (int32_t)T, k, (int32_t)R, row_bytes, {}};
-  const uintptr_t low = (uintptr_t)x | (uintptr_t)out | (uintptr_t)row_bytes;
   auto go = [&](auto u) {
     constexpr int U = decltype(u)::value;
-    const dim3 grid = row_grid(T, row_bytes / U, a.grid);
+    const dim3 grid = row_grid(T, (row_bytes + U - 1) / U, a.grid);
     hipLaunchKernelGGL((gather_kernel<U>), grid, dim3(kRThreads), 0, stream, a);
   };
-  if (low % 16 == 0) go(Int<16>{});
-  else if (low % 8 == 0) go(Int<8>{});
-  else if (low % 4 == 0) go(Int<4>{});
-  else if (low % 2 == 0) go(Int<2>{});
+  if (row_bytes >= 16) go(Int<16>{});
   else go(Int<1>{});
   return hip_status();
 }
@@ -240,10 +236,10 @@ int fp8_route_combine(int64_t T, int32_t k, int64_t D, int64_t R, const void* y,
   if (T == 0 || D == 0) return FP8_OK;
   if ((R > 0 && !y) || !pos || !out) return FP8_ERR_NULL;
   CombineArgs a = {y, pos, weights, out, (int32_t)T, k, (int32_t)R, D, {}};
-  const bool vec = D % 8 == 0 && aligned16(y) && aligned16(out);
+  const bool vec = D >= 8;
   by_type(dtype, [&](auto in) {
     constexpr int IN = decltype(in)::value;
-    const dim3 grid = row_grid(T, vec ? D / 8 : D, a.grid);
+    const dim3 grid = row_grid(T, vec ? (D + 7) / 8 : D, a.grid);
     const bool uni = a.grid.width_log >= 6;  // a wave's pieces are one token's
     auto go = [&](auto n, auto u) {
       hipLaunchKernelGGL((combine_kernel<IN, decltype(n)::value, decltype(u)::value>), grid,
@@ -251,7 +247,6 @@ int fp8_route_combine(int64_t T, int32_t k, int64_t D, int64_t R, const void* y,
     };
     if (vec && uni) go(Int<8>{}, std::true_type{});
     else if (vec) go(Int<8>{}, std::false_type{});
-    else if (uni) go(Int<1>{}, std::true_type{});
     else go(Int<1>{}, std::false_type{});
   });
   return hip_status();
@@ -266,7 +261,7 @@ int fp8_route_combine_bwd(int64_t T, int32_t k, int64_t D, int64_t R, const void
   if (T == 0) return FP8_OK;
   if (!pos || !weights || (D > 0 && !dout) || (D > 0 && R > 0 && dweights && !y)) return FP8_ERR_NULL;
   CombineBwdArgs a = {dout, y, pos, weights, dy, dweights, (int32_t)T, k, (int32_t)R, D};
-  const bool vec = D % 8 == 0 && aligned16(dout) && aligned16(y) && aligned16(dy);
+  const bool vec = D >= 8;
   const int64_t blocks = (T + 3) / 4, cap = 1 << 20;
   const dim3 grid((unsigned)(blocks < cap ? blocks : cap));
   by_type(dtype, [&](auto in) {

@@ -975,19 +975,21 @@ constexpr int route_place_lds(int E) {
 
 // ---------------------------------------------------------------- rows
 
-// A row's pieces of U bytes (U: the widest that sizes and pointers allow) go
-// to `width` neighbouring threads (a power of two up to the block's), the
-// block's 256 / width tokens side by side, further pieces over blockIdx.y.
+// A row's pieces go to `width` neighbouring threads (a power of two up to the
+// block's), the block's 256 / width tokens side by side, further pieces over
+// blockIdx.y.  A piece is 16 bytes (8 values), at any address; the last one of a
+// row ends with it and may overlap the one before, which then holds the same
+// (4096 x 8 rows of 4097 bf16 values, us so / value by value: there 64 / 138,
+// back 61 / 177, gradients 123 / 360).  Rows shorter than a piece go by single
+// bytes or values.
 struct RowGrid {
   int32_t width_log, pieces;
 };
 
 template <int U>
-struct Bytes;
-template <> struct Bytes<16> { typedef uint4 T; };
-template <> struct Bytes<8> { typedef uint2 T; };
-template <> struct Bytes<4> { typedef uint32_t T; };
-template <> struct Bytes<2> { typedef uint16_t T; };
+struct Bytes {
+  typedef uint32_t T __attribute__((ext_vector_type(4), aligned(1)));
+};
 template <> struct Bytes<1> { typedef uint8_t T; };
 
 struct GatherArgs {
@@ -1005,7 +1007,7 @@ __global__ __launch_bounds__(kRThreads) void gather_kernel(GatherArgs a) {
   const int piece = blockIdx.y * (1 << a.grid.width_log) + (threadIdx.x & ((1 << a.grid.width_log) - 1));
   if (piece >= a.grid.pieces) return;
   const int per = kRThreads >> a.grid.width_log;
-  const int64_t at = (int64_t)piece * U;
+  const int64_t at = min<int64_t>((int64_t)piece * U, a.row - U);
   for (int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.grid.width_log); t < a.T;
        t += (int64_t)gridDim.x * per) {
     const P v = *reinterpret_cast<const P*>(a.x + t * a.row + at);
@@ -1026,12 +1028,7 @@ struct CombineArgs {
   RowGrid grid;
 };
 
-// A piece of N values of a row: N = 8 with 16-byte accesses, or 1.
-template <int IN, int N>
-FP8L_DEV void load_n(const void* p, int64_t i, float (&v)[N]) {
-  if constexpr (N == 8) load8<IN>(p, i, v);
-  else v[0] = load1<IN>(p, i);
-}
+// A piece of N values of a row, 8 or 1.
 template <int IN, int N>
 FP8L_DEV void store_n(void* p, int64_t i, const float (&v)[N]) {
   if constexpr (N == 8) store8<IN>(p, i, v);
@@ -1070,7 +1067,7 @@ template <int IN, int N, bool UNI>
 __global__ __launch_bounds__(kRThreads) void combine_kernel(CombineArgs a) {
   const int piece = blockIdx.y * (1 << a.grid.width_log) + (threadIdx.x & ((1 << a.grid.width_log) - 1));
   const int per = kRThreads >> a.grid.width_log;
-  const int64_t at = (int64_t)piece * N;
+  const int64_t at = min<int64_t>((int64_t)piece * N, a.D - N);
   for (int64_t t0 = (int64_t)blockIdx.x * per + (threadIdx.x >> a.grid.width_log); t0 < a.T;
        t0 += (int64_t)gridDim.x * per) {
     const int t = UNI ? __builtin_amdgcn_readfirstlane((int)t0) : (int)t0;
@@ -1114,7 +1111,7 @@ template <int IN, int N>
 __global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a) {
   constexpr int S = kSlotBatch;
   const int lane = threadIdx.x & 63;
-  const int64_t pieces = a.D / N;
+  const int64_t pieces = (a.D + N - 1) / N;
   for (int64_t t0 = (int64_t)blockIdx.x * (kRThreads / 64) + (threadIdx.x >> 6); t0 < a.T;
        t0 += (int64_t)gridDim.x * (kRThreads / 64)) {
     const int t = __builtin_amdgcn_readfirstlane((int)t0);
@@ -1125,20 +1122,25 @@ __global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a
 #pragma unroll
       for (int s = 0; s < S; ++s) dot[s] = 0.0f;
       for (int64_t c = lane; c < pieces; c += 64) {
+        const int64_t at = min<int64_t>(c * N, a.D - N);
+        const int seen = (int)(c * N - at);  // values of the piece before
+        Raw<IN, N> raw;
+        raw.load(a.dout, t * a.D + at);
         float g[N];
-        load_n<IN>(a.dout, t * a.D + c * N, g);
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[j] = raw.get(j);
         if (a.dw) {
           Raw<IN, N> v[S];
 #pragma unroll
           for (int s = 0; s < S; ++s) {
-            if (p[s] >= 0) v[s].template load<true>(a.y, p[s] * a.D + c * N);
+            if (p[s] >= 0) v[s].template load<true>(a.y, p[s] * a.D + at);
             else v[s].zero();
           }
 #pragma unroll
           for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int j = 0; j < N; ++j)
-              if (p[s] >= 0) dot[s] = __builtin_fmaf(g[j], v[s].get(j), dot[s]);
+              if (p[s] >= 0 && j >= seen) dot[s] = __builtin_fmaf(g[j], v[s].get(j), dot[s]);
         }
         if (a.dy) {
 #pragma unroll
@@ -1147,7 +1149,7 @@ __global__ __launch_bounds__(kRThreads) void combine_bwd_kernel(CombineBwdArgs a
             float v[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) v[j] = w[s] * g[j];
-            store_n<IN>(a.dy, p[s] * a.D + c * N, v);
+            store_n<IN>(a.dy, p[s] * a.D + at, v);
           }
         }
       }

@@ -14,42 +14,35 @@ FP8L_DEV void store1(void* p, int64_t i, float v) {
   else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
 }
 
-// 8 consecutive elements, aligned as for load8.
+// 16 bytes at any address that suits the type: gfx950 takes such wide accesses.
+typedef uint32_t Any4 __attribute__((ext_vector_type(4), aligned(2)));
+
+// 8 consecutive elements at any address that suits the type.
 template <int IN>
 FP8L_DEV void store8(void* p, int64_t i, const float v[8]) {
+  Any4* const q = reinterpret_cast<Any4*>(reinterpret_cast<uint8_t*>(p) + i * (IN == kInF32 ? 4 : 2));
   if constexpr (IN == kInF32) {
-    float4* const q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    q[0] = Any4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                __float_as_uint(v[3])};
+    q[1] = Any4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                __float_as_uint(v[7])};
   } else {
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o[j] = IN == kInF16 ? f32_to_f16(v[2 * j]) | (f32_to_f16(v[2 * j + 1]) << 16)
                           : pk_bf16(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint4(o[0], o[1], o[2], o[3]);
+    q[0] = Any4{o[0], o[1], o[2], o[3]};
   }
 }
 
-// N values (1, or 8 aligned as for load8) as loaded, and in 32 bits: several
-// are in flight when all are loaded before the first is looked at.  ONCE: a
-// streaming load (values that are read once).
+// N values (1, or 8 at any address that suits the type) as loaded, and in 32
+// bits: several are in flight when all are loaded before the first is looked
+// at.  ONCE: a streaming load (values that are read once).
 template <int IN, int N>
 struct Raw {
   static constexpr int kWords = N == 1 ? 1 : (IN == kInF32 ? 8 : 4);
-  typedef uint32_t words4 __attribute__((ext_vector_type(4)));
   uint32_t w[kWords];
-  // At any address that suits the type (N = 8): gfx950 takes such wide loads.
-  FP8L_DEV void load_any(const void* p, int64_t i) {
-    typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
-    const any4* const q = reinterpret_cast<const any4*>(reinterpret_cast<const uint8_t*>(p) +
-                                                        i * (IN == kInF32 ? 4 : 2));
-#pragma unroll
-    for (int j = 0; j < kWords / 4; ++j) {
-      const any4 x = q[j];
-      w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
-    }
-  }
   FP8L_DEV void put(int j, float f) {  // of a value that the type holds
     if constexpr (N == 1 || IN == kInF32) w[j] = __float_as_uint(f);
     else {
@@ -62,12 +55,11 @@ struct Raw {
     if constexpr (N == 1) {
       w[0] = __float_as_uint(load1<IN>(p, i));
     } else {
-      const uint4* const q = reinterpret_cast<const uint4*>(
-          reinterpret_cast<const uint8_t*>(p) + i * (IN == kInF32 ? 4 : 2));
+      const Any4* const q = reinterpret_cast<const Any4*>(reinterpret_cast<const uint8_t*>(p) +
+                                                          i * (IN == kInF32 ? 4 : 2));
 #pragma unroll
       for (int j = 0; j < kWords / 4; ++j) {
-        const words4* const at = reinterpret_cast<const words4*>(q + j);
-        const words4 x = ONCE ? __builtin_nontemporal_load(at) : *at;
+        const Any4 x = ONCE ? __builtin_nontemporal_load(q + j) : q[j];
         w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
       }
     }

@@ -14,8 +14,8 @@ pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}
 TINY = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}
-SIZES = [(1, 1, 1), (1, 4, 64), (24, 4, 1536), (7, 8, 40), (65, 3, 129), (33, 9, 520), (5, 17, 1003),
-         (130, 2, 256), (2, 64, 8), (3, 5, 4104)]
+SIZES = [(1, 1, 1), (1, 4, 64), (24, 4, 1536), (7, 8, 40), (65, 3, 129), (33, 9, 520), (5, 17, 1003), (9, 3, 9),
+         (40, 2, 15), (6, 5, 7), (12, 8, 1025), (130, 2, 256), (2, 64, 8), (3, 5, 4104)]
 
 
 def _places(T, k, seed):
@@ -117,6 +117,24 @@ def test_places_outside_the_rows_are_left_alone():
     F.fp8_route_combine_bwd(out, y, pos, w, guard[1:5], dw)
     assert (guard[0] == 5).all() and (guard[5] == 5).all() and (guard[2:4] == 5).all()
     assert dw[0, 1] == 0 and not dw[1].any() and dw[2, 1] == 0
+
+
+def test_the_longest_rows():
+    """Rows of 2^24 - 1 bytes, and the longest sums."""
+    n = (1 << 24) - 1
+    x = torch.arange(n, device=DEV).to(torch.uint8).view(1, n)
+    out = torch.zeros(3, n, dtype=torch.uint8, device=DEV)
+    F.fp8_route_gather(x, torch.tensor([[2, 0]], dtype=torch.int32, device=DEV), out)
+    assert torch.equal(out[2], x[0]) and torch.equal(out[0], x[0]) and not out[1].any()
+    for D in (1 << 22, (1 << 22) - 1):
+        y = torch.ones(2, D, dtype=torch.bfloat16, device=DEV)
+        s = torch.empty(1, D, dtype=torch.bfloat16, device=DEV)
+        pos = torch.tensor([[1, 0]], dtype=torch.int32, device=DEV)
+        F.fp8_route_combine(y, pos, None, s)
+        assert (s == 2).all()
+        dw = torch.empty(1, 2, device=DEV)
+        F.fp8_route_combine_bwd(s, y, pos, torch.ones(1, 2, device=DEV), None, dw)
+        assert (dw == 2 * D).all()  # sums of whole numbers below 2^24: exact
 
 
 def test_no_rows():

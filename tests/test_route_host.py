@@ -60,7 +60,7 @@ def test_workspace():
     w = F.fp8_route_workspace_bytes
     assert w(0, 8, 2) == 0 and w(16384, 8, 2) == 0 and w(16385, 8, 2) == 17 * 8 * 4
     assert w(-1, 8, 2) == 0 and w(10000, 2000, 2) == 0
-    for T in (1 << 10, 1 << 17, 1 << 20, 1 << 24):  # at most 512 chunks
+    for T in (1 << 10, 1 << 17, 1 << 20, 1 << 24):  # at most 512 chunks' counts
         assert w(T, 256, 8) <= 512 * 256 * 4
 
 
