@@ -24,6 +24,7 @@
 
 #include "fp8l_gemm3.hpp"
 #include "fp8l_grouped.hpp"
+#include "fp8l_mx4_span.hpp"
 #include "fp8l_values.hpp"
 
 namespace fp8l {
@@ -276,15 +277,15 @@ struct MxPieces {
       : rb(mx_rsrc(g.b, cols * g.ld)),
         // words of rows past the end are those of other rows, or zeros past the
         // last step: they meet zero codes or columns that are not stored
-        rsb(mx_rsrc(g.sb, ((int64_t)(g.steps - 1) * g.sb_step + cols) * 4)),
+        rsb(mx_rsrc(g.sb, mx_scale_span(g.steps, g.sb_step, cols))),
         ra(mx_rsrc(g.a, NX ? g.M * g.ld : 0)),
-        rsa(mx_rsrc(g.sa, NX ? ((int64_t)(g.steps - 1) * g.sa_step + g.M) * 4 : 0)),
+        rsa(mx_rsrc(g.sa, NX ? mx_scale_span(g.steps, g.sa_step, g.M) : 0)),
         ld((uint32_t)g.ld), sb_step((uint32_t)g.sb_step), sa_step((uint32_t)g.sa_step),
         steps((uint32_t)g.steps), j0(j0), mine(mine) {}
 
-  // Piece p, zeros past the last block.
+  // Piece p, zeros past the last block (a wave's first one is loaded whether it
+  // has one or not).
   FP8L_DEV void load(Regs& t, uint32_t p) const {
-    constexpr uint32_t kNowhere = 0x80000000u;
     const uint32_t lane = threadIdx.x & 63, row = lane >> 3, k = 128 * p + 16 * (lane & 7);
 #pragma unroll
     for (int o = 0; o < kOperands; ++o)
@@ -292,7 +293,7 @@ struct MxPieces {
       for (int j = 0; j < 2; ++j) {
         const uint32_t at = (o ? 16 * (o - 1) : j0) + 8 * j + row;
         t.c[o][j] = __builtin_bit_cast(
-            v4i, __builtin_amdgcn_raw_buffer_load_b128(o ? ra : rb, k < ld ? at * ld + k : kNowhere,
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(o ? ra : rb, k < ld ? at * ld + k : kMxNowhere,
                                                        0, 0));
       }
     const uint32_t s = 2 * p + (lane >> 4 & 1), r = lane & 15, half = lane >> 5;
@@ -301,7 +302,7 @@ struct MxPieces {
       const uint32_t m = 2 * (i - 1) + half;  // of X
       const bool in = s < steps && (i ? m < NX : half == 0);
       const uint32_t at = i ? s * sa_step + 16 * m + r : s * sb_step + j0 + r;
-      t.e[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(i ? rsa : rsb, in ? 4 * at : kNowhere,
+      t.e[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(i ? rsa : rsb, in ? 4 * at : kMxNowhere,
                                                               0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -1,0 +1,20 @@
+// Which bytes the 4-bit kernels may touch: plain arithmetic of sizes and
+// offsets, the same for the kernels and for a test on the CPU.
+#pragma once
+
+#include <stdint.h>
+
+namespace fp8l {
+
+// An offset past every buffer descriptor of these kernels: a load from it
+// gives zeros.
+constexpr uint32_t kMxNowhere = 0x80000000u;
+
+// Bytes of scale words that a tile's descriptor covers: `rows` rows of each of
+// `steps` steps, whose words lie `step` words apart.  None without a step
+// (K = 0, where the last step's number would be -1).
+constexpr int64_t mx_scale_span(int64_t steps, int64_t step, int64_t rows) {
+  return steps > 0 ? ((steps - 1) * step + rows) * 4 : 0;
+}
+
+}  // namespace fp8l
