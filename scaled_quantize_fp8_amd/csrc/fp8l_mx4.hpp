@@ -161,10 +161,9 @@ __global__ __launch_bounds__(kMxThreads) void mx4_dequantize_kernel(MxDequantArg
       uint32_t w[kU], word[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        // past the last value: the first piece again, not stored
-        const int64_t s = s0 + u * across, at = s * 128 + 8 * sl < a.K ? s : 0;
-        w[u] = *reinterpret_cast<const uint32_t*>(codes + at * 64 + (at == s ? 4 * sl : 0));
-        word[u] = a.scales[(mat * a.steps + at) * a.rows + r];
+        const MxPiece p = mx_piece(s0 + u * across, sl, a.K);
+        w[u] = *reinterpret_cast<const uint32_t*>(codes + p.byte);
+        word[u] = a.scales[(mat * a.steps + p.step) * a.rows + r];
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {

@@ -17,4 +17,14 @@ constexpr int64_t mx_scale_span(int64_t steps, int64_t step, int64_t rows) {
   return steps > 0 ? ((steps - 1) * step + rows) * 4 : 0;
 }
 
+// The codes of values [128 s + 8 sl, + 8) in a row of K (four bytes, with the
+// scale word of their step); past the last value the row's first ones, which
+// are not stored then.
+struct MxPiece {
+  int64_t step, byte;
+};
+constexpr MxPiece mx_piece(int64_t s, int sl, int64_t K) {
+  return 128 * s + 8 * sl < K ? MxPiece{s, 64 * s + 4 * sl} : MxPiece{0, 0};
+}
+
 }  // namespace fp8l

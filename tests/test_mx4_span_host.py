@@ -17,6 +17,8 @@ uint32_t nowhere() { return fp8l::kMxNowhere; }
 int64_t scale_span(int64_t steps, int64_t step, int64_t rows) {
   return fp8l::mx_scale_span(steps, step, rows);
 }
+int64_t piece_byte(int64_t s, int sl, int64_t K) { return fp8l::mx_piece(s, sl, K).byte; }
+int64_t piece_step(int64_t s, int sl, int64_t K) { return fp8l::mx_piece(s, sl, K).step; }
 }
 """
 
@@ -36,6 +38,9 @@ def span(tmp_path_factory):
     L.nowhere.restype = ctypes.c_uint32
     L.scale_span.restype = ctypes.c_int64
     L.scale_span.argtypes = [ctypes.c_int64] * 3
+    for f in (L.piece_byte, L.piece_step):
+        f.restype = ctypes.c_int64
+        f.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]
     return L
 
 
@@ -56,3 +61,17 @@ def test_scale_descriptors_end_with_the_scales(span, unit, K):
             assert 4 * first + n <= 4 * steps * rows or n == 0
             last = ((steps - 1) * rows + here - 1) * 4  # the last word of its rows
             assert n == (last + 4 if steps else 0)
+
+
+@pytest.mark.parametrize("K", [1, 8, 31, 32, 33, 64, 72, 96, 97, 127, 128, 129, 160, 300, 513, 1003])
+def test_dequantize_reads_inside_the_row(span, K):
+    """Every lane of every step, up to three batches of four steps past the
+    last: four bytes of the row's codes, a scale word of the row, and for a
+    value of the row its own."""
+    steps, row_bytes = -(-K // 128), 16 * -(-K // 32)
+    for s in range(steps + 12):
+        for sl in range(16):
+            byte, step = span.piece_byte(s, sl, K), span.piece_step(s, sl, K)
+            assert 0 <= byte <= row_bytes - 4 and 0 <= step < steps, (s, sl)
+            if 128 * s + 8 * sl < K:
+                assert step == s and byte == (128 * s + 8 * sl) // 2
