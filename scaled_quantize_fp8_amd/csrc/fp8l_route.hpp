@@ -382,9 +382,10 @@ FP8L_DEV float slot_weight(const RouteArgs& a, const float (&z)[V], float m, boo
 template <int V>
 constexpr int key_low() { return V == 1 ? 4 : V == 4 ? 6 : V == 8 ? 7 : 8; }
 
-// Order-preserving integer of a float that is no NaN.
+// Order-preserving integer of a float that is no NaN.  The sum makes -0 a +0,
+// which it ties with.
 FP8L_DEV uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(f + 0.0f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 // Value of the next lane of 16 (the last one's: its own).
