@@ -65,6 +65,15 @@ void by_row(int E, int k, F&& f) {
   }
 }
 
+// Rows of one launch of the choice or of its gradient, up to 64 lanes each: a
+// grid of 2^32 threads or more would wrap.  More rows take further launches;
+// these start at multiples of 16 bytes where the first one does.
+constexpr int64_t kPartRows = 1 << 24;
+template <class F>
+void by_parts(int64_t T, F&& f) {  // f(first row, rows)
+  for (int64_t t = 0; t < T; t += kPartRows) f(t, T - t < kPartRows ? T - t : kPartRows);
+}
+
 void enqueue_plan(const int32_t* idx, int64_t T, int32_t k, int32_t E, int32_t* offsets,
                   int32_t* pos, void* ws, hipStream_t st) {
   const int64_t n = T * k;
@@ -159,8 +168,14 @@ int fp8_route_fwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t d
             return;
           }
         }
-        hipLaunchKernelGGL((route_kernel<IN, L, V>), dim3((unsigned)((T + per - 1) / per)),
-                           dim3(kRThreads), 0, stream, a);
+        by_parts(T, [&](int64_t t0, int64_t rows) {
+          a.z = reinterpret_cast<const uint8_t*>(logits) + t0 * E * size;
+          a.idx = idx + t0 * k;
+          a.w = weights + t0 * k;
+          a.T = (int32_t)rows;
+          hipLaunchKernelGGL((route_kernel<IN, L, V>), dim3((unsigned)((rows + per - 1) / per)),
+                             dim3(kRThreads), 0, stream, a);
+        });
       });
     });
   if (offsets && !placed) enqueue_plan(idx, T, k, E, offsets, pos, ws, stream);
@@ -177,22 +192,25 @@ int fp8_route_bwd(int64_t T, int32_t E, int32_t k, const void* logits, int32_t d
   if (T > 0 && (!logits || !idx || !dweights || !dlogits)) return FP8_ERR_NULL;
   if (T == 0) return FP8_OK;
   RouteBwdArgs a = {};
-  a.r.z = logits;
-  a.r.idx = const_cast<int32_t*>(idx);
-  a.r.T = (int32_t)T;
   a.r.E = E;
   a.r.k = k;
   a.r.score = score == FP8_ROUTE_SIGMOID;
   a.r.renorm = renorm != 0;
   a.r.scale = scale;
-  a.dw = dweights;
-  a.dz = dlogits;
   by_type(dtype, [&](auto in) {
     by_row(E, k, [&](auto l, auto v) {
       constexpr int IN = decltype(in)::value, L = decltype(l)::value, V = decltype(v)::value;
       constexpr int per = kRThreads / L;
-      hipLaunchKernelGGL((route_bwd_kernel<IN, L, V>), dim3((unsigned)((T + per - 1) / per)),
-                         dim3(kRThreads), 0, stream, a);
+      by_parts(T, [&](int64_t t0, int64_t rows) {
+        const int64_t at = t0 * E * (dtype == FP8_DT_F32 ? 4 : 2);
+        a.r.z = reinterpret_cast<const uint8_t*>(logits) + at;
+        a.r.idx = const_cast<int32_t*>(idx) + t0 * k;
+        a.r.T = (int32_t)rows;
+        a.dw = dweights + t0 * k;
+        a.dz = reinterpret_cast<uint8_t*>(dlogits) + at;
+        hipLaunchKernelGGL((route_bwd_kernel<IN, L, V>), dim3((unsigned)((rows + per - 1) / per)),
+                           dim3(kRThreads), 0, stream, a);
+      });
     });
   });
   return hip_status();
