@@ -276,9 +276,9 @@ struct MxPieces {
       : rb(mx_rsrc(g.b, cols * g.ld)),
         // words of rows past the end are those of other rows, or zeros past the
         // last step: they meet zero codes or columns that are not stored
-        rsb(mx_rsrc(g.sb, mx_scale_span(g.steps, g.sb_step, cols))),
+        rsb(mx_rsrc(g.sb, mx_scale_span(g.steps, (int32_t)g.sb_step, (int32_t)cols))),
         ra(mx_rsrc(g.a, NX ? g.M * g.ld : 0)),
-        rsa(mx_rsrc(g.sa, NX ? mx_scale_span(g.steps, g.sa_step, g.M) : 0)),
+        rsa(mx_rsrc(g.sa, NX ? mx_scale_span(g.steps, (int32_t)g.sa_step, (int32_t)g.M) : 0)),
         ld((uint32_t)g.ld), sb_step((uint32_t)g.sb_step), sa_step((uint32_t)g.sa_step),
         steps((uint32_t)g.steps), j0(j0), mine(mine) {}
 

@@ -14,7 +14,7 @@ SOURCE = r"""
 #include "fp8l_mx4_span.hpp"
 extern "C" {
 uint32_t nowhere() { return fp8l::kMxNowhere; }
-int64_t scale_span(int64_t steps, int64_t step, int64_t rows) {
+uint32_t scale_span(int32_t steps, int32_t step, int32_t rows) {
   return fp8l::mx_scale_span(steps, step, rows);
 }
 int64_t piece_byte(int64_t s, int sl, int64_t K) { return fp8l::mx_piece(s, sl, K).byte; }
@@ -36,8 +36,8 @@ def span(tmp_path_factory):
                    check=True)
     L = ctypes.CDLL(so)
     L.nowhere.restype = ctypes.c_uint32
-    L.scale_span.restype = ctypes.c_int64
-    L.scale_span.argtypes = [ctypes.c_int64] * 3
+    L.scale_span.restype = ctypes.c_uint32
+    L.scale_span.argtypes = [ctypes.c_int32] * 3
     for f in (L.piece_byte, L.piece_step):
         f.restype = ctypes.c_int64
         f.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]
@@ -51,7 +51,8 @@ def test_scale_descriptors_end_with_the_scales(span, unit, K):
     descriptor reaches to the end of the scales at most, covers every word of
     its rows, and ends before the offset that stands for no word."""
     steps = -(-K // 128)
-    for rows in (1, 3, unit - 1, unit, unit + 1, 2 * unit, 300, 1003, 4096):
+    for rows in (1, 3, unit - 1, unit, unit + 1, 2 * unit, 300, 1003, 4096, (1 << 29) - 1,
+                 (1 << 31) - 1):
         if steps * rows >= 1 << 29:
             continue
         for first in {0, (rows - 1) // unit * unit, min(rows - 1, unit) // unit * unit}:
