@@ -652,9 +652,11 @@ int fp8_route_combine(int64_t T, int32_t k, int64_t D, int64_t R, const void* y,
 /*
  * Gradients of fp8_route_combine: dy[pos[t, i]] = weights[t, i] dout[t] (rows
  * that no slot names are left as they were) and dweights[t, i] =
- * dout[t] . y[pos[t, i]] in 32 bits (0 without a place).  dy or dweights may be
- * NULL (not computed; y is needed for dweights only).  A place named by two
- * slots makes that row of dy unspecified.
+ * dout[t] . y[pos[t, i]] in 32 bits (0 without a place): 64 sums of D / 64
+ * products each, then theirs, so off by at most (D / 64 + 16) 2^-24 of the sum
+ * of the products' magnitudes.  dy or dweights may be NULL (not computed; y is
+ * needed for dweights only).  A place named by two slots makes that row of dy
+ * unspecified.
  */
 int fp8_route_combine_bwd(int64_t T, int32_t k, int64_t D, int64_t R, const void* dout,
                           const void* y, int32_t dtype, const int32_t* pos, const float* weights,
