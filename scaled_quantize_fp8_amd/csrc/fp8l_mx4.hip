@@ -158,7 +158,11 @@ void launch_skinny(MxArgs& g, const Groups* gr, const MxStrides& s, hipStream_t 
 // 2 to 3 us (bf16, us fused / in two launches: one row of 4096 -> 11008 6.6 /
 // 10.1, of 11008 -> 4096 8.0 / 10.0; four rows of 1536 -> 6912 4.5 / 7.1, of 4096
 // -> 11008 8.4 / 10.0, of 6912 -> 1536 7.5 / 8.0; eight of 4096 -> 11008 10.9 /
-// 10.1).  Groups: two rows per expert on average (any unit may have 16, whose
+// 10.1).  The blocks do it side by side, so the bound is on a block's own work,
+// rows K, whatever N is: one row of 4096 -> 128 3.9 / 7.0, of 4096 -> 32000 12.5 /
+// 15.7, four of 1536 -> 100000 15.5 / 18.9; at the bound, seven of 4096 -> 512 7.0 /
+// 7.3, of 4096 -> 32000 15.9 / 16.1, one of 28672 -> 4096 15.5 / 15.3.
+// Groups: two rows per expert on average (any unit may have 16, whose
 // codes must leave room for two blocks per CU; 24 rows, 64 experts of 1536 ->
 // 6912 19.3 / 22.6; 16 rows, 16 of 4096 -> 11008 52.2 / 55.1).  groups 0: dense.
 bool fuse_x(const void* x, int32_t dt, int64_t rows, int64_t groups, int64_t N, int64_t K) {

@@ -374,7 +374,12 @@ FP8L_DEV float slot_weight(const RouteArgs& a, const float (&z)[V], float m, boo
 //   groups   scored in 32 bits, in lanes or, where groups end inside a lane, from
 //            LDS; right if the least kept and the best dropped group are further
 //            apart than the scores' errors.
-//   else     the wave does the row again in 64 bits, with all of its lanes.
+//   else     the wave does the row again in 64 bits, with all of its lanes.  So
+//            it is wherever the k-th and the (k + 1)-th c are equal, but for
+//            16-bit logits without a bias: no proof settles a tie there.  Few
+//            rows of fp32 logits, but 9% of bf16 ones of 256 experts under a bias
+//            of zeros, k 8 (16384 rows 29 us, under a bias of 24 bits 15.5;
+//            4096 27 and 6.1; 131072 118 and 67).
 //
 // One row per 16 lanes, V experts per lane.
 
