@@ -82,7 +82,8 @@ FP8L_DEV MxEight mx_eight(const float v[8], bool inside, int sl) {
 
 // A block of 256 threads walks its tile of rows along K, kU steps at a time
 // with their loads in flight together (11008 x 4096 bf16, 114 MB in and out:
-// 22 us; one step at a time 34).
+// 22 us with X in the last-level cache, where one step at a time takes 34; 26
+// from memory).
 // VEC: K a multiple of 8.
 template <int IN, bool VEC>
 __global__ __launch_bounds__(kMxThreads) void mx4_quantize_kernel(MxQuantArgs a) {
